@@ -19,6 +19,10 @@
  *   key, value      [num_tokens, num_kv_heads, head_dim]  (tokens to append)
  *   k/v cache pool  [num_blocks, num_kv_heads, block_size, head_dim]
  *   k/v scale pool  [num_blocks, num_kv_heads, block_size] float32 (INT8 pools)
+ *   4-bit pools     codes uint8 [num_blocks, num_kv_heads, block_size, head_dim/2],
+ *                   element 2i in the low half of byte i, 2i+1 in the high half;
+ *                   (scale, zero) pairs [num_blocks, num_kv_heads, block_size,
+ *                   head_dim/64, 2] fp16 or bf16, one per 64 elements of a row
  *   block_tables    [batch, max_blocks_per_seq] int32 physical block ids
  *   context_lens    [batch] int32, tokens already in the cache per request
  *   slot_mapping    [num_tokens] int32, slot = block * block_size + offset;
@@ -190,7 +194,7 @@ kvp_status kvp_copy_blocks(void* k_cache, void* v_cache, float* k_scale, float* 
  * merged by a reduce pass (flash-decoding); a return value >= max_blocks_per_seq
  * means single-pass (no workspace needed).  Returns 0 on invalid sizes.
  * kv_8bit: 0 for the fp16/bf16 decodes, 1 for the INT8 decode, 2 for the FP8
- * decode (the decodes run differently shaped CTAs).
+ * decode, 4 for the 4-bit decode (the decodes run differently shaped CTAs).
  */
 int32_t kvp_decode_partition_blocks(int32_t batch, int32_t num_q_heads, kvp_cache_desc cache,
                                     int32_t max_blocks_per_seq, int32_t kv_8bit);
@@ -202,7 +206,7 @@ int32_t kvp_decode_partition_blocks(int32_t batch, int32_t num_q_heads, kvp_cach
  * partition), the partition's running max, sum and unnormalised output in
  * float32; it needs no initialisation and is fully rewritten by each call.
  * kv_8bit: 0 for the fp16/bf16 decodes, 1 for the INT8 decode, 2 for the FP8
- * decode; other values answer 0.
+ * decode, 4 for the 4-bit decode; other values answer 0.
  */
 size_t kvp_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, kvp_cache_desc cache,
                                   int32_t max_blocks_per_seq, int32_t partition_blocks,
@@ -290,6 +294,173 @@ kvp_status kvp_attention_decode_fp8(void* out, const void* q, kvp_dtype q_dtype,
                                     int32_t partition_blocks, void* workspace,
                                     size_t workspace_bytes, int32_t phases, int32_t* dev_status,
                                     kvp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit cache.  A row's value is code * scale + zero with one (scale, zero) pair
+ * per group of 64 elements; the pairs have the type of key, value and q
+ * (`dtype`).  Bytes per token and kv head at head_dim 128: 144 (INT8 264, fp16
+ * 512).  All pools 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * kvp_append_int4 -- quantise new tokens to 4 bits, then scatter.  For each
+ * token, head and group of 64 elements x (float32 arithmetic, IEEE division):
+ *   zero = min x;  scale = (max x - min x) / 15 rounded to `dtype`;
+ *   code = scale > 0 ? min(15, rint((x - zero) / scale)) : 0
+ * (round half to even).  Results are bit-exact with that definition for finite
+ * rows whose range max x - min x is finite.  key, value: [num_tokens, Hkv, D]
+ * of `dtype`, 16-byte aligned.  Slots and errors as kvp_append.
+ */
+kvp_status kvp_append_int4(const void* key, const void* value, kvp_dtype dtype, uint8_t* k_cache,
+                           uint8_t* v_cache, void* k_scale_zero, void* v_scale_zero,
+                           const int32_t* slot_mapping, int32_t num_tokens, kvp_cache_desc cache,
+                           int32_t* dev_status, kvp_stream_t stream);
+
+/*
+ * kvp_read_int4 -- the rows of given slots as `dtype` values (read_page and
+ * dequantize of "KV Cache 优化与显存管理", 三, for 4-bit codes):
+ *   key[t, h, :] = code * scale + zero of slot_mapping[t] (V likewise),
+ * rounded once to float32 and once to `dtype`.  key, value: [num_tokens, Hkv, D],
+ * 16-byte aligned; rows of a negative slot are left as they are.  A slot may be
+ * named several times.  E.g. to lay a 4-bit prefix out as 16-bit blocks for
+ * kvp_attention_prefill.  Device errors: KVP_ERR_BAD_BLOCK for slot >= NB * bs
+ * (that token's rows are written as zeros).
+ */
+kvp_status kvp_read_int4(void* key, void* value, kvp_dtype dtype, const uint8_t* k_cache,
+                         const uint8_t* v_cache, const void* k_scale_zero,
+                         const void* v_scale_zero, const int32_t* slot_mapping,
+                         int32_t num_tokens, kvp_cache_desc cache, int32_t* dev_status,
+                         kvp_stream_t stream);
+
+/* kvp_copy_blocks_int4 -- kvp_copy_blocks for 4-bit pools (codes and pairs). */
+kvp_status kvp_copy_blocks_int4(uint8_t* k_cache, uint8_t* v_cache, void* k_scale_zero,
+                                void* v_scale_zero, const int32_t* pairs, int32_t num_pairs,
+                                kvp_cache_desc cache, int32_t* dev_status, kvp_stream_t stream);
+
+/*
+ * kvp_attention_decode_int4 -- as kvp_attention_decode over 4-bit pools:
+ * K_i = code * scale + zero (V likewise), products with the codes in fp16 with
+ * float32 accumulation; q, out and the pairs are of `dtype`.  Workspace from
+ * kvp_decode_workspace_bytes with kv_8bit = 4.  KVP_DECODE_MERGE_RUNS is
+ * accepted and changes nothing (blocks are fetched one by one).  Arguments
+ * otherwise as kvp_attention_decode.
+ */
+kvp_status kvp_attention_decode_int4(void* out, const void* q, kvp_dtype dtype,
+                                     const uint8_t* k_cache, const uint8_t* v_cache,
+                                     const void* k_scale_zero, const void* v_scale_zero,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* context_lens, int32_t batch,
+                                     int32_t num_q_heads, float scale, kvp_cache_desc cache,
+                                     int32_t partition_blocks, void* workspace,
+                                     size_t workspace_bytes, int32_t phases, int32_t* dev_status,
+                                     kvp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions on one to four axes, fused with the append.
+ * ---------------------------------------------------------------------- */
+
+/* Which pairs of a row are rotated, and by which axis' position. */
+typedef struct {
+  int32_t rotary_dim;  /* R <= head_dim, a multiple of 16; the rest is not rotated  */
+  int32_t num_axes;    /* 1 to 4 (e.g. 3: time, height, width)                      */
+  int32_t sections[4]; /* pairs per axis, in order: axis 0 turns the first
+                          sections[0] pairs, and so on; their sum is R / 2          */
+  int32_t interleaved; /* 0: pair i is elements (i, i + R/2); else (2i, 2i + 1)     */
+} kvp_rope_desc;
+
+/*
+ * kvp_rope_append -- rotate q and k by their tokens' positions, write q to q_out
+ * and scatter K (rotated) and V into their slots of fp16/bf16 pools.  For token
+ * t, pair i on axis a, (c, s) = (cos_sin[p, i], cos_sin[p, R/2 + i]) with
+ * p = positions[a, t], and x, y the pair's elements (every product and sum
+ * rounded to float32, the results once to `dtype`):
+ *   x' = x c - y s,   y' = y c + x s.
+ * q, q_out: num_q_heads heads of D elements per token, q_stride / q_out_stride
+ * elements from one token to the next; q_out may be q (same stride).  With
+ * num_q_heads = 0 both may be NULL.  key, value: Hkv heads per token, k_stride /
+ * v_stride apart -- so q, key and value may be slices of one projection's output.
+ * All rows and pools 16-byte aligned, strides multiples of 8 elements.
+ * cos_sin: float32 [max_position, R], 16-byte aligned; positions: int32
+ * [num_axes, num_tokens].  A token with a negative slot is padding: nothing of it
+ * is written, its q_out rows included.  Slots must be distinct (as kvp_append).
+ * Device errors: KVP_ERR_BAD_BLOCK for a slot past the pool or a position outside
+ * [0, max_position) (that token's q_out rows are written as zeros, its K/V not).
+ */
+kvp_status kvp_rope_append(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                           const void* key, int64_t k_stride, const void* value,
+                           int64_t v_stride, void* k_cache, void* v_cache, const float* cos_sin,
+                           int32_t max_position, const int32_t* positions,
+                           const int32_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                           kvp_rope_desc rope, kvp_cache_desc cache, kvp_dtype dtype,
+                           int32_t* dev_status, kvp_stream_t stream);
+
+/*
+ * kvp_rope_append_int4 -- as kvp_rope_append into 4-bit pools: the rotated K,
+ * rounded to `dtype`, and V are quantised as kvp_append_int4 does.
+ */
+kvp_status kvp_rope_append_int4(void* q_out, int64_t q_out_stride, const void* q,
+                                int64_t q_stride, const void* key, int64_t k_stride,
+                                const void* value, int64_t v_stride, uint8_t* k_cache,
+                                uint8_t* v_cache, void* k_scale_zero, void* v_scale_zero,
+                                const float* cos_sin, int32_t max_position,
+                                const int32_t* positions, const int32_t* slot_mapping,
+                                int32_t num_tokens, int32_t num_q_heads, kvp_rope_desc rope,
+                                kvp_cache_desc cache, kvp_dtype dtype, int32_t* dev_status,
+                                kvp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Block tables and slot maps on the GPU, for loops that plan their own steps
+ * (e.g. captured in a graph).  The free blocks are a stack in device memory:
+ * free_blocks[0 .. *free_count) of num_blocks entries, the last one on top.
+ * Every block belongs to one request (no shared prefixes, no reference counts:
+ * those stay with the host block manager).  At most 16384 requests
+ * (KVP_ERR_UNSUPPORTED above).  Blocks hold 16 tokens.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * kvp_extend_tables -- grow every request by its step's new tokens.  Request b
+ * holds n = context_lens[b] tokens and gets new_lens[b] >= 0 more; it takes
+ * ceil((n + new) / 16) - ceil(n / 16) blocks off the stack (in request order, top
+ * first), which are written behind its present table entries.  Written:
+ *   block_tables      the new entries only
+ *   context_lens_out  n + new (may be context_lens itself)
+ *   free_count_out    the stack's new height (may be free_count itself)
+ *   query_start       [batch + 1]: first new token of each request, and their
+ *                     number -- as kvp_attention_prefill takes it
+ *   slot_mapping      [num_tokens]: slots of the new tokens in request order, -1
+ *                     behind the last one (padding, as the appends take it)
+ *   positions         [num_tokens] or NULL: the new tokens' positions, 0 behind
+ * All or nothing.  Device errors: KVP_ERR_OOM when the stack holds too few
+ * blocks; KVP_ERR_BAD_BLOCK for a negative length, n + new past the table, more
+ * than num_tokens new tokens, a stack height outside [0, num_blocks], or a block
+ * id outside [0, num_blocks) among those used.  Then lengths, tables and stack
+ * keep their values, query_start is all 0 and every slot -1 (an empty step).
+ * context_lens_out (unless it is context_lens itself) and the other outputs must
+ * not overlap any input or each other.
+ */
+kvp_status kvp_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
+                             const int32_t* context_lens, const int32_t* new_lens, int32_t batch,
+                             const int32_t* free_blocks, const int32_t* free_count,
+                             int32_t num_blocks, int32_t* context_lens_out,
+                             int32_t* free_count_out, int32_t* slot_mapping, int32_t num_tokens,
+                             int32_t* query_start, int32_t* positions, int32_t* dev_status,
+                             kvp_stream_t stream);
+
+/*
+ * kvp_release_tables -- push the blocks of every request with finished[b] != 0
+ * on the free stack (request order, then table order) and set its length to 0.
+ * Table entries are not changed.  context_lens_out may be context_lens,
+ * free_count_out may be free_count.  All or nothing.  Device errors:
+ * KVP_ERR_BAD_BLOCK for a length outside the table, a stack height outside
+ * [0, num_blocks] or a block id outside [0, num_blocks); KVP_ERR_REFCOUNT when
+ * the stack would hold more than num_blocks blocks.  Then nothing changes
+ * (context_lens_out and free_count_out get the present values).
+ */
+kvp_status kvp_release_tables(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                              const int32_t* context_lens, const int32_t* finished,
+                              int32_t batch, int32_t* free_blocks, const int32_t* free_count,
+                              int32_t num_blocks, int32_t* context_lens_out,
+                              int32_t* free_count_out, int32_t* dev_status, kvp_stream_t stream);
 
 /*
  * kvp_attention_prefill -- causal multi-query paged attention over fp16/bf16

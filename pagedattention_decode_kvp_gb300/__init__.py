@@ -45,6 +45,11 @@ class kvp_cache_desc(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class kvp_rope_desc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32)]
+
+
 class kvp_bm_stats_t(ctypes.Structure):
     _fields_ = [("total_blocks", ctypes.c_int32), ("used_blocks", ctypes.c_int32),
                 ("free_blocks", ctypes.c_int32), ("active_requests", ctypes.c_int32),
@@ -62,6 +67,7 @@ class KvpError(RuntimeError):
 _P, _I32, _I64, _SZ, _F = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                             ctypes.c_float)
 _D = kvp_cache_desc
+_R = kvp_rope_desc
 SIGNATURES = {
     "kvp_status_string": (ctypes.c_char_p, [_I32]),
     "kvp_version": (_I32, []),
@@ -88,6 +94,18 @@ SIGNATURES = {
     "kvp_decode_shared_prefix_workspace_bytes": (_SZ, [_I32, _I32, _D, _I32, _I32, _I32]),
     "kvp_attention_decode_shared_prefix": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _F,
                                                   _D, _I32, _I32, _I32, _P, _SZ, _P, _P]),
+    "kvp_append_int4": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _P, _I32, _D, _P, _P]),
+    "kvp_read_int4": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _P, _I32, _D, _P, _P]),
+    "kvp_copy_blocks_int4": (_I32, [_P, _P, _P, _P, _P, _I32, _D, _P, _P]),
+    "kvp_attention_decode_int4": (_I32, [_P, _P, _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32,
+                                         _F, _D, _I32, _P, _SZ, _I32, _P, _P]),
+    "kvp_rope_append": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I32, _P, _P,
+                               _I32, _I32, _R, _D, _I32, _P, _P]),
+    "kvp_rope_append_int4": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                    _I32, _P, _P, _I32, _I32, _R, _D, _I32, _P, _P]),
+    "kvp_extend_tables": (_I32, [_P, _I32, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _I32, _P, _P,
+                                 _P, _P]),
+    "kvp_release_tables": (_I32, [_P, _I32, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _P]),
     "kvp_read_status": (_I32, [_P, _P]),
     "kvp_selftest_wait_timeout": (_I32, [_P, _I64, _P]),
     "kvp_bm_create": (_P, [_I32, _I32, _I64]),
@@ -249,23 +267,25 @@ def kvp_copy_blocks(k_cache, v_cache, pairs, *, k_scale=None, v_scale=None, stat
                                _ptr(status), _stream_ptr(stream)), "kvp_copy_blocks")
 
 
-def _kv_8bit(kv_int8, kv_fp8):
-    return 2 if kv_fp8 else (1 if kv_int8 else 0)
+def _kv_8bit(kv_int8, kv_fp8, kv_int4):
+    return 4 if kv_int4 else (2 if kv_fp8 else (1 if kv_int8 else 0))
 
 
 def kvp_decode_partition_blocks(batch, num_q_heads, desc: kvp_cache_desc, max_blocks,
-                                kv_int8=False, kv_fp8=False) -> int:
-    """kv_int8 / kv_fp8: the pools hold INT8 / FP8 codes (their decodes are
-    shaped differently)."""
+                                kv_int8=False, kv_fp8=False, kv_int4=False) -> int:
+    """kv_int8 / kv_fp8 / kv_int4: the pools hold INT8 / FP8 / 4-bit codes (their
+    decodes are shaped differently)."""
     return load_library().kvp_decode_partition_blocks(int(batch), int(num_q_heads), desc,
-                                                      int(max_blocks), _kv_8bit(kv_int8, kv_fp8))
+                                                      int(max_blocks),
+                                                      _kv_8bit(kv_int8, kv_fp8, kv_int4))
 
 
 def kvp_decode_workspace_bytes(batch, num_q_heads, desc: kvp_cache_desc, max_blocks,
-                               partition_blocks=0, kv_int8=False, kv_fp8=False) -> int:
+                               partition_blocks=0, kv_int8=False, kv_fp8=False,
+                               kv_int4=False) -> int:
     return int(load_library().kvp_decode_workspace_bytes(int(batch), int(num_q_heads), desc,
                                                          int(max_blocks), int(partition_blocks),
-                                                         _kv_8bit(kv_int8, kv_fp8)))
+                                                         _kv_8bit(kv_int8, kv_fp8, kv_int4)))
 
 
 def kvp_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, *,
@@ -406,6 +426,289 @@ def kvp_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, 
         int(block_tables.shape[1]), _ptr(context_lens), _ptr(query_start), T, B, Hq,
         int(max_query_len), int(shared_prefix_blocks), float(scale), cache_desc(k_cache),
         _dtype_code(q), _ptr(status), _stream_ptr(stream)), "kvp_attention_prefill")
+
+
+# ------------------------------------------------------------------ 4-bit cache
+def _on_one_device(stream, *ts) -> int:
+    """CUDA tensors of one device, which is the current one (kernels launch
+    there); returns the stream to use."""
+    torch = _torch()
+    dev = -1
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
+        d = t.get_device()
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{d} in one call")
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if dev >= 0 and stream.device_index != dev:
+        raise ValueError(f"tensors on cuda:{dev}, but the stream is of cuda:{stream.device_index}")
+    return stream.cuda_stream
+
+
+def _need(t, name, dtype, *shape):
+    """A contiguous tensor of the given type and shape (None: any extent)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the GPU entry points must be contiguous")
+
+
+def cache_desc_int4(k_cache) -> kvp_cache_desc:
+    """kvp_cache_desc of a 4-bit pool's codes [NB, Hkv, block_size, D / 2] (uint8)."""
+    if k_cache.dim() != 4:
+        raise ValueError("4-bit pools are [num_blocks, num_kv_heads, block_size, head_dim / 2]")
+    nb, hkv, bs, half = k_cache.shape
+    return kvp_cache_desc(nb, hkv, bs, 2 * half)
+
+
+def _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype=None) -> kvp_cache_desc:
+    torch = _torch()
+    d = cache_desc_int4(k_cache)
+    codes = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim // 2)
+    _need(k_cache, "k_cache", torch.uint8, *codes)
+    _need(v_cache, "v_cache", torch.uint8, *codes)
+    if d.head_dim in (64, 128):  # the library refuses others
+        pairs = codes[:3] + (d.head_dim // 64, 2)
+        dtype = k_scale_zero.dtype if dtype is None else dtype
+        _need(k_scale_zero, "k_scale_zero", dtype, *pairs)
+        _need(v_scale_zero, "v_scale_zero", dtype, *pairs)
+    return d
+
+
+def kvp_append_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot_mapping, *,
+                    status=None, stream=None) -> None:
+    """Quantise key/value [T, Hkv, D] (fp16/bf16) to 4 bits with one (scale, zero)
+    pair per 64 elements and scatter them: codes into uint8 pools
+    [NB, Hkv, bs, D/2], pairs into [NB, Hkv, bs, D/64, 2] of key's dtype."""
+    lib = load_library()
+    s = _on_one_device(stream, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
+                       slot_mapping, status)
+    code = _dtype_code(key)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
+    _need(slot_mapping, "slot_mapping", _torch().int32, None)
+    T = slot_mapping.shape[0]
+    _need(key, "key", key.dtype, T, d.num_kv_heads, d.head_dim)
+    _need(value, "value", key.dtype, T, d.num_kv_heads, d.head_dim)
+    _check(lib.kvp_append_int4(key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(),
+                               v_cache.data_ptr(), k_scale_zero.data_ptr(),
+                               v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
+                               _ptr(status), s), "kvp_append_int4")
+
+
+def kvp_read_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot_mapping, *,
+                  status=None, stream=None) -> None:
+    """key/value [T, Hkv, D] = the values held in 4 bits at slot_mapping [T]
+    (rows of negative slots are left as they are)."""
+    lib = load_library()
+    s = _on_one_device(stream, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
+                       slot_mapping, status)
+    code = _dtype_code(key)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
+    _need(slot_mapping, "slot_mapping", _torch().int32, None)
+    T = slot_mapping.shape[0]
+    _need(key, "key", key.dtype, T, d.num_kv_heads, d.head_dim)
+    _need(value, "value", key.dtype, T, d.num_kv_heads, d.head_dim)
+    _check(lib.kvp_read_int4(key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(),
+                             v_cache.data_ptr(), k_scale_zero.data_ptr(),
+                             v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
+                             _ptr(status), s), "kvp_read_int4")
+
+
+def kvp_copy_blocks_int4(k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, *, status=None,
+                         stream=None) -> None:
+    """Copy block pairs[i, 0] onto pairs[i, 1] in 4-bit pools (codes and pairs)."""
+    lib = load_library()
+    s = _on_one_device(stream, k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, status)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero)
+    _need(pairs, "pairs", _torch().int32, None, 2)
+    _check(lib.kvp_copy_blocks_int4(k_cache.data_ptr(), v_cache.data_ptr(),
+                                    k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
+                                    pairs.data_ptr(), pairs.shape[0], d, _ptr(status), s),
+           "kvp_copy_blocks_int4")
+
+
+def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_zero, block_tables,
+                              context_lens, scale, *, workspace=None, partition_blocks=0,
+                              phases=KVP_PHASE_ALL, status=None, stream=None) -> None:
+    """As kvp_attention_decode over 4-bit pools (see kvp_append_int4); q, out and
+    the (scale, zero) pairs share one dtype.  Workspace:
+    kvp_decode_workspace_bytes(..., kv_int4=True)."""
+    lib = load_library()
+    s = _on_one_device(stream, out, q, k_cache, v_cache, k_scale_zero, v_scale_zero, block_tables,
+                       context_lens, workspace, status)
+    code = _dtype_code(q)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, q.dtype)
+    _need(q, "q", q.dtype, None, None, d.head_dim)
+    B, Hq = q.shape[0], q.shape[1]
+    _need(out, "out", q.dtype, B, Hq, d.head_dim)
+    i32 = _torch().int32
+    _need(block_tables, "block_tables", i32, B, None)
+    _need(context_lens, "context_lens", i32, B)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("tensors passed to the GPU entry points must be contiguous")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.kvp_attention_decode_int4(
+        out.data_ptr(), q.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale), d,
+        int(partition_blocks), ws, ws_bytes, int(phases), _ptr(status), s),
+        "kvp_attention_decode_int4")
+
+
+# ------------------------------------------------------------------ rotary append
+def _rows(t, name, dtype, T, heads, dim) -> int:
+    """Element stride between the tokens of t [T, heads, dim], whose rows are
+    contiguous and lie behind one another (a slice of a projection's output)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must have shape {(T, heads, dim)}, got {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st if T > 1 else heads * dim
+
+
+def _rope_args(q_out, q, key, value, kv_heads, dim, cos_sin, positions, slot_mapping, sections,
+               interleaved):
+    torch = _torch()
+    _need(slot_mapping, "slot_mapping", torch.int32, None)
+    T = slot_mapping.shape[0]
+    _need(cos_sin, "cos_sin", torch.float32, None, None)
+    P, R = cos_sin.shape
+    if positions.dim() == 1:
+        positions = positions[None]
+    _need(positions, "positions", torch.int32, None, T)
+    A = positions.shape[0]
+    sections = (R // 2,) if sections is None else sections
+    if len(sections) != A or A > 4:
+        raise ValueError(f"positions has {A} axes (1 to 4 are allowed), sections {len(sections)}")
+    rope = kvp_rope_desc(R, A, (ctypes.c_int32 * 4)(*sections), 1 if interleaved else 0)
+    ks = _rows(key, "key", key.dtype, T, kv_heads, dim)
+    vs = _rows(value, "value", key.dtype, T, kv_heads, dim)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is None:
+        return T, 0, rope, P, (None, 0, None, 0, key.data_ptr(), ks, value.data_ptr(), vs)
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    qs = _rows(q, "q", key.dtype, T, Hq, dim)
+    qo = _rows(q_out, "q_out", key.dtype, T, Hq, dim)
+    return T, Hq, rope, P, (q_out.data_ptr(), qo, q.data_ptr(), qs, key.data_ptr(), ks,
+                            value.data_ptr(), vs)
+
+
+def kvp_rope_append(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping, *,
+                    sections=None, interleaved=False, status=None, stream=None) -> None:
+    """Rotate q [T, Hq, D] into q_out and key [T, Hkv, D] into its slots of the
+    fp16/bf16 pools; value is scattered as it is.
+
+    cos_sin: float32 [max_position, R], R/2 cosines then R/2 sines per position
+    (R <= D elements of a row are rotated); positions: int32 [T] or [A, T], one
+    row per axis (time, height, width, ...); sections: pairs per axis, summing
+    to R/2 (default: all on one axis); interleaved: pairs (2i, 2i+1) instead of
+    (i, i + R/2).  q, key and value may be slices of one projection's output
+    (contiguous heads, any token stride that is a multiple of 8); q_out may be
+    q.  Tokens with a negative slot are skipped."""
+    lib = load_library()
+    s = _on_one_device(stream, q_out, q, key, value, k_cache, v_cache, cos_sin, positions,
+                       slot_mapping, status)
+    code = _dtype_code(key)
+    d = cache_desc(k_cache)
+    pool = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
+    _need(k_cache, "k_cache", key.dtype, *pool)
+    _need(v_cache, "v_cache", key.dtype, *pool)
+    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d.num_kv_heads, d.head_dim, cos_sin,
+                                      positions, slot_mapping, sections, interleaved)
+    _check(lib.kvp_rope_append(*rows, k_cache.data_ptr(), v_cache.data_ptr(), cos_sin.data_ptr(),
+                               P, positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, rope, d,
+                               code, _ptr(status), s), "kvp_rope_append")
+
+
+def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
+                         cos_sin, positions, slot_mapping, *, sections=None, interleaved=False,
+                         status=None, stream=None) -> None:
+    """As kvp_rope_append into 4-bit pools (see kvp_append_int4): the rotated key,
+    rounded to its dtype, and value are quantised."""
+    lib = load_library()
+    s = _on_one_device(stream, q_out, q, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
+                       cos_sin, positions, slot_mapping, status)
+    code = _dtype_code(key)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
+    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d.num_kv_heads, d.head_dim, cos_sin,
+                                      positions, slot_mapping, sections, interleaved)
+    _check(lib.kvp_rope_append_int4(*rows, k_cache.data_ptr(), v_cache.data_ptr(),
+                                    k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
+                                    cos_sin.data_ptr(), P, positions.data_ptr(),
+                                    slot_mapping.data_ptr(), T, Hq, rope, d, code, _ptr(status),
+                                    s), "kvp_rope_append_int4")
+
+
+# ------------------------------------------------------------------ device-side tables
+def kvp_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_count,
+                      context_lens_out, free_count_out, slot_mapping, query_start,
+                      positions=None, *, status=None, stream=None) -> None:
+    """Grow request b by new_lens[b] tokens: blocks come off the free stack
+    (free_blocks[:free_count], last on top) into block_tables [B, MB];
+    context_lens_out [B], free_count_out [1], query_start [B+1], slot_mapping [T]
+    (-1 behind the new tokens) and positions [T] are written.  All int32.
+    context_lens_out / free_count_out may be context_lens / free_count.  All or
+    nothing: see kvp.h for the device errors."""
+    lib = load_library()
+    s = _on_one_device(stream, block_tables, context_lens, new_lens, free_blocks, free_count,
+                       context_lens_out, free_count_out, slot_mapping, query_start, positions,
+                       status)
+    i32 = _torch().int32
+    _need(block_tables, "block_tables", i32, None, None)
+    B, MB = block_tables.shape
+    for t, name, n in ((context_lens, "context_lens", B), (new_lens, "new_lens", B),
+                       (context_lens_out, "context_lens_out", B), (free_count, "free_count", 1),
+                       (free_count_out, "free_count_out", 1), (free_blocks, "free_blocks", None),
+                       (query_start, "query_start", B + 1),
+                       (slot_mapping, "slot_mapping", None)):
+        _need(t, name, i32, n)
+    T = slot_mapping.shape[0]
+    if positions is not None:
+        _need(positions, "positions", i32, T)
+    _check(lib.kvp_extend_tables(block_tables.data_ptr(), MB, context_lens.data_ptr(),
+                                 new_lens.data_ptr(), B, free_blocks.data_ptr(),
+                                 free_count.data_ptr(), free_blocks.shape[0],
+                                 context_lens_out.data_ptr(), free_count_out.data_ptr(),
+                                 slot_mapping.data_ptr(), T, query_start.data_ptr(),
+                                 _ptr(positions), _ptr(status), s), "kvp_extend_tables")
+
+
+def kvp_release_tables(block_tables, context_lens, finished, free_blocks, free_count,
+                       context_lens_out, free_count_out, *, status=None, stream=None) -> None:
+    """Push the blocks of every request with finished[b] != 0 on the free stack
+    and set its length to 0 (all int32; outputs as kvp_extend_tables)."""
+    lib = load_library()
+    s = _on_one_device(stream, block_tables, context_lens, finished, free_blocks, free_count,
+                       context_lens_out, free_count_out, status)
+    i32 = _torch().int32
+    _need(block_tables, "block_tables", i32, None, None)
+    B, MB = block_tables.shape
+    for t, name, n in ((context_lens, "context_lens", B), (finished, "finished", B),
+                       (context_lens_out, "context_lens_out", B), (free_count, "free_count", 1),
+                       (free_count_out, "free_count_out", 1), (free_blocks, "free_blocks", None)):
+        _need(t, name, i32, n)
+    _check(lib.kvp_release_tables(block_tables.data_ptr(), MB, context_lens.data_ptr(),
+                                  finished.data_ptr(), B, free_blocks.data_ptr(),
+                                  free_count.data_ptr(), free_blocks.shape[0],
+                                  context_lens_out.data_ptr(), free_count_out.data_ptr(),
+                                  _ptr(status), s), "kvp_release_tables")
 
 
 def kvp_selftest_wait_timeout(status, limit_ns, stream=None):

@@ -27,7 +27,10 @@ SOURCES = [
     "kvp_decode_int8.cu",
     "kvp_decode_fp8.cu",
     "kvp_decode_fp8_umma.cu",
+    "kvp_decode_int4.cu",
     "kvp_reduce.cu",
+    "kvp_rope_append.cu",
+    "kvp_tables.cu",
     "kvp_prefill.cu",
     "kvp_block_manager.cpp",
     "kvp_noalloc.cu",

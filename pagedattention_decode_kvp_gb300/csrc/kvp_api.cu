@@ -148,6 +148,7 @@ constexpr double kReduceCostBlocks = 2.0;
 int resident_ctas(DecodePath path) {
   switch (path) {
     case DecodePath::kMmaInt8: return 4;
+    case DecodePath::kInt4: return 4;
     case DecodePath::kUmmaFp8: return 2;
     default: return 3;
   }
@@ -174,7 +175,8 @@ int auto_partition(DecodePath path, long long units, int max_blocks) {
   return best_pb;
 }
 
-// kv_8bit: 0 for 16-bit pools, 1 for INT8 codes, 2 for FP8 (E4M3) codes.
+// kv_8bit: 0 for 16-bit pools, 1 for INT8 codes, 2 for FP8 (E4M3) codes, 4 for
+// 4-bit codes.
 kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int max_blocks,
                         int partition_blocks, int kv_8bit, DecodeShape* out) {
   if (batch < 0 || num_q_heads <= 0 || max_blocks <= 0) return KVP_ERR_INVALID_ARG;
@@ -184,7 +186,10 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
   if (partition_blocks < 0 || partition_blocks > kMaxPartBlocks) return KVP_ERR_INVALID_ARG;
   const int G = num_q_heads / c.num_kv_heads;
   DecodeShape s;
-  if (kv_8bit == 2 && c.head_dim == 128) {
+  if (kv_8bit == 4) {
+    s.path = DecodePath::kInt4;
+    s.heads_per_cta = G < kHeadsPerCta ? G : kHeadsPerCta;
+  } else if (kv_8bit == 2 && c.head_dim == 128) {
     s.path = DecodePath::kUmmaFp8;  // FP8 codes straight into the tensor core
     s.heads_per_cta = G < kHeadsPerCta ? G : kHeadsPerCta;
   } else if (kv_8bit) {
@@ -211,13 +216,20 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
   return KVP_OK;
 }
 
+// Values of kv_8bit that the sizing calls know.
+bool sizing_kind(int kv_8bit) { return (kv_8bit >= 0 && kv_8bit <= 2) || kv_8bit == 4; }
+
+// kv_kind: 0 fp16, 1 bf16, 2 INT8, 3 FP8, 5 4-bit pools (one more than the
+// sizing calls' kv_8bit where there are scales).  ks, vs: float32 scales, or
+// the (scale, zero) pairs of 4-bit pools.
 kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, const void* kc,
-                         const void* vc, const float* ks, const float* vs, const int32_t* tables,
+                         const void* vc, const void* ks, const void* vs, const int32_t* tables,
                          int32_t max_blocks, const int32_t* lens, int32_t batch, int32_t hq,
                          float scale, kvp_cache_desc c, int32_t partition_blocks, void* ws,
                          size_t ws_bytes, int32_t phases, int32_t* status, kvp_stream_t stream,
                          const void* new_k = nullptr, const void* new_v = nullptr) {
-  const bool int8 = kv_kind >= 2;  // 8-bit codes with scales: INT8 (2) or FP8 E4M3 (3)
+  const bool int8 = kv_kind >= 2;  // codes with scales: INT8 (2), FP8 E4M3 (3) or 4-bit (5)
+  const bool int4 = kv_kind == 5;
   DecodeShape sh;
   const kvp_status st =
       shape_decode(batch, hq, c, max_blocks, partition_blocks, int8 ? kv_kind - 1 : 0, &sh);
@@ -238,8 +250,10 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
   DecodeParams p{};
   p.out = out;
   p.q = q;
-  p.k_scale = ks;
-  p.v_scale = vs;
+  p.k_scale = int4 ? nullptr : static_cast<const float*>(ks);
+  p.v_scale = int4 ? nullptr : static_cast<const float*>(vs);
+  p.k_sz = int4 ? ks : nullptr;
+  p.v_sz = int4 ? vs : nullptr;
   p.block_tables = tables;
   p.context_lens = lens;
   p.ws_o = static_cast<float*>(ws);
@@ -274,7 +288,9 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
     DecodeMaps maps;
     maps.merged = merge_runs && sh.path != DecodePath::kUmmaFp8;  // (per-block fetch only)
     kvp_status r = KVP_OK;
-    if (maps.merged) {
+    if (int4) {
+      // whole tiles by untiled bulk copies: no maps
+    } else if (maps.merged) {
       const int runs[3] = {1, 2, 4};
       for (int i = 0; i < 3 && r == KVP_OK; ++i) {
         r = make_pool_run_map(&maps.runs.k[i], kc, c, eb, runs[i]);
@@ -295,6 +311,9 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
         break;
       case DecodePath::kUmmaFp8:
         e = launch_decode_fp8_umma(p, maps.k, maps.v, sh.max_parts, s);
+        break;
+      case DecodePath::kInt4:
+        e = launch_decode_int4(p, sh.max_parts, s);
         break;
       default:
         e = kv_kind == 3 ? launch_decode_mma_fp8(p, maps, sh.max_parts, s)
@@ -349,6 +368,90 @@ kvp_status shape_prefix_decode(int batch, int hq, const kvp_cache_desc& c, int m
   }
   *out = s;
   return KVP_OK;
+}
+
+// Argument checks of the 4-bit entry points' pools; pairs are read and written
+// as 4- to 8-byte words, codes as 4-byte words and 16-byte pieces.
+bool int4_pools_ok(const void* kc, const void* vc, const void* ksz, const void* vsz) {
+  return kc && vc && ksz && vsz && aligned(kc, 16) && aligned(vc, 16) && aligned(ksz, 16) &&
+         aligned(vsz, 16);
+}
+
+// A token stride of rows of `heads` heads: whole 16-byte pieces, no overlap.
+bool stride_ok(int64_t stride, int heads, int head_dim) {
+  return stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * head_dim;
+}
+
+kvp_status rope_append_common(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                              const void* key, int64_t k_stride, const void* value,
+                              int64_t v_stride, void* kc, void* vc, void* ksz, void* vsz,
+                              bool int4, const float* cos_sin, int32_t max_position,
+                              const int32_t* positions, const int32_t* slots, int32_t num_tokens,
+                              int32_t num_q_heads, const kvp_rope_desc& rope,
+                              const kvp_cache_desc& c, kvp_dtype dtype, int32_t* status,
+                              kvp_stream_t stream) {
+  const kvp_status ds = check_desc(c);
+  if (ds != KVP_OK) return ds;
+  if (num_tokens < 0 || num_q_heads < 0 || (dtype != KVP_F16 && dtype != KVP_BF16))
+    return KVP_ERR_INVALID_ARG;
+  if (rope.num_axes < 1 || rope.num_axes > 4 || rope.rotary_dim < 0 ||
+      rope.rotary_dim > c.head_dim || max_position <= 0)
+    return KVP_ERR_INVALID_ARG;
+  if (rope.rotary_dim == 0 || rope.rotary_dim % 16 != 0) return KVP_ERR_UNSUPPORTED;
+  long long pairs = 0;
+  bool by4 = true;
+  for (int a = 0; a < rope.num_axes; ++a) {
+    if (rope.sections[a] < 0) return KVP_ERR_INVALID_ARG;
+    pairs += rope.sections[a];
+    by4 = by4 && rope.sections[a] % 4 == 0;
+  }
+  if (pairs != rope.rotary_dim / 2) return KVP_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_q_heads) + c.num_kv_heads > 65535) return KVP_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return KVP_OK;
+  if (!key || !value || !kc || !vc || !cos_sin || !positions || !slots) return KVP_ERR_INVALID_ARG;
+  if (num_q_heads > 0 && (!q || !q_out)) return KVP_ERR_INVALID_ARG;
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(kc, 16) || !aligned(vc, 16) ||
+      !aligned(cos_sin, 16) || !aligned(q, 16) || !aligned(q_out, 16))
+    return KVP_ERR_INVALID_ARG;
+  if (int4 && !int4_pools_ok(kc, vc, ksz, vsz)) return KVP_ERR_INVALID_ARG;
+  if (!stride_ok(k_stride, c.num_kv_heads, c.head_dim) ||
+      !stride_ok(v_stride, c.num_kv_heads, c.head_dim) ||
+      (num_q_heads > 0 && (!stride_ok(q_stride, num_q_heads, c.head_dim) ||
+                           !stride_ok(q_out_stride, num_q_heads, c.head_dim))))
+    return KVP_ERR_INVALID_ARG;
+  RowParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.key = static_cast<const uint16_t*>(key);
+  p.value = static_cast<const uint16_t*>(value);
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_cache = kc;
+  p.v_cache = vc;
+  p.k_sz = static_cast<uint32_t*>(ksz);
+  p.v_sz = static_cast<uint32_t*>(vsz);
+  p.cos_sin = cos_sin;
+  p.positions = positions;
+  p.slots = slots;
+  p.status = status;
+  p.num_tokens = num_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = c.num_kv_heads;
+  p.num_slots = c.num_blocks * kBlockSize;
+  p.max_position = max_position;
+  p.rotary_dim = rope.rotary_dim;
+  p.num_axes = rope.num_axes;
+  int end = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (a < rope.num_axes) end += rope.sections[a];
+    p.axis_end[a] = end;
+  }
+  p.interleaved = rope.interleaved != 0;
+  p.sections_by_4 = by4;
+  return from_cuda(launch_rope_append(p, dtype == KVP_BF16, c.head_dim, int4,
+                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -473,7 +576,7 @@ kvp_status kvp_copy_blocks(void* k_cache, void* v_cache, float* k_scale, float* 
 int32_t kvp_decode_partition_blocks(int32_t batch, int32_t num_q_heads, kvp_cache_desc cache,
                                     int32_t max_blocks_per_seq, int32_t kv_int8) {
   DecodeShape sh;
-  if (kv_int8 < 0 || kv_int8 > 2 ||
+  if (!sizing_kind(kv_int8) ||
       shape_decode(batch, num_q_heads, cache, max_blocks_per_seq, 0, kv_int8, &sh) != KVP_OK)
     return 0;
   return sh.part_blocks;
@@ -483,7 +586,7 @@ size_t kvp_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, kvp_cache_
                                   int32_t max_blocks_per_seq, int32_t partition_blocks,
                                   int32_t kv_int8) {
   DecodeShape sh;
-  if (kv_int8 < 0 || kv_int8 > 2 ||
+  if (!sizing_kind(kv_int8) ||
       shape_decode(batch, num_q_heads, cache, max_blocks_per_seq, partition_blocks, kv_int8,
                    &sh) != KVP_OK)
     return 0;
@@ -556,6 +659,182 @@ kvp_status kvp_attention_decode_fp8(void* out, const void* q, kvp_dtype q_dtype,
                        block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads, scale,
                        cache, partition_blocks, workspace, workspace_bytes, phases, dev_status,
                        stream);
+}
+
+kvp_status kvp_append_int4(const void* key, const void* value, kvp_dtype dtype, uint8_t* k_cache,
+                           uint8_t* v_cache, void* k_scale_zero, void* v_scale_zero,
+                           const int32_t* slot_mapping, int32_t num_tokens, kvp_cache_desc cache,
+                           int32_t* dev_status, kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_append_int4");
+  const kvp_status ds = check_desc(cache);
+  if (ds != KVP_OK) return ds;
+  if (num_tokens < 0 || (dtype != KVP_F16 && dtype != KVP_BF16)) return KVP_ERR_INVALID_ARG;
+  if (num_tokens == 0) return KVP_OK;
+  if (!key || !value || !slot_mapping || !aligned(key, 16) || !aligned(value, 16) ||
+      !int4_pools_ok(k_cache, v_cache, k_scale_zero, v_scale_zero))
+    return KVP_ERR_INVALID_ARG;
+  RowParams p{};
+  p.key = static_cast<const uint16_t*>(key);
+  p.value = static_cast<const uint16_t*>(value);
+  p.k_stride = p.v_stride = static_cast<long long>(cache.num_kv_heads) * cache.head_dim;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_sz = static_cast<uint32_t*>(k_scale_zero);
+  p.v_sz = static_cast<uint32_t*>(v_scale_zero);
+  p.slots = slot_mapping;
+  p.status = dev_status;
+  p.num_tokens = num_tokens;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.num_slots = cache.num_blocks * kBlockSize;
+  return from_cuda(launch_append_int4(p, dtype == KVP_BF16, cache.head_dim,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_read_int4(void* key, void* value, kvp_dtype dtype, const uint8_t* k_cache,
+                         const uint8_t* v_cache, const void* k_scale_zero,
+                         const void* v_scale_zero, const int32_t* slot_mapping,
+                         int32_t num_tokens, kvp_cache_desc cache, int32_t* dev_status,
+                         kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_read_int4");
+  const kvp_status ds = check_desc(cache);
+  if (ds != KVP_OK) return ds;
+  if (num_tokens < 0 || (dtype != KVP_F16 && dtype != KVP_BF16)) return KVP_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_tokens) * cache.num_kv_heads * (cache.head_dim / 16) >
+      256ll * 0x7fffffffll)
+    return KVP_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return KVP_OK;
+  if (!key || !value || !slot_mapping || !aligned(key, 16) || !aligned(value, 16) ||
+      !int4_pools_ok(k_cache, v_cache, k_scale_zero, v_scale_zero))
+    return KVP_ERR_INVALID_ARG;
+  return from_cuda(launch_read_int4(key, value, dtype == KVP_BF16, k_cache, v_cache, k_scale_zero,
+                                    v_scale_zero, slot_mapping, num_tokens, cache, dev_status,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_copy_blocks_int4(uint8_t* k_cache, uint8_t* v_cache, void* k_scale_zero,
+                                void* v_scale_zero, const int32_t* pairs, int32_t num_pairs,
+                                kvp_cache_desc cache, int32_t* dev_status, kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_copy_blocks_int4");
+  const kvp_status ds = check_desc(cache);
+  if (ds != KVP_OK) return ds;
+  if (num_pairs < 0) return KVP_ERR_INVALID_ARG;
+  if (num_pairs == 0) return KVP_OK;
+  if (!pairs || !int4_pools_ok(k_cache, v_cache, k_scale_zero, v_scale_zero))
+    return KVP_ERR_INVALID_ARG;
+  return from_cuda(launch_copy_blocks_int4(k_cache, v_cache, k_scale_zero, v_scale_zero, pairs,
+                                           num_pairs, cache, dev_status,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_attention_decode_int4(void* out, const void* q, kvp_dtype dtype,
+                                     const uint8_t* k_cache, const uint8_t* v_cache,
+                                     const void* k_scale_zero, const void* v_scale_zero,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* context_lens, int32_t batch,
+                                     int32_t num_q_heads, float scale, kvp_cache_desc cache,
+                                     int32_t partition_blocks, void* workspace,
+                                     size_t workspace_bytes, int32_t phases, int32_t* dev_status,
+                                     kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_attention_decode_int4");
+  if (dtype != KVP_F16 && dtype != KVP_BF16) return KVP_ERR_INVALID_ARG;
+  return decode_common(out, q, dtype == KVP_BF16, 5, k_cache, v_cache, k_scale_zero, v_scale_zero,
+                       block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads, scale,
+                       cache, partition_blocks, workspace, workspace_bytes, phases, dev_status,
+                       stream);
+}
+
+kvp_status kvp_rope_append(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                           const void* key, int64_t k_stride, const void* value,
+                           int64_t v_stride, void* k_cache, void* v_cache, const float* cos_sin,
+                           int32_t max_position, const int32_t* positions,
+                           const int32_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                           kvp_rope_desc rope, kvp_cache_desc cache, kvp_dtype dtype,
+                           int32_t* dev_status, kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_rope_append");
+  return rope_append_common(q_out, q_out_stride, q, q_stride, key, k_stride, value, v_stride,
+                            k_cache, v_cache, nullptr, nullptr, false, cos_sin, max_position,
+                            positions, slot_mapping, num_tokens, num_q_heads, rope, cache, dtype,
+                            dev_status, stream);
+}
+
+kvp_status kvp_rope_append_int4(void* q_out, int64_t q_out_stride, const void* q,
+                                int64_t q_stride, const void* key, int64_t k_stride,
+                                const void* value, int64_t v_stride, uint8_t* k_cache,
+                                uint8_t* v_cache, void* k_scale_zero, void* v_scale_zero,
+                                const float* cos_sin, int32_t max_position,
+                                const int32_t* positions, const int32_t* slot_mapping,
+                                int32_t num_tokens, int32_t num_q_heads, kvp_rope_desc rope,
+                                kvp_cache_desc cache, kvp_dtype dtype, int32_t* dev_status,
+                                kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_rope_append_int4");
+  return rope_append_common(q_out, q_out_stride, q, q_stride, key, k_stride, value, v_stride,
+                            k_cache, v_cache, k_scale_zero, v_scale_zero, true, cos_sin,
+                            max_position, positions, slot_mapping, num_tokens, num_q_heads, rope,
+                            cache, dtype, dev_status, stream);
+}
+
+kvp_status kvp_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
+                             const int32_t* context_lens, const int32_t* new_lens, int32_t batch,
+                             const int32_t* free_blocks, const int32_t* free_count,
+                             int32_t num_blocks, int32_t* context_lens_out,
+                             int32_t* free_count_out, int32_t* slot_mapping, int32_t num_tokens,
+                             int32_t* query_start, int32_t* positions, int32_t* dev_status,
+                             kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_extend_tables");
+  if (batch < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || num_tokens < 0)
+    return KVP_ERR_INVALID_ARG;
+  if (batch > kMaxTableBatch || num_blocks > 0x7fffffff / kBlockSize ||
+      max_blocks_per_seq > 0x7fffffff / kBlockSize)
+    return KVP_ERR_UNSUPPORTED;
+  if (!free_blocks || !free_count || !free_count_out || !query_start) return KVP_ERR_INVALID_ARG;
+  if (batch > 0 && (!block_tables || !context_lens || !new_lens || !context_lens_out))
+    return KVP_ERR_INVALID_ARG;
+  if (num_tokens > 0 && !slot_mapping) return KVP_ERR_INVALID_ARG;
+  TableParams p{};
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.new_lens = new_lens;
+  p.free_blocks = const_cast<int32_t*>(free_blocks);  // only read
+  p.free_count = free_count;
+  p.context_lens_out = context_lens_out;
+  p.free_count_out = free_count_out;
+  p.slot_mapping = slot_mapping;
+  p.query_start = query_start;
+  p.positions = positions;
+  p.status = dev_status;
+  p.batch = batch;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.num_tokens = num_tokens;
+  return from_cuda(launch_extend_tables(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_release_tables(const int32_t* block_tables, int32_t max_blocks_per_seq,
+                              const int32_t* context_lens, const int32_t* finished,
+                              int32_t batch, int32_t* free_blocks, const int32_t* free_count,
+                              int32_t num_blocks, int32_t* context_lens_out,
+                              int32_t* free_count_out, int32_t* dev_status, kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_release_tables");
+  if (batch < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0) return KVP_ERR_INVALID_ARG;
+  if (batch > kMaxTableBatch || num_blocks > 0x7fffffff / kBlockSize ||
+      max_blocks_per_seq > 0x7fffffff / kBlockSize)
+    return KVP_ERR_UNSUPPORTED;
+  if (!free_blocks || !free_count || !free_count_out) return KVP_ERR_INVALID_ARG;
+  if (batch > 0 && (!block_tables || !context_lens || !finished || !context_lens_out))
+    return KVP_ERR_INVALID_ARG;
+  TableParams p{};
+  p.block_tables = const_cast<int32_t*>(block_tables);  // only read
+  p.context_lens = context_lens;
+  p.finished = finished;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.context_lens_out = context_lens_out;
+  p.free_count_out = free_count_out;
+  p.status = dev_status;
+  p.batch = batch;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  return from_cuda(launch_release_tables(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kvp_status kvp_attention_prefill(void* out, const void* q, const void* k_cache,

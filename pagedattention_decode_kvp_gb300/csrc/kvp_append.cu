@@ -348,23 +348,39 @@ cudaError_t launch_append_fp8(const void* key, const void* value, bool src_bf16,
                                        0.f, 0.f, slots, num_tokens, c, status, s);
 }
 
-cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
-                               int elem_bytes, const int32_t* pairs, int num_pairs,
-                               const kvp_cache_desc& c, int32_t* status, cudaStream_t s) {
+// chunks_kv, chunks_scale: 16-byte chunks of one block's K (or V) codes and of
+// its scales.
+static cudaError_t launch_copy_chunks(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                                      long long chunks_kv, long long chunks_scale,
+                                      const int32_t* pairs, int num_pairs, int num_blocks,
+                                      int32_t* status, cudaStream_t s) {
   if (num_pairs == 0) return cudaSuccess;
-  const long long block_bytes =
-      static_cast<long long>(c.num_kv_heads) * kBlockSize * c.head_dim * elem_bytes;
-  const long long chunks_kv = block_bytes / 16;
-  const long long chunks_scale = static_cast<long long>(c.num_kv_heads) * kBlockSize * 4 / 16;
   long long gx = (chunks_kv + 1023) / 1024;  // ~4 chunks per thread
   if (gx < 1) gx = 1;
   if (gx > 1024) gx = 1024;
   const dim3 grid(static_cast<unsigned>(gx),
                   static_cast<unsigned>(num_pairs < 65535 ? num_pairs : 65535));
   return launch_pdl(copy_blocks_kernel, grid, dim3(256), 0, s, static_cast<uint4*>(k_cache),
-                    static_cast<uint4*>(v_cache), reinterpret_cast<uint4*>(k_scale),
-                    reinterpret_cast<uint4*>(v_scale), pairs, num_pairs, chunks_kv,
-                    chunks_scale, c.num_blocks, status);
+                    static_cast<uint4*>(v_cache), static_cast<uint4*>(k_scale),
+                    static_cast<uint4*>(v_scale), pairs, num_pairs, chunks_kv, chunks_scale,
+                    num_blocks, status);
+}
+
+cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                               int elem_bytes, const int32_t* pairs, int num_pairs,
+                               const kvp_cache_desc& c, int32_t* status, cudaStream_t s) {
+  const long long rows = static_cast<long long>(c.num_kv_heads) * kBlockSize;
+  return launch_copy_chunks(k_cache, v_cache, k_scale, v_scale, rows * c.head_dim * elem_bytes / 16,
+                            rows * 4 / 16, pairs, num_pairs, c.num_blocks, status, s);
+}
+
+cudaError_t launch_copy_blocks_int4(void* k_cache, void* v_cache, void* k_sz, void* v_sz,
+                                    const int32_t* pairs, int num_pairs, const kvp_cache_desc& c,
+                                    int32_t* status, cudaStream_t s) {
+  const long long rows = static_cast<long long>(c.num_kv_heads) * kBlockSize;
+  return launch_copy_chunks(k_cache, v_cache, k_sz, v_sz, rows * (c.head_dim / 2) / 16,
+                            rows * (c.head_dim / 64) * 4 / 16, pairs, num_pairs, c.num_blocks,
+                            status, s);
 }
 
 }  // namespace kvp
