@@ -431,37 +431,45 @@ def kvp_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, 
 # ------------------------------------------------------------------ 4-bit cache
 def _on_one_device(stream, *ts) -> int:
     """CUDA tensors of one device, which is the current one (kernels launch
-    there); returns the stream to use."""
+    there); returns the stream to use.  (These calls are short: the checks are
+    written to cost less than the launch.)"""
     torch = _torch()
-    dev = -1
+    dev = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
         d = t.get_device()
-        if dev < 0:
+        if d != dev:
+            if d < 0:
+                raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
+            if dev is not None:
+                raise ValueError(f"tensors on cuda:{dev} and cuda:{d} in one call")
             dev = d
-        elif d != dev:
-            raise ValueError(f"tensors on cuda:{dev} and cuda:{d} in one call")
-    if dev >= 0 and dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+                         f"cuda:{torch._C._cuda_getDevice()}")
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if dev >= 0 and stream.device_index != dev:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
         raise ValueError(f"tensors on cuda:{dev}, but the stream is of cuda:{stream.device_index}")
     return stream.cuda_stream
 
 
-def _need(t, name, dtype, *shape):
-    """A contiguous tensor of the given type and shape (None: any extent)."""
-    if t.dtype != dtype:
+def _need(t, name, dtype, shape):
+    """A contiguous tensor of the given type and shape."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError("tensors passed to the GPU entry points must be contiguous")
+
+
+def _extents(t, name, dims):
+    """Shape of a tensor of that many dimensions."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 def cache_desc_int4(k_cache) -> kvp_cache_desc:
@@ -476,13 +484,13 @@ def _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype=None) -> kvp
     torch = _torch()
     d = cache_desc_int4(k_cache)
     codes = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim // 2)
-    _need(k_cache, "k_cache", torch.uint8, *codes)
-    _need(v_cache, "v_cache", torch.uint8, *codes)
+    _need(k_cache, "k_cache", torch.uint8, codes)
+    _need(v_cache, "v_cache", torch.uint8, codes)
     if d.head_dim in (64, 128):  # the library refuses others
         pairs = codes[:3] + (d.head_dim // 64, 2)
         dtype = k_scale_zero.dtype if dtype is None else dtype
-        _need(k_scale_zero, "k_scale_zero", dtype, *pairs)
-        _need(v_scale_zero, "v_scale_zero", dtype, *pairs)
+        _need(k_scale_zero, "k_scale_zero", dtype, pairs)
+        _need(v_scale_zero, "v_scale_zero", dtype, pairs)
     return d
 
 
@@ -496,10 +504,11 @@ def kvp_append_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, sl
                        slot_mapping, status)
     code = _dtype_code(key)
     d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
-    _need(slot_mapping, "slot_mapping", _torch().int32, None)
-    T = slot_mapping.shape[0]
-    _need(key, "key", key.dtype, T, d.num_kv_heads, d.head_dim)
-    _need(value, "value", key.dtype, T, d.num_kv_heads, d.head_dim)
+    T, = _extents(slot_mapping, "slot_mapping", 1)
+    _need(slot_mapping, "slot_mapping", _torch().int32, (T,))
+    rows = (T, d.num_kv_heads, d.head_dim)
+    _need(key, "key", key.dtype, rows)
+    _need(value, "value", key.dtype, rows)
     _check(lib.kvp_append_int4(key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(),
                                v_cache.data_ptr(), k_scale_zero.data_ptr(),
                                v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
@@ -515,10 +524,11 @@ def kvp_read_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot
                        slot_mapping, status)
     code = _dtype_code(key)
     d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
-    _need(slot_mapping, "slot_mapping", _torch().int32, None)
-    T = slot_mapping.shape[0]
-    _need(key, "key", key.dtype, T, d.num_kv_heads, d.head_dim)
-    _need(value, "value", key.dtype, T, d.num_kv_heads, d.head_dim)
+    T, = _extents(slot_mapping, "slot_mapping", 1)
+    _need(slot_mapping, "slot_mapping", _torch().int32, (T,))
+    rows = (T, d.num_kv_heads, d.head_dim)
+    _need(key, "key", key.dtype, rows)
+    _need(value, "value", key.dtype, rows)
     _check(lib.kvp_read_int4(key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(),
                              v_cache.data_ptr(), k_scale_zero.data_ptr(),
                              v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
@@ -531,7 +541,7 @@ def kvp_copy_blocks_int4(k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, *,
     lib = load_library()
     s = _on_one_device(stream, k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, status)
     d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero)
-    _need(pairs, "pairs", _torch().int32, None, 2)
+    _need(pairs, "pairs", _torch().int32, (_extents(pairs, "pairs", 2)[0], 2))
     _check(lib.kvp_copy_blocks_int4(k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
                                     pairs.data_ptr(), pairs.shape[0], d, _ptr(status), s),
@@ -549,12 +559,14 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
                        context_lens, workspace, status)
     code = _dtype_code(q)
     d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, q.dtype)
-    _need(q, "q", q.dtype, None, None, d.head_dim)
-    B, Hq = q.shape[0], q.shape[1]
-    _need(out, "out", q.dtype, B, Hq, d.head_dim)
+    B, Hq, _ = _extents(q, "q", 3)
+    rows = (B, Hq, d.head_dim)
+    _need(q, "q", q.dtype, rows)
+    _need(out, "out", q.dtype, rows)
     i32 = _torch().int32
-    _need(block_tables, "block_tables", i32, B, None)
-    _need(context_lens, "context_lens", i32, B)
+    MB = _extents(block_tables, "block_tables", 2)[1]
+    _need(block_tables, "block_tables", i32, (B, MB))
+    _need(context_lens, "context_lens", i32, (B,))
     ws, ws_bytes = None, 0
     if workspace is not None:
         if not workspace.is_contiguous():
@@ -563,8 +575,7 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
     _check(lib.kvp_attention_decode_int4(
         out.data_ptr(), q.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), B, Hq, float(scale), d,
-        int(partition_blocks), ws, ws_bytes, int(phases), _ptr(status), s),
+        MB, context_lens.data_ptr(), B, Hq, float(scale), d, int(partition_blocks), ws, ws_bytes, int(phases), _ptr(status), s),
         "kvp_attention_decode_int4")
 
 
@@ -572,9 +583,9 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
 def _rows(t, name, dtype, T, heads, dim) -> int:
     """Element stride between the tokens of t [T, heads, dim], whose rows are
     contiguous and lie behind one another (a slice of a projection's output)."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[1] != heads or t.shape[2] != dim:
+    if t.shape != (T, heads, dim):
         raise ValueError(f"{name} must have shape {(T, heads, dim)}, got {tuple(t.shape)}")
     st, sh, sd = t.stride()
     if sd != 1 or (sh != dim and heads > 1):
@@ -585,14 +596,12 @@ def _rows(t, name, dtype, T, heads, dim) -> int:
 def _rope_args(q_out, q, key, value, kv_heads, dim, cos_sin, positions, slot_mapping, sections,
                interleaved):
     torch = _torch()
-    _need(slot_mapping, "slot_mapping", torch.int32, None)
-    T = slot_mapping.shape[0]
-    _need(cos_sin, "cos_sin", torch.float32, None, None)
-    P, R = cos_sin.shape
-    if positions.dim() == 1:
-        positions = positions[None]
-    _need(positions, "positions", torch.int32, None, T)
-    A = positions.shape[0]
+    T, = _extents(slot_mapping, "slot_mapping", 1)
+    _need(slot_mapping, "slot_mapping", torch.int32, (T,))
+    P, R = _extents(cos_sin, "cos_sin", 2)
+    _need(cos_sin, "cos_sin", torch.float32, (P, R))
+    A = positions.shape[0] if positions.dim() == 2 else 1
+    _need(positions, "positions", torch.int32, (A, T) if positions.dim() == 2 else (T,))
     sections = (R // 2,) if sections is None else sections
     if len(sections) != A or A > 4:
         raise ValueError(f"positions has {A} axes (1 to 4 are allowed), sections {len(sections)}")
@@ -628,8 +637,8 @@ def kvp_rope_append(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, 
     code = _dtype_code(key)
     d = cache_desc(k_cache)
     pool = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
-    _need(k_cache, "k_cache", key.dtype, *pool)
-    _need(v_cache, "v_cache", key.dtype, *pool)
+    _need(k_cache, "k_cache", key.dtype, pool)
+    _need(v_cache, "v_cache", key.dtype, pool)
     T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d.num_kv_heads, d.head_dim, cos_sin,
                                       positions, slot_mapping, sections, interleaved)
     _check(lib.kvp_rope_append(*rows, k_cache.data_ptr(), v_cache.data_ptr(), cos_sin.data_ptr(),
@@ -671,20 +680,24 @@ def kvp_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_co
                        context_lens_out, free_count_out, slot_mapping, query_start, positions,
                        status)
     i32 = _torch().int32
-    _need(block_tables, "block_tables", i32, None, None)
-    B, MB = block_tables.shape
-    for t, name, n in ((context_lens, "context_lens", B), (new_lens, "new_lens", B),
-                       (context_lens_out, "context_lens_out", B), (free_count, "free_count", 1),
-                       (free_count_out, "free_count_out", 1), (free_blocks, "free_blocks", None),
-                       (query_start, "query_start", B + 1),
-                       (slot_mapping, "slot_mapping", None)):
-        _need(t, name, i32, n)
-    T = slot_mapping.shape[0]
+    B, MB = _extents(block_tables, "block_tables", 2)
+    T, = _extents(slot_mapping, "slot_mapping", 1)
+    NB, = _extents(free_blocks, "free_blocks", 1)
+    per_request = (B,)
+    _need(block_tables, "block_tables", i32, (B, MB))
+    _need(context_lens, "context_lens", i32, per_request)
+    _need(new_lens, "new_lens", i32, per_request)
+    _need(context_lens_out, "context_lens_out", i32, per_request)
+    _need(free_blocks, "free_blocks", i32, (NB,))
+    _need(free_count, "free_count", i32, (1,))
+    _need(free_count_out, "free_count_out", i32, (1,))
+    _need(query_start, "query_start", i32, (B + 1,))
+    _need(slot_mapping, "slot_mapping", i32, (T,))
     if positions is not None:
-        _need(positions, "positions", i32, T)
+        _need(positions, "positions", i32, (T,))
     _check(lib.kvp_extend_tables(block_tables.data_ptr(), MB, context_lens.data_ptr(),
                                  new_lens.data_ptr(), B, free_blocks.data_ptr(),
-                                 free_count.data_ptr(), free_blocks.shape[0],
+                                 free_count.data_ptr(), NB,
                                  context_lens_out.data_ptr(), free_count_out.data_ptr(),
                                  slot_mapping.data_ptr(), T, query_start.data_ptr(),
                                  _ptr(positions), _ptr(status), s), "kvp_extend_tables")
@@ -698,15 +711,19 @@ def kvp_release_tables(block_tables, context_lens, finished, free_blocks, free_c
     s = _on_one_device(stream, block_tables, context_lens, finished, free_blocks, free_count,
                        context_lens_out, free_count_out, status)
     i32 = _torch().int32
-    _need(block_tables, "block_tables", i32, None, None)
-    B, MB = block_tables.shape
-    for t, name, n in ((context_lens, "context_lens", B), (finished, "finished", B),
-                       (context_lens_out, "context_lens_out", B), (free_count, "free_count", 1),
-                       (free_count_out, "free_count_out", 1), (free_blocks, "free_blocks", None)):
-        _need(t, name, i32, n)
+    B, MB = _extents(block_tables, "block_tables", 2)
+    NB, = _extents(free_blocks, "free_blocks", 1)
+    per_request = (B,)
+    _need(block_tables, "block_tables", i32, (B, MB))
+    _need(context_lens, "context_lens", i32, per_request)
+    _need(finished, "finished", i32, per_request)
+    _need(context_lens_out, "context_lens_out", i32, per_request)
+    _need(free_blocks, "free_blocks", i32, (NB,))
+    _need(free_count, "free_count", i32, (1,))
+    _need(free_count_out, "free_count_out", i32, (1,))
     _check(lib.kvp_release_tables(block_tables.data_ptr(), MB, context_lens.data_ptr(),
                                   finished.data_ptr(), B, free_blocks.data_ptr(),
-                                  free_count.data_ptr(), free_blocks.shape[0],
+                                  free_count.data_ptr(), NB,
                                   context_lens_out.data_ptr(), free_count_out.data_ptr(),
                                   _ptr(status), s), "kvp_release_tables")
 

@@ -126,10 +126,15 @@ struct DecodeShape {
   DecodePath path;
   int heads_per_cta;
   int qgroups;
-  int part_blocks;
-  int max_parts;
+  int part_blocks;  // 0: balanced (4-bit pools)
+  int run_blocks;   // blocks per CTA when every context fills its table
+  int max_parts;    // partitions, or CTAs of a balanced decode
   size_t ws_bytes;
 };
+
+// 4-bit contexts of up to 16 blocks take one CTA per unit and no merge: the
+// second launch costs more than the split saves there.
+constexpr int kInt4SinglePass = 16;
 
 // Split-context rule.  Each (request, kv head, query group) unit is cut into
 // `parts` partitions of ceil(MB / parts) blocks, run as independent CTAs on
@@ -148,7 +153,7 @@ constexpr double kReduceCostBlocks = 2.0;
 int resident_ctas(DecodePath path) {
   switch (path) {
     case DecodePath::kMmaInt8: return 4;
-    case DecodePath::kInt4: return 4;
+    case DecodePath::kInt4: return 3;
     case DecodePath::kUmmaFp8: return 2;
     default: return 3;
   }
@@ -204,10 +209,26 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
   }
   s.qgroups = (G + s.heads_per_cta - 1) / s.heads_per_cta;
   const long long units = static_cast<long long>(batch) * c.num_kv_heads * s.qgroups;
+  if (s.path == DecodePath::kInt4 && partition_blocks == 0 && max_blocks > kInt4SinglePass) {
+    // balanced: equal pieces of all contexts, a CTA per piece and unit of a
+    // request; two partial states of up to 8 heads per CTA and a note
+    const int per_request = c.num_kv_heads * s.qgroups;
+    const int pieces = std::max(1, kInt4Ctas / per_request);
+    const long long even = (static_cast<long long>(batch) * max_blocks + pieces - 1) / pieces;
+    s.part_blocks = 0;
+    s.run_blocks = static_cast<int>(std::min<long long>(std::max(even, 8ll), max_blocks));
+    s.max_parts = pieces * per_request;
+    s.ws_bytes = static_cast<size_t>(s.max_parts) *
+                 (2 * kHeadsPerCta * (static_cast<size_t>(c.head_dim) + 2) * sizeof(float) +
+                  sizeof(::int4));
+    *out = s;
+    return KVP_OK;
+  }
   int pb = partition_blocks > 0 ? partition_blocks : auto_partition(s.path, units, max_blocks);
   if (pb >= max_blocks) pb = max_blocks;
   if (pb > kMaxPartBlocks) return KVP_ERR_UNSUPPORTED;  // one partition must fit on chip
   s.part_blocks = pb;
+  s.run_blocks = pb;
   s.max_parts = (max_blocks + pb - 1) / pb;
   s.ws_bytes = s.max_parts > 1 ? static_cast<size_t>(batch) * num_q_heads * s.max_parts *
                                      (static_cast<size_t>(c.head_dim) + 2) * sizeof(float)
@@ -257,9 +278,11 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
   p.block_tables = tables;
   p.context_lens = lens;
   p.ws_o = static_cast<float*>(ws);
-  p.ws_ml = sh.ws_bytes ? static_cast<float*>(ws) + static_cast<size_t>(batch) * hq *
-                                                        sh.max_parts * c.head_dim
-                        : nullptr;
+  const bool balanced = sh.part_blocks == 0;
+  const size_t ws_rows = balanced ? static_cast<size_t>(sh.max_parts) * 2 * kHeadsPerCta
+                                  : static_cast<size_t>(batch) * hq * sh.max_parts;
+  p.ws_ml = sh.ws_bytes ? static_cast<float*>(ws) + ws_rows * c.head_dim : nullptr;
+  p.notes = balanced ? reinterpret_cast<::int4*>(p.ws_ml + ws_rows * 2) : nullptr;
   p.status = status;
   p.batch = batch;
   p.num_q_heads = hq;
@@ -323,7 +346,9 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
     if (e != cudaSuccess) return KVP_ERR_CUDA;
   }
   if ((phases & KVP_PHASE_REDUCE) && sh.max_parts > 1) {
-    if (launch_decode_reduce(p, s) != cudaSuccess) return KVP_ERR_CUDA;
+    if ((balanced ? launch_decode_int4_merge(p, sh.max_parts, s) : launch_decode_reduce(p, s)) !=
+        cudaSuccess)
+      return KVP_ERR_CUDA;
   }
   return KVP_OK;
 }
@@ -579,7 +604,7 @@ int32_t kvp_decode_partition_blocks(int32_t batch, int32_t num_q_heads, kvp_cach
   if (!sizing_kind(kv_int8) ||
       shape_decode(batch, num_q_heads, cache, max_blocks_per_seq, 0, kv_int8, &sh) != KVP_OK)
     return 0;
-  return sh.part_blocks;
+  return sh.run_blocks;
 }
 
 size_t kvp_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, kvp_cache_desc cache,

@@ -12,8 +12,7 @@
 //
 // A block is 2 (8 D + 32 D / 64) bytes = 2304 at D = 128, little over half of
 // an INT8 block, while a warp has the same 32 D codes to widen: the kernel is
-// bound by issue slots before HBM, so the arithmetic is arranged to widen a
-// code with less than one instruction.
+// bound by issue slots before HBM, so everything here saves instructions.
 //   * A code left where it lies is already a number: the fp16 bit pattern
 //     0x000c is the subnormal c 2^-24 and 0x00c0 is 16 c 2^-24, both exact
 //     tensor-core operands.  So one AND turns two codes into an operand pair,
@@ -25,25 +24,65 @@
 //     largest lose their last bits, 2^-35 of it), so one fp16 operand type
 //     serves both and a bf16 q needs no second path.
 //   * K's s multiplies a group's accumulator, z multiplies Q_g.
-//   * V's s goes into the weight, a_t = p_t s_t rho, rounded to fp16 (2^-12
-//     relative, independent from token to token); rho is a power of two per
-//     head that keeps a within [0, 4096], moved only when a block exceeds that,
-//     so the accumulators stay in the tensor core's registers and no block
-//     costs a rescale.  A product with ones gives sum_t a_t of the rounded
-//     weights; subtracting 7.5 times it centres the codes, so that the
-//     rounding of a is weighted by c - 7.5 and not by c.
-//   * The reference m of the softmax is moved in that same rare branch (when a
-//     weight passes 2^16), which saves the six shuffles of a maximum per block.
-//   * z's part, sum_t p_t (z_t + 7.5 s_t), is float32 on the lanes.
+//   * V's s goes into the weight, a_t = P_t s_t with P_t = 2^(u_t - r), rounded
+//     to fp16 (2^-12 relative on average, independent from token to token).  The
+//     reference r is not the maximum: it is set so that the largest a of a block
+//     lies in [8, 16) and moved only when an a passes 4096, so a block costs
+//     neither a maximum over its tokens nor a rescale.  Weights 2^-28 of the
+//     largest are the smallest that count, as for any fp16 weight.
+//   * A product with ones gives sum_t a_t of the rounded weights; subtracting
+//     7.5 times it centres the codes, so that the rounding of a is weighted by
+//     c - 7.5 and not by c.  (The ones are 1.0: with the subnormal 2^-24 in
+//     their place the sum came out 1e-6 too small, as if products were cut off
+//     where a normal operand's would be, and that is 5e-4 of the centred output
+//     at 4096 tokens per warp.)
+//   * A block's products start from zero and are added to the float32 sums in
+//     the lanes: the tensor core truncates to the size of its accumulator, and
+//     over a long context that loss, unlike a rounding, adds up.
+//   * z's part, sum_t P_t (z_t + 7.5 s_t), is float32 on the lanes.
+//   * Blocks come by cp.async, 16 bytes per lane (5 instructions a block at
+//     D = 128 where an elected lane's bulk copies, barriers and fences took 64),
+//     each warp through a ring of its own that needs no barrier at all.
 // Rows t of the score fragment hold tokens in the order 4 (t % 2) + t / 2 (+ 8
-// in the upper half), so that the four tokens a V load touches lie in
-// different shared-memory banks.
+// in the upper half), and the two groups of a row change places in every other
+// pair of rows, so that neither the K nor the V loads meet in a bank.
 #include "kvp_decode.cuh"
 
 namespace kvp {
 namespace {
 
-constexpr int kInt4Stages = 4;  // blocks in flight per warp
+constexpr int kStep = 2;                    // blocks a warp takes at a time
+constexpr int kBuf = 3;                     // steps per warp: one in use, two on the way
+constexpr int kInt4Stages = kStep * kBuf;   // blocks
+constexpr int kTable = 512;                 // table entries of a segment
+constexpr int kMinRun = 8;                  // blocks a balanced CTA takes at least
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+  const __half2 r =
+      __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Byte that 16-byte piece c of token row r takes in a block's code tile.
+template <int D>
+__device__ __forceinline__ int code_piece(int r, int c) {
+  const int swap = D == 128 ? 2 * (((r >> 1) ^ (r >> 2)) & 1) : 0;
+  return r * (D / 2) + ((c ^ swap) << 4);
+}
 
 template <bool kBf16, int D>
 struct Int4Path {
@@ -51,22 +90,23 @@ struct Int4Path {
   static constexpr int kHeads = 8;
   static constexpr int kElemBytes = 1;  // (no fused append)
   static constexpr int kGroups = D / 64;
-  static constexpr int kCodeBytes = 16 * D / 2;      // K or V codes of a block
+  static constexpr int kCodeBytes = 16 * D / 2;        // K or V codes of a block
   static constexpr int kPairBytes = 16 * kGroups * 4;  // their (s, z) pairs
   static constexpr int kStageBytes = 2 * (kCodeBytes + kPairBytes);
   static constexpr int kS = kWarps * kInt4Stages;
-  static_assert(kStageBytes % 128 == 0, "stages stay aligned for bulk copies");
-  static_assert(kWarps * kHeads * (D + 2) * 4 <= kS * kStageBytes, "merge area must fit");
+  static_assert(kStageBytes % 128 == 0, "stages stay aligned for 16-byte copies");
+
+  static constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // code pairs of a word
+  static constexpr uint32_t kOnes = 0x3c003c00u;
 
   struct State {
     uint32_t qb[kGroups][4][2];  // q operand per k-step
-    float o[kGroups][4][4];      // 2^-24 sum a c (rows 0, 1) and 2^-20 sum a c (rows 2, 3)
-    float as[kGroups][4];        // 2^-24 sum a, in every row
-    float zo[kGroups][2];        // sum p (z + 7.5 s), this lane's tokens
+    float o[kGroups][4][4];      // 2^-24 sum a c (0, 1) and 2^-20 sum a c (2, 3)
+    float as[kGroups][2];        // sum a
+    float zo[kGroups][2];        // sum P (z + 7.5 s), this lane's tokens
     float qz[kGroups][2];        // scale log2(e) Q_g
     float f[2];                  // scale log2(e) 2^20 / kappa
-    float m[2], l[2];            // reference and sum (this lane's tokens)
-    float rho[2];
+    float r[2], l[2];            // reference and sum of P (this lane's tokens)
   };
 
   // Power of two that takes x > 0 into [2^k, 2^(k+1)), its exponent within +-100.
@@ -76,21 +116,36 @@ struct Int4Path {
     return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
   }
 
-  __device__ __forceinline__ static void init(State& st, const DecodeParams& p, int b, int head0,
-                                              int nheads, int lane) {
+  // This lane's 16 elements per group of query head g8.
+  struct Query {
+    uint4 raw[kGroups][2];
+  };
+
+  __device__ __forceinline__ static void load_query(Query& x, const DecodeParams& p, int b,
+                                                    int head0, int nheads, int lane) {
     const int g8 = lane >> 2, t4 = lane & 3;
     const uint16_t* q = static_cast<const uint16_t*>(p.q) +
                         (static_cast<size_t>(b) * p.num_q_heads + head0 + g8) * D;
-    uint4 raw[kGroups][2];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        x.raw[g][w] = make_uint4(0u, 0u, 0u, 0u);
+        if (g8 < nheads)
+          x.raw[g][w] = *reinterpret_cast<const uint4*>(q + 64 * g + 16 * t4 + 8 * w);
+      }
+    }
+  }
+
+  __device__ __forceinline__ static void init(State& st, const Query& x, float scale_log2,
+                                              int lane) {
+    const int t4 = lane & 3;
     float big = 0.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        raw[g][w] = make_uint4(0u, 0u, 0u, 0u);
-        if (g8 < nheads)
-          raw[g][w] = *reinterpret_cast<const uint4*>(q + 64 * g + 16 * t4 + 8 * w);
-        const uint32_t r[4] = {raw[g][w].x, raw[g][w].y, raw[g][w].z, raw[g][w].w};
+        const uint32_t r[4] = {x.raw[g][w].x, x.raw[g][w].y, x.raw[g][w].z, x.raw[g][w].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 v = dev::unpack2<kBf16>(r[i]);
@@ -107,13 +162,13 @@ struct Int4Path {
       qs[g] = 0.f;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t r[4] = {raw[g][w].x, raw[g][w].y, raw[g][w].z, raw[g][w].w};
+        const uint32_t r[4] = {x.raw[g][w].x, x.raw[g][w].y, x.raw[g][w].z, x.raw[g][w].w};
         float v[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 x = dev::unpack2<kBf16>(r[i]);
-          v[2 * i] = x.x;
-          v[2 * i + 1] = x.y;
+          const float2 y = dev::unpack2<kBf16>(r[i]);
+          v[2 * i] = y.x;
+          v[2 * i + 1] = y.y;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -133,21 +188,20 @@ struct Int4Path {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int src = 4 * (2 * t4 + i);
-      st.f[i] = p.scale_log2 * 1048576.f / __shfl_sync(0xffffffffu, kappa, src);
+      st.f[i] = scale_log2 * 1048576.f / __shfl_sync(0xffffffffu, kappa, src);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        st.qz[g][i] = p.scale_log2 * __shfl_sync(0xffffffffu, qs[g], src);
+        st.qz[g][i] = scale_log2 * __shfl_sync(0xffffffffu, qs[g], src);
         st.zo[g][i] = 0.f;
       }
-      st.m[i] = -INFINITY;
+      st.r[i] = 0.f;
       st.l[i] = 0.f;
-      st.rho[i] = 1.f;
     }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
+      st.as[g][0] = st.as[g][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        st.as[g][i] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) st.o[g][j][i] = 0.f;
       }
@@ -173,26 +227,28 @@ struct Int4Path {
     }
   }
 
-  // A block's tiles: K codes, V codes, K pairs, V pairs.
-  __device__ __forceinline__ static void consume(State& st, const uint8_t* tile, int valid,
-                                                 int lane) {
-    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  // Scores of one block relative to the present reference (v = u - r) of this
+  // lane's rows g8, g8 + 8 and heads 2 t4, 2 t4 + 1, and V's pairs of those
+  // tokens.  kTail: only the first `valid` tokens count (other slots may hold
+  // anything).
+  template <bool kTail>
+  __device__ __forceinline__ static void scores(const State& st, const uint8_t* tile, int valid,
+                                                int lane, float (&v)[4], float (&s0)[kGroups],
+                                                float (&z0)[kGroups], float (&s1)[kGroups],
+                                                float (&z1)[kGroups]) {
     const int g8 = lane >> 2, t4 = lane & 3;
-    const int tok0 = 4 * (g8 & 1) + (g8 >> 1), tok1 = tok0 + 8;  // rows g8, g8 + 8
-    const uint8_t* kc = tile;
-    const uint8_t* vc = tile + kCodeBytes;
-    const uint8_t* kp = tile + 2 * kCodeBytes;
-    const uint8_t* vp = kp + kPairBytes;
-
-    // ---- scores
+    const int tok0 = 4 * (g8 & 1) + (g8 >> 1), tok1 = tok0 + 8;
     float ks0[kGroups], kz0[kGroups], ks1[kGroups], kz1[kGroups];
-    load_pairs(kp, tok0, ks0, kz0);
-    load_pairs(kp, tok1, ks1, kz1);
-    float u[4] = {0.f, 0.f, 0.f, 0.f}, uz[4] = {0.f, 0.f, 0.f, 0.f};
+    load_pairs(tile + 2 * kCodeBytes, tok0, ks0, kz0);
+    load_pairs(tile + 2 * kCodeBytes, tok1, ks1, kz1);
+    float us[4] = {0.f, 0.f, 0.f, 0.f};
+    v[0] = v[2] = -st.r[0];
+    v[1] = v[3] = -st.r[1];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const uint2 a = *reinterpret_cast<const uint2*>(kc + tok0 * (D / 2) + 32 * g + 8 * t4);
-      const uint2 b = *reinterpret_cast<const uint2*>(kc + tok1 * (D / 2) + 32 * g + 8 * t4);
+      const int at = code_piece<D>(tok0, 2 * g + (t4 >> 1)) + 8 * (t4 & 1);
+      const uint2 a = *reinterpret_cast<const uint2*>(tile + at);
+      const uint2 b = *reinterpret_cast<const uint2*>(tile + at + 8 * (D / 2));
       const uint32_t wa[2] = {a.x, a.y}, wb[2] = {b.x, b.y};
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -203,265 +259,669 @@ struct Int4Path {
         dev::mma16816<false>(acc, xs & kLow, ys & kLow, xs & kHigh, ys & kHigh,
                              st.qb[g][2 * w + 1][0], st.qb[g][2 * w + 1][1]);
       }
-      u[0] = fmaf(ks0[g], acc[0], u[0]);
-      u[1] = fmaf(ks0[g], acc[1], u[1]);
-      u[2] = fmaf(ks1[g], acc[2], u[2]);
-      u[3] = fmaf(ks1[g], acc[3], u[3]);
-      uz[0] = fmaf(kz0[g], st.qz[g][0], uz[0]);
-      uz[1] = fmaf(kz0[g], st.qz[g][1], uz[1]);
-      uz[2] = fmaf(kz1[g], st.qz[g][0], uz[2]);
-      uz[3] = fmaf(kz1[g], st.qz[g][1], uz[3]);
+      us[0] = fmaf(ks0[g], acc[0], us[0]);
+      us[1] = fmaf(ks0[g], acc[1], us[1]);
+      us[2] = fmaf(ks1[g], acc[2], us[2]);
+      us[3] = fmaf(ks1[g], acc[3], us[3]);
+      v[0] = fmaf(kz0[g], st.qz[g][0], v[0]);
+      v[1] = fmaf(kz0[g], st.qz[g][1], v[1]);
+      v[2] = fmaf(kz1[g], st.qz[g][0], v[2]);
+      v[3] = fmaf(kz1[g], st.qz[g][1], v[3]);
     }
-    u[0] = fmaf(u[0], st.f[0], uz[0]);
-    u[1] = fmaf(u[1], st.f[1], uz[1]);
-    u[2] = fmaf(u[2], st.f[0], uz[2]);
-    u[3] = fmaf(u[3], st.f[1], uz[3]);
-    float vs0[kGroups], vz0[kGroups], vs1[kGroups], vz1[kGroups];
-    load_pairs(vp, tok0, vs0, vz0);
-    load_pairs(vp, tok1, vs1, vz1);
-    if (valid < 16) {  // slots past the context may hold anything
+    v[0] = fmaf(us[0], st.f[0], v[0]);
+    v[1] = fmaf(us[1], st.f[1], v[1]);
+    v[2] = fmaf(us[2], st.f[0], v[2]);
+    v[3] = fmaf(us[3], st.f[1], v[3]);
+    load_pairs(tile + 2 * kCodeBytes + kPairBytes, tok0, s0, z0);
+    load_pairs(tile + 2 * kCodeBytes + kPairBytes, tok1, s1, z1);
+    if constexpr (kTail) {
       const bool in0 = tok0 < valid, in1 = tok1 < valid;
-      u[0] = in0 ? u[0] : -INFINITY;
-      u[1] = in0 ? u[1] : -INFINITY;
-      u[2] = in1 ? u[2] : -INFINITY;
-      u[3] = in1 ? u[3] : -INFINITY;
+      v[0] = in0 ? v[0] : -INFINITY;
+      v[1] = in0 ? v[1] : -INFINITY;
+      v[2] = in1 ? v[2] : -INFINITY;
+      v[3] = in1 ? v[3] : -INFINITY;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        vs0[g] = in0 ? vs0[g] : 0.f;
-        vz0[g] = in0 ? vz0[g] : 0.f;
-        vs1[g] = in1 ? vs1[g] : 0.f;
-        vz1[g] = in1 ? vz1[g] : 0.f;
-      }
-    }
-
-    // ---- weights against the present reference
-    float pr[4], a[kGroups][4];
-    auto weights = [&] {
-      pr[0] = dev::ex2_approx(u[0] - st.m[0]);
-      pr[1] = dev::ex2_approx(u[1] - st.m[1]);
-      pr[2] = dev::ex2_approx(u[2] - st.m[0]);
-      pr[3] = dev::ex2_approx(u[3] - st.m[1]);
-      const float r0 = pr[0] * st.rho[0], r1 = pr[1] * st.rho[1];
-      const float r2 = pr[2] * st.rho[0], r3 = pr[3] * st.rho[1];
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        a[g][0] = r0 * vs0[g];
-        a[g][1] = r1 * vs0[g];
-        a[g][2] = r2 * vs1[g];
-        a[g][3] = r3 * vs1[g];
-      }
-    };
-    weights();
-    float amax = fmaxf(fmaxf(a[0][0], a[0][1]), fmaxf(a[0][2], a[0][3]));
-    if constexpr (kGroups == 2)
-      amax = fmaxf(amax, fmaxf(fmaxf(a[1][0], a[1][1]), fmaxf(a[1][2], a[1][3])));
-    const float pmax = fmaxf(fmaxf(pr[0], pr[1]), fmaxf(pr[2], pr[3]));
-    if (__any_sync(0xffffffffu, amax > 4096.f || pmax > 65536.f || st.m[0] == -INFINITY)) {
-      // ---- rare: move the reference to the block's maximum and rho to its weights
-      float mx0 = fmaxf(u[0], u[2]), mx1 = fmaxf(u[1], u[3]);
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-      }
-      const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
-      const float al[2] = {dev::ex2_approx(st.m[0] - mn0), dev::ex2_approx(st.m[1] - mn1)};
-      st.m[0] = mn0;
-      st.m[1] = mn1;
-      const float old[2] = {st.rho[0], st.rho[1]};
-      st.rho[0] = st.rho[1] = 1.f;
-      weights();
-      float ax[2] = {fmaxf(a[0][0], a[0][2]), fmaxf(a[0][1], a[0][3])};
-      if constexpr (kGroups == 2) {
-        ax[0] = fmaxf(ax[0], fmaxf(a[1][0], a[1][2]));
-        ax[1] = fmaxf(ax[1], fmaxf(a[1][1], a[1][3]));
-      }
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        ax[0] = fmaxf(ax[0], __shfl_xor_sync(0xffffffffu, ax[0], o));
-        ax[1] = fmaxf(ax[1], __shfl_xor_sync(0xffffffffu, ax[1], o));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // no weight yet (constant rows): the largest rho, until one exceeds it
-        st.rho[i] = ax[i] > 0.f ? pow2_to(ax[i], 3) : 1.2676506e30f;  // 2^100
-        const int e = (static_cast<int>(__float_as_uint(st.rho[i])) -
-                       static_cast<int>(__float_as_uint(old[i]))) >> 23;
-        const float ratio =
-            al[i] * __uint_as_float(static_cast<uint32_t>(127 + min(126, max(-126, e))) << 23);
-        st.l[i] *= al[i];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          st.zo[g][i] *= al[i];
-          st.as[g][i] *= ratio;
-          st.as[g][i + 2] *= ratio;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            st.o[g][j][i] *= ratio;
-            st.o[g][j][i + 2] *= ratio;
-          }
-        }
-      }
-      weights();
-    }
-    st.l[0] += pr[0] + pr[2];
-    st.l[1] += pr[1] + pr[3];
-
-    // ---- values
-    const uint8_t* vrow = vc + t4 * (D / 2) + 4 * g8;  // token t4, this lane's 8 codes
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const float z0 = fmaf(7.5f, vs0[g], vz0[g]), z1 = fmaf(7.5f, vs1[g], vz1[g]);
-      st.zo[g][0] = fmaf(pr[0], z0, fmaf(pr[2], z1, st.zo[g][0]));
-      st.zo[g][1] = fmaf(pr[1], z0, fmaf(pr[3], z1, st.zo[g][1]));
-      const uint32_t b0 = dev::movm_t(dev::pack2<false>(a[g][0], a[g][1]));
-      const uint32_t b1 = dev::movm_t(dev::pack2<false>(a[g][2], a[g][3]));
-      const uint32_t wa = *reinterpret_cast<const uint32_t*>(vrow + 32 * g);
-      const uint32_t wb = *reinterpret_cast<const uint32_t*>(vrow + 32 * g + 4 * (D / 2));
-      const uint32_t wc = *reinterpret_cast<const uint32_t*>(vrow + 32 * g + 8 * (D / 2));
-      const uint32_t wd = *reinterpret_cast<const uint32_t*>(vrow + 32 * g + 12 * (D / 2));
-      dev::mma16816<false>(st.as[g], 0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u, b0, b1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // codes 0-3, then 4-7, of each token's word
-        const uint32_t x = dev::prmt(wa, wb, h == 0 ? 0x5410u : 0x7632u);
-        const uint32_t y = dev::prmt(wc, wd, h == 0 ? 0x5410u : 0x7632u);
-        const uint32_t xs = x >> 8, ys = y >> 8;
-        dev::mma16816<false>(st.o[g][2 * h], x & kLow, x & kHigh, y & kLow, y & kHigh, b0, b1);
-        dev::mma16816<false>(st.o[g][2 * h + 1], xs & kLow, xs & kHigh, ys & kLow, ys & kHigh, b0,
-                             b1);
+        s0[g] = in0 ? s0[g] : 0.f;
+        z0[g] = in0 ? z0[g] : 0.f;
+        s1[g] = in1 ? s1[g] : 0.f;
+        z1[g] = in1 ? z1[g] : 0.f;
       }
     }
   }
 
-  __device__ __forceinline__ static void finalize(State& st, float* mo, float* mm, float* ml,
-                                                  int lane) {
+  // Two blocks, kStageBytes apart (each: K codes, V codes, K pairs, V pairs).
+  // kTail: only the first `valid` of their 32 tokens count.  first: the warp's
+  // first pair, which sets the reference.
+  template <bool kTail>
+  __device__ __forceinline__ static void consume(State& st, const uint8_t* tile, int valid,
+                                                 bool first, int lane) {
     const int g8 = lane >> 2, t4 = lane & 3;
+    float v[kStep][4], s0[kStep][kGroups], z0[kStep][kGroups], s1[kStep][kGroups], z1[kStep][kGroups];
+#pragma unroll
+    for (int b = 0; b < kStep; ++b)
+      scores<kTail>(st, tile + b * kStageBytes, valid - 16 * b, lane, v[b], s0[b], z0[b], s1[b],
+                    z1[b]);
+
+    // ---- weights
+    float pr[kStep][4], l0, l1;
+    uint32_t ap[kStep][kGroups][2];  // a of rows g8 and g8 + 8, two heads each
+    auto weights = [&] {
+      l0 = st.l[0];
+      l1 = st.l[1];
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr[b][i] = dev::ex2_approx(v[b][i]);
+        l0 += pr[b][0] + pr[b][2];
+        l1 += pr[b][1] + pr[b][3];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          ap[b][g][0] = dev::pack2<false>(pr[b][0] * s0[b][g], pr[b][1] * s0[b][g]);
+          ap[b][g][1] = dev::pack2<false>(pr[b][2] * s1[b][g], pr[b][3] * s1[b][g]);
+        }
+      }
+    };
+    weights();
+    uint32_t top = 0u;
+#pragma unroll
+    for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) top = max_half2(top, max_half2(ap[b][g][0], ap[b][g][1]));
+    }
+    // an a above 4096 (0x6c00 in either half; a is never negative), or a sum of
+    // weights that nears the float range (2^110: weights of rows without scale)
+    const bool move =
+        ((top + 0x13ff13ffu) & 0x80008000u) != 0u || fmaxf(l0, l1) > 1.2980742e33f;
+    if (__any_sync(0xffffffffu, move || first)) {
+      reference(st, v, s0, s1, first);
+      weights();
+    }
+    st.l[0] = l0;
+    st.l[1] = l1;
+#pragma unroll
+    for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float c0 = fmaf(7.5f, s0[b][g], z0[b][g]), c1 = fmaf(7.5f, s1[b][g], z1[b][g]);
+        st.zo[g][0] = fmaf(pr[b][0], c0, fmaf(pr[b][2], c1, st.zo[g][0]));
+        st.zo[g][1] = fmaf(pr[b][1], c0, fmaf(pr[b][3], c1, st.zo[g][1]));
+      }
+    }
+
+    // ---- values: both blocks' products of a group in one chain
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f}, c[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+        const uint8_t* vc = tile + b * kStageBytes + kCodeBytes;
+        const uint32_t b0 = dev::movm_t(ap[b][g][0]);
+        const uint32_t b1 = dev::movm_t(ap[b][g][1]);
+        uint32_t w[4];  // this lane's 8 codes of tokens t4, t4 + 4, t4 + 8, t4 + 12
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = *reinterpret_cast<const uint32_t*>(
+              vc + code_piece<D>(t4 + 4 * i, 2 * g + (g8 >> 2)) + 4 * (g8 & 3));
+        dev::mma16816<false>(sum, kOnes, kOnes, kOnes, kOnes, b0, b1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // codes 0-3, then 4-7, of each token's word
+          const uint32_t x = dev::prmt(w[0], w[1], h == 0 ? 0x5410u : 0x7632u);
+          const uint32_t y = dev::prmt(w[2], w[3], h == 0 ? 0x5410u : 0x7632u);
+          const uint32_t xs = x >> 8, ys = y >> 8;
+          dev::mma16816<false>(c[2 * h], x & kLow, x & kHigh, y & kLow, y & kHigh, b0, b1);
+          dev::mma16816<false>(c[2 * h + 1], xs & kLow, xs & kHigh, ys & kLow, ys & kHigh, b0, b1);
+        }
+      }
+      st.as[g][0] += sum[0];
+      st.as[g][1] += sum[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[g][j][i] += c[j][i];
+      }
+    }
+  }
+
+  // Rare: move the reference so that the pair's largest a lies in [8, 16),
+  // never down.  v is relative to the old one on entry, to the new one on exit.
+  __device__ __forceinline__ static void reference(State& st, float (&v)[kStep][4],
+                                                   const float (&s0)[kStep][kGroups],
+                                                   const float (&s1)[kStep][kGroups], bool first) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = -INFINITY, big = 0.f;
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+        v[b][i] += st.r[i];
+        v[b][i + 2] += st.r[i];
+        mx = fmaxf(mx, fmaxf(v[b][i], v[b][i + 2]));
+      }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          big = fmaxf(big, fmaxf(dev::ex2_approx(v[b][i] - mx) * s0[b][g],
+                                 dev::ex2_approx(v[b][i + 2] - mx) * s1[b][g]));
+      }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      // no weight yet (rows of one value): 2^60, until one exceeds it
+      const int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+      const float shift = big > 0.f ? static_cast<float>(max(e, -80) - 3) : -60.f;
+      const float now = first ? mx + shift : fmaxf(st.r[i], mx + shift);
+      const float al = first ? 0.f : dev::ex2_approx(st.r[i] - now);
+      st.r[i] = now;
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+        v[b][i] -= now;
+        v[b][i + 2] -= now;
+      }
+      st.l[i] *= al;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        st.zo[g][i] *= al;
+        st.as[g][i] *= al;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          st.o[g][j][i] *= al;
+          st.o[g][j][i + 2] *= al;
+        }
+      }
+    }
+  }
+
+  // The warp's state for the merge: per (group, head parity) and lane, the 8
+  // outputs d = 64 g + 8 g8 ... + 7 of head 2 t4 + i as two 16-byte words, each
+  // at a place of its own for all 32 lanes (no two in a bank).
+  static constexpr int kParts = 2 * kGroups;  // (group, parity) pairs
+  static constexpr int kMergeFloats = kWarps * (kParts * 256 + 16);
+
+  __device__ __forceinline__ static void finalize(State& st, float* merge, int warp, int lane) {
+    const int g8 = lane >> 2, t4 = lane & 3;
+    float* ml = merge + kWarps * kParts * 256 + warp * 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float l = st.l[i];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      const float un = 16777216.f / st.rho[i];  // 2^24 / rho
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         float z = st.zo[g][i];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         const float mid = 7.5f * st.as[g][i];
-        float* row = mo + (2 * t4 + i) * D + 64 * g + 8 * g8;
+        float4* at = reinterpret_cast<float4*>(merge + (warp * kParts + 2 * g + i) * 256) + lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          row[2 * j] = fmaf(st.o[g][j][i] - mid, un, z);
-          row[2 * j + 1] = fmaf(fmaf(st.o[g][j][i + 2], 0.0625f, -mid), un, z);
-        }
+        for (int h = 0; h < 2; ++h)
+          at[32 * h] = make_float4(fmaf(st.o[g][2 * h][i], 16777216.f, -mid) + z,
+                                   fmaf(st.o[g][2 * h][i + 2], 1048576.f, -mid) + z,
+                                   fmaf(st.o[g][2 * h + 1][i], 16777216.f, -mid) + z,
+                                   fmaf(st.o[g][2 * h + 1][i + 2], 1048576.f, -mid) + z);
       }
       if (g8 == 0) {
-        mm[2 * t4 + i] = st.m[i];
-        ml[2 * t4 + i] = l;
+        ml[2 * t4 + i] = st.r[i];
+        ml[8 + 2 * t4 + i] = l;
       }
+    }
+  }
+
+  // Thread `tid` of the first 32 kParts merges 8 outputs of one head: their
+  // unnormalised sum, the reference M and the weight L (0 without tokens).
+  __device__ __forceinline__ static void merge8(const float* merge, int tid, float (&o)[8],
+                                                float& M, float& L, int& head, int& d) {
+    const int part = tid >> 5, lane = tid & 31;
+    head = 2 * (lane & 3) + (part & 1);
+    d = 64 * (part >> 1) + 8 * (lane >> 2);
+    const float* ml = merge + kWarps * kParts * 256;
+    M = -INFINITY;
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (ml[w * 16 + 8 + head] > 0.f) M = fmaxf(M, ml[w * 16 + head]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float l = ml[w * 16 + 8 + head];
+      const float f = l > 0.f ? exp2f(ml[w * 16 + head] - M) : 0.f;
+      L = fmaf(f, l, L);
+      const float4* at = reinterpret_cast<const float4*>(merge + (w * kParts + part) * 256) + lane;
+      const float4 x = at[0], y = at[32];
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(f, v[e], o[e]);
     }
   }
 };
 
-template <class Path>
-constexpr size_t int4_smem_for(int part_blocks) {
-  return 1024 + static_cast<size_t>(Path::kS) * Path::kStageBytes + Path::kS * 8 +
-         static_cast<size_t>(part_blocks) * 4 + 16;
+// What a CTA walks: segments of up to kTable blocks of one context.  A run (the
+// CTA's share of a context) is one segment or several.
+enum : int {
+  kInit = 1,      // a run's first segment
+  kMerge = 2,     // a run's last
+  kWhole = 4,     // the run is a whole context: its rows are final
+  kStart = 8,     // the run starts a context that later pieces end
+  kLater = 16     // not the CTA's first run
+};
+struct Segment {
+  int b, blk0, nb;  // request, its blocks blk0 ... blk0 + nb - 1 (nb = 0: no more)
+  int tail;         // valid tokens of the last one
+  int flags;
+  int runs;         // kStart: pieces the context spans
+};
+
+// Where a balanced CTA's runs lie.  The requests' blocks are laid end to end and
+// cut into equal pieces, and each (piece, unit) is a CTA, a unit being a kv head
+// and a group of its query heads, so that ragged contexts load the SMs evenly: a
+// CTA walks the end of one context, whole ones, and the start of another.  The
+// CTAs of a piece's units are neighbours and walk the same blocks at the same
+// time, which keeps the tiles of a block's kv heads together on their way
+// through the DRAM (units one after the other in one line instead: 99 us where
+// this took 82, contexts of 512 to 8192 tokens, 64 x 8 heads).  Only a piece's
+// first and last run can be partial; their states go to the CTA's two workspace
+// slots, and the CTA that starts a cut context leaves a note for the merge.
+struct Walk {
+  long long pos, end, size;  // blocks: next, the piece's end, per piece
+  int index;                 // of the piece
+  int b, n, nblk, blk0;      // context, its tokens and blocks, the next block
+  int left;                  // blocks of the present run
+  int flags, runs;
+};
+
+__device__ __forceinline__ int blocks_of(const DecodeParams& p, int n) {
+  return n <= 0 || n > p.max_blocks * kBlockSize ? 0 : (n + kBlockSize - 1) / kBlockSize;
+}
+
+// Sets the walk of piece `index` of `pieces`; false when it has no blocks.
+__device__ __forceinline__ bool find_piece(const DecodeParams& p, int index, int pieces,
+                                           Walk& walk) {
+  __shared__ long long part[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
+  const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += blocks_of(p, p.context_lens[b]);
+  long long sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) part[warp] = sum;
+  __syncthreads();
+  long long total = 0, at = sum - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at += part[w];
+    total += part[w];
+  }
+  const long long even = (total + pieces - 1) / pieces;
+  const long long size = even > kMinRun ? even : kMinRun;
+  const long long pos = index * size;
+  if (pos >= total) return false;
+  if (at <= pos && pos < at + mine) {  // one thread's requests hold the piece's start
+    int b = b0, nblk;
+    while (pos >= at + (nblk = blocks_of(p, p.context_lens[b]))) {
+      at += nblk;
+      ++b;
+    }
+    walk.pos = pos;
+    walk.end = min(total, pos + size);
+    walk.size = size;
+    walk.index = index;
+    walk.b = b;
+    walk.n = p.context_lens[b];
+    walk.nblk = nblk;
+    walk.blk0 = static_cast<int>(pos - at);
+    walk.left = walk.flags = 0;
+  }
+  __syncthreads();
+  return true;
+}
+
+// One thread: the walk's next segment.
+__device__ __forceinline__ void next_segment(const DecodeParams& p, Walk& walk, Segment& seg) {
+  int flags = walk.flags & ~kInit;
+  if (walk.left == 0) {
+    if (walk.pos >= walk.end) {
+      seg.nb = 0;
+      return;
+    }
+    flags = (flags & kLater) | kInit;
+    if (walk.blk0 == walk.nblk) {
+      do {
+        walk.n = p.context_lens[++walk.b];
+        walk.nblk = blocks_of(p, walk.n);
+      } while (walk.nblk == 0);
+      walk.blk0 = 0;
+    }
+    walk.left = static_cast<int>(
+        min(static_cast<long long>(walk.nblk - walk.blk0), walk.end - walk.pos));
+    if (walk.blk0 == 0) flags |= walk.left == walk.nblk ? kWhole : kStart;
+    walk.runs = static_cast<int>((walk.pos + walk.nblk - 1) / walk.size) - walk.index + 1;
+  }
+  seg.b = walk.b;
+  seg.blk0 = walk.blk0;
+  seg.nb = min(walk.left, kTable);
+  seg.runs = walk.runs;
+  walk.left -= seg.nb;
+  walk.blk0 += seg.nb;
+  walk.pos += seg.nb;
+  seg.tail = walk.blk0 == walk.nblk ? walk.n - (walk.nblk - 1) * kBlockSize : kBlockSize;
+  seg.flags = flags | (walk.left == 0 ? kMerge : 0);
+  walk.flags = walk.left == 0 ? kLater : flags;
 }
 
 template <class Path>
-__global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodeParams p) {
-  using namespace dev;
-  constexpr int S = Path::kS;
+constexpr size_t int4_smem() {
+  return static_cast<size_t>(Path::kS) * Path::kStageBytes + Path::kMergeFloats * sizeof(float) +
+         2 * kTable * sizeof(int32_t);
+}
+
+// part_blocks > 0: grid (partitions, units, requests), one run per CTA.
+// part_blocks == 0: balanced, grid units * pieces.
+template <class Path>
+__global__ void __launch_bounds__(kWarps * 32, 3) decode_int4_kernel(const DecodeParams p) {
+  constexpr int D = Path::kD, H = Path::kHeads;
   constexpr int kCB = Path::kCodeBytes, kPB = Path::kPairBytes, kSB = Path::kStageBytes;
-  extern __shared__ uint8_t smem_raw[];
-  DecodeSmem sm;
-  sm.stages = align1024(smem_raw);
-  sm.scales = nullptr;
-  sm.bars = reinterpret_cast<uint64_t*>(sm.stages + S * kSB);
-  sm.tbl = reinterpret_cast<int32_t*>(sm.bars + S);
-  __shared__ int cta_flag;
+  constexpr int kPieces = kCB / 16;  // 16-byte pieces of a block's K (or V) codes
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + Path::kS * kSB);
+  int32_t* tables = reinterpret_cast<int32_t*>(merge + Path::kMergeFloats);
+  __shared__ Walk walk;
+  __shared__ Segment segs[4];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const bool balanced = p.part_blocks == 0;
+  const int units = p.num_kv_heads * p.qgroups;
+  const int unit = balanced ? blockIdx.x % units : blockIdx.y;
+  const int kvh = unit / p.qgroups;
+  const int head0 = kvh * p.group + unit % p.qgroups * p.heads_per_cta;
+  const int nheads = min(p.heads_per_cta, p.group - unit % p.qgroups * p.heads_per_cta);
 
-  DecodeCta c;
-  bool any_bad = false;
-  if (!decode_prologue<Path>(p, sm, c, &any_bad, [&] {
-        cta_flag = 0;
-#pragma unroll
-        for (int s = 0; s < S; ++s) mbar_init(smem_addr(sm.bars + s), 1);
-      }))
-    return;
+  dev::grid_dependency_wait();
+  if (balanced) {
+    // requests without tokens, or with a bad length
+    const int pieces = gridDim.x / units, index = blockIdx.x / units;
+    for (int b = index; b < p.batch; b += pieces) {
+      const int n = p.context_lens[b];
+      if (blocks_of(p, n) == 0) {
+        zero_rows<D>(p, b, head0, nheads);
+        if (n != 0 && threadIdx.x == 0) dev::set_status(p.status, kErrBadBlock);
+      }
+    }
+    if (threadIdx.x == 0) p.notes[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (!find_piece(p, index, pieces, walk)) return;
+  } else {
+    const int b = blockIdx.z, n = p.context_lens[b], nblk = blocks_of(p, n);
+    const int blk0 = blockIdx.x * p.part_blocks;
+    if (nblk == 0 && blk0 == 0) {
+      zero_rows<D>(p, b, head0, nheads);
+      if (n != 0 && threadIdx.x == 0) dev::set_status(p.status, kErrBadBlock);
+    }
+    if (blk0 >= nblk) return;
+    if (threadIdx.x == 0) {
+      walk.pos = 0;
+      walk.end = min(p.part_blocks, nblk - blk0);
+      walk.size = 1;
+      walk.b = b;
+      walk.n = n;
+      walk.nblk = nblk;
+      walk.blk0 = blk0;
+      walk.index = walk.left = walk.flags = 0;
+    }
+  }
+  if (threadIdx.x == 0) {
+    next_segment(p, walk, segs[0]);
+    next_segment(p, walk, segs[1]);
+  }
+  __syncthreads();
 
-  // lanes 0-3 of the warp: fetch the warp's j-th block, one copy each
-  const uint8_t* src = static_cast<const uint8_t*>(
-      lane == 0 ? p.k_pool : lane == 1 ? p.v_pool : lane == 2 ? p.k_sz : p.v_sz);
-  const uint32_t bytes = lane < 2 ? kCB : kPB;
-  const uint32_t at = lane < 2 ? lane * kCB : 2 * kCB + (lane - 2) * kPB;
-  auto issue = [&](int j) {
-    const int stage = warp * kInt4Stages + (j % kInt4Stages);
-    const uint32_t bar = smem_addr(sm.bars + stage);
-    const size_t tile = static_cast<size_t>(sm.tbl[warp + j * kWarps]) * p.num_kv_heads + c.kvh;
-    if (lane == 0) mbar_arrive_expect_tx(bar, kSB);
-    __syncwarp();
-    if (lane < 4) bulk_load(smem_addr(sm.stages + stage * kSB) + at, src + tile * bytes, bytes, bar);
+  // This lane's pieces of a block: K and V codes lane, lane + 32, ..., and one
+  // of the pairs' pieces on the first lanes.
+  constexpr int kPairPieces = kPB / 16;
+  const bool is_v = lane >= kPairPieces;
+  uint8_t* ring = smem + warp * kInt4Stages * kSB;
+  constexpr int kRowPieces = D / 32;
+  const uint32_t code_at =
+      dev::smem_addr(ring) + code_piece<D>(lane / kRowPieces, lane % kRowPieces);
+  const uint32_t pair_at = dev::smem_addr(ring) + 2 * kCB + lane * 16;
+  const uint8_t* kc = static_cast<const uint8_t*>(p.k_pool) + lane * 16;
+  const uint8_t* vc = static_cast<const uint8_t*>(p.v_pool) + lane * 16;
+  const uint8_t* pairs = static_cast<const uint8_t*>(is_v ? p.v_sz : p.k_sz) +
+                         (lane - (is_v ? kPairPieces : 0)) * 16;
+  constexpr int kStride = kStep * kWarps, kStepBytes = kStep * kSB;
+
+  // A segment's slice of the block table comes on chip during the segment
+  // before ("踩坑一"), entry by entry; each thread checks those it fetched.
+  auto fetch_table = [&](int s) {
+    const Segment& seg = segs[s & 3];
+    const int32_t* row =
+        p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks + seg.blk0;
+    const uint32_t to = dev::smem_addr(tables + (s & 1) * kTable);
+    for (int i = threadIdx.x; i < seg.nb; i += blockDim.x) cp_async4(to + i * 4, row + i);
+  };
+  auto table_bad = [&](int s) {
+    bool bad = false;
+    for (int i = threadIdx.x; i < segs[s & 3].nb; i += blockDim.x) {
+      const int id = tables[(s & 1) * kTable + i];
+      bad |= id < 0 || id >= p.num_blocks;
+    }
+    return bad;
   };
 
+  fetch_table(0);
+  cp_async_commit();
+  cp_async_wait<0>();
+  bool bad = __syncthreads_or(table_bad(0)) != 0;  // of this segment's table
+  bool run_bad = false;                            // of the run
   typename Path::State st;
-  bool ok = !any_bad;
-  if (ok) {
-    Path::init(st, p, c.b, c.head0, c.nheads, lane);
-    const int my_blocks = c.nb > warp ? (c.nb - warp + kWarps - 1) / kWarps : 0;
-    const int prologue = my_blocks < kInt4Stages ? my_blocks : kInt4Stages;
-    for (int j = 0; j < prologue; ++j) issue(j);
-    int issued = prologue;
-    int j = 0;
-    for (; j < my_blocks; ++j) {
-      const int stage = warp * kInt4Stages + (j % kInt4Stages);
-      const bool landed = mbar_wait_bounded(smem_addr(sm.bars + stage), (j / kInt4Stages) & 1);
-      if (!__all_sync(0xffffffffu, landed)) {
-        ok = false;
-        break;
-      }
-      const int i = warp + j * kWarps;
-      const int valid = (c.last_part && i == c.nb - 1) ? c.tail_valid : kBlockSize;
-      Path::consume(st, sm.stages + stage * kSB, valid, lane);
-      __syncwarp();
-      if (j + kInt4Stages < my_blocks) {
-        fence_proxy_async_smem();
-        issue(j + kInt4Stages);
-        ++issued;
-      }
-    }
-    if (!ok) {
-      // A transfer did not land in time: wait (bounded) for this warp's copies
-      // still in flight so no copy outlives the CTA, then report.
-      if (lane == 0) {
-        for (int jj = j; jj < issued; ++jj) {
-          const int stage = warp * kInt4Stages + (jj % kInt4Stages);
-          mbar_wait_bounded(smem_addr(sm.bars + stage), (jj / kInt4Stages) & 1);
+  int done_flags = 0, done_b = 0, done_runs = 0;   // of the segment before
+  for (int s = 0;; ++s) {
+    const Segment& seg = segs[s & 3];
+    const int nb = seg.nb;
+    const int32_t* tbl = tables + (s & 1) * kTable;
+    auto issue_step = [&](int i, int at) {  // table entries i, i + 4 to byte `at` of the ring
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+        if (i + b * kWarps < nb) {
+          const uint32_t tile = static_cast<uint32_t>(tbl[i + b * kWarps]) * p.num_kv_heads + kvh;
+          const uint8_t* ks = kc + static_cast<uint64_t>(tile) * kCB;
+          const uint8_t* vs = vc + static_cast<uint64_t>(tile) * kCB;
+#pragma unroll
+          for (int x = 0; x < kPieces; x += 32) {  // (32 pieces on: 8 rows, the same swap)
+            cp_async16(code_at + at + b * kSB + x * 16, ks + x * 16);
+            cp_async16(code_at + at + b * kSB + kCB + x * 16, vs + x * 16);
+          }
+          if (lane < 2 * kPairPieces)
+            cp_async16(pair_at + at + b * kSB, pairs + static_cast<uint64_t>(tile) * kPB);
         }
-        set_status(p.status, kErrTimeout);
-        atomicExch(&cta_flag, 1);
+      }
+      cp_async_commit();
+    };
+    // ---- the first blocks, the next table and the query set out ...
+    typename Path::Query query;
+    if (nb > 0) {
+      fetch_table(s + 1);
+      if (!bad) {
+#pragma unroll
+        for (int b = 0; b < kBuf - 1; ++b) issue_step(warp + b * kStride, b * kStepBytes);
+      } else {
+        cp_async_commit();
+      }
+      if (seg.flags & kInit) Path::load_query(query, p, seg.b, head0, nheads, lane);
+    }
+    // ---- ... while the run before is merged over the warps
+    if (done_flags & kMerge) {
+      const size_t row0 = static_cast<size_t>(done_b) * p.num_q_heads + head0;
+      if (threadIdx.x < 32 * Path::kParts) {
+        float o[8], M, L;
+        int hh, d;
+        Path::merge8(merge, threadIdx.x, o, M, L, hh, d);
+        if (run_bad) L = -1.f;  // marks a failed run
+        if (hh >= nheads) {
+          // (a column without a query head)
+        } else if (done_flags & kWhole) {
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = L > 0.f ? o[2 * e] * inv : 0.f, y = L > 0.f ? o[2 * e + 1] * inv : 0.f;
+            w[e] = p.q_bf16 ? dev::pack2<true>(x, y) : dev::pack2<false>(x, y);
+          }
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row0 + hh) * D + d) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          const size_t prow =
+              balanced ? (static_cast<size_t>(blockIdx.x) * 2 + (done_flags & kLater ? 1 : 0)) * H +
+                             hh
+                       : (row0 + hh) * p.max_parts + blockIdx.x;
+          float4* to = reinterpret_cast<float4*>(p.ws_o + prow * D + d);
+          to[0] = make_float4(o[0], o[1], o[2], o[3]);
+          to[1] = make_float4(o[4], o[5], o[6], o[7]);
+          if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * prow) = make_float2(M, L);
+        }
+      }
+      if (balanced && (done_flags & kStart) && threadIdx.x == 0)
+        p.notes[blockIdx.x] =
+            make_int4(static_cast<int>(row0), nheads, done_runs, done_flags & kLater ? 1 : 0);
+      run_bad = false;
+    }
+    if (nb == 0) break;
+    if (threadIdx.x == 0) next_segment(p, walk, segs[(s + 2) & 3]);
+    if (seg.flags & kInit) Path::init(st, query, p.scale_log2, lane);
+
+    // ---- the segment's blocks
+    run_bad |= bad;
+    if (!bad) {
+      const int tail = seg.tail;
+      const bool init = (seg.flags & kInit) != 0;
+      int at = 0, next = (kBuf - 1) * kStepBytes;
+      for (int i = warp; i < nb; i += kStride) {
+        cp_async_wait<kBuf - 2>();
+        __syncwarp();  // the step has landed; its predecessor's stages are read
+        issue_step(i + (kBuf - 1) * kStride, next);
+        const int have = min(kStep, (nb - i + kWarps - 1) / kWarps);
+        int valid = kBlockSize * have;
+        if (i + (have - 1) * kWarps == nb - 1) valid += tail - kBlockSize;
+        const bool first = init && i == warp;
+        if (valid == kBlockSize * kStep)
+          Path::template consume<false>(st, ring + at, valid, first, lane);
+        else
+          Path::template consume<true>(st, ring + at, valid, first, lane);
+        at = at == (kBuf - 1) * kStepBytes ? 0 : at + kStepBytes;
+        next = next == (kBuf - 1) * kStepBytes ? 0 : next + kStepBytes;
+      }
+    } else if (threadIdx.x == 0) {
+      dev::set_status(p.status, kErrBadBlock);
+    }
+    done_flags = seg.flags;
+    done_b = seg.b;
+    done_runs = seg.runs;
+    cp_async_wait<0>();
+    if (done_flags & kMerge) {
+      __syncthreads();  // the merge before this one has been read
+      Path::finalize(st, merge, warp, lane);
+    }
+    bad = __syncthreads_or(table_bad(s + 1)) != 0;
+  }
+  dev::launch_dependents();
+}
+
+// Merge of the cut contexts: block i takes the one that CTA i started, kSplit
+// warps per head; the rest of it are the first runs (slot 0) of the unit's next
+// pieces.  note: first output row, heads, runs, slot of the first run.
+template <int D, bool kBf16Out, int kSplit>
+__global__ void __launch_bounds__(kSplit * 8 * 32) merge_int4_kernel(const DecodeParams p) {
+  constexpr int E = D / 32, H = 8;
+  __shared__ float s_o[kSplit > 1 ? H : 1][kSplit > 1 ? kSplit : 1][kSplit > 1 ? D : 1];
+  __shared__ float2 s_ml[H][kSplit];
+  dev::grid_dependency_wait();
+  dev::launch_dependents();
+  const int4 note = p.notes[blockIdx.x];
+  if (note.x < 0) return;
+  const int lane = threadIdx.x & 31, hh = (threadIdx.x >> 5) / kSplit,
+            sub = (threadIdx.x >> 5) % kSplit;
+  const int first = blockIdx.x, runs = note.z, units = p.num_kv_heads * p.qgroups;
+  float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  bool bad = false;
+  if (hh < note.y) {
+#pragma unroll 4
+    for (int i = sub; i < runs; i += kSplit) {
+      const size_t prow =
+          (static_cast<size_t>(first + i * units) * 2 + (i == 0 ? note.w : 0)) * H + hh;
+      const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * prow);
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(p.ws_o + prow * D + lane * E);
+        x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(p.ws_o + prow * D + lane * E);
+        x[0] = t.x, x[1] = t.y;
+      }
+      bad |= v.y < 0.f;  // a failed run
+      const float mn = fmaxf(M, v.x);
+      const float f0 = exp2f(M - mn), f1 = exp2f(v.x - mn);
+      M = mn;
+      L = fmaf(L, f0, f1 * v.y);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f0, f1 * x[e]);
+    }
+  }
+  if constexpr (kSplit > 1) {
+    if (lane == 0) s_ml[hh][sub] = make_float2(M, bad ? -1.f : L);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[hh][sub][lane * E + e] = acc[e];
+    __syncthreads();
+    if (sub != 0) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kSplit; ++w) {
+      bad |= s_ml[hh][w].y < 0.f;
+      if (s_ml[hh][w].y > 0.f) M = fmaxf(M, s_ml[hh][w].x);
+    }
+    L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSplit; ++w) {
+      if (s_ml[hh][w].y > 0.f) {
+        const float f = exp2f(s_ml[hh][w].x - M);
+        L = fmaf(f, s_ml[hh][w].y, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, s_o[hh][w][lane * E + e], acc[e]);
       }
     }
-  } else if (threadIdx.x == 0) {
-    set_status(p.status, kErrBadBlock);
   }
-
-  launch_dependents();
-  __syncthreads();
-  decode_epilogue<Path>(p, sm, c, st, any_bad || cta_flag != 0);
+  if (hh >= note.y) return;
+  const float inv = !bad && L > 0.f ? 1.f / L : 0.f;
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e)
+    w[e] = inv > 0.f ? dev::pack2<kBf16Out>(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + (static_cast<size_t>(note.x) + hh) * D + lane * E;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = w[0];
 }
 
 template <class Path>
 cudaError_t launch_int4(const DecodeParams& p, int grid_x, cudaStream_t s) {
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(&decode_int4_kernel<Path>),
-                                         int4_smem_for<Path>(kMaxPartBlocks));
+  constexpr size_t smem = int4_smem<Path>();
+  const cudaError_t e =
+      ensure_smem_attr(reinterpret_cast<const void*>(&decode_int4_kernel<Path>), smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(grid_x, p.num_kv_heads * p.qgroups, p.batch);
-  return launch_pdl(decode_int4_kernel<Path>, grid, dim3(kWarps * 32),
-                    int4_smem_for<Path>(p.part_blocks), s, p);
+  const dim3 grid = p.part_blocks == 0 ? dim3(grid_x)
+                                       : dim3(grid_x, p.num_kv_heads * p.qgroups, p.batch);
+  return launch_pdl(decode_int4_kernel<Path>, grid, dim3(kWarps * 32), smem, s, p);
 }
 
 }  // namespace
@@ -473,6 +933,23 @@ cudaError_t launch_decode_int4(const DecodeParams& p, int grid_x, cudaStream_t s
   if (bf && p.head_dim == 64) return launch_int4<Int4Path<true, 64>>(p, grid_x, s);
   if (bf && p.head_dim == 128) return launch_int4<Int4Path<true, 128>>(p, grid_x, s);
   return cudaErrorInvalidValue;
+}
+
+template <int kSplit>
+static cudaError_t launch_merge(const DecodeParams& p, int grid_x, cudaStream_t s) {
+  const dim3 grid(grid_x), block(kSplit * 8 * 32);
+  if (p.head_dim == 64)
+    return p.q_bf16 ? launch_pdl(merge_int4_kernel<64, true, kSplit>, grid, block, 0, s, p)
+                    : launch_pdl(merge_int4_kernel<64, false, kSplit>, grid, block, 0, s, p);
+  return p.q_bf16 ? launch_pdl(merge_int4_kernel<128, true, kSplit>, grid, block, 0, s, p)
+                  : launch_pdl(merge_int4_kernel<128, false, kSplit>, grid, block, 0, s, p);
+}
+
+cudaError_t launch_decode_int4_merge(const DecodeParams& p, int grid_x, cudaStream_t s) {
+  // A context spans pieces / batch runs when all are alike: from 8 on, four
+  // warps share a head.
+  const int pieces = grid_x / (p.num_kv_heads * p.qgroups);
+  return pieces >= 8 * p.batch ? launch_merge<4>(p, grid_x, s) : launch_merge<1>(p, grid_x, s);
 }
 
 }  // namespace kvp

@@ -64,7 +64,11 @@ struct DecodeParams {
                                 // partitions cover [skip, n) and are written as 1, 2, ...
   const void* k_sz;             // 4-bit pools: (scale, zero) pairs [NB, Hkv, bs, D / 64, 2]
   const void* v_sz;
+  int4* notes;                  // 4-bit balanced decode (part_blocks == 0): one per CTA
 };
+
+// CTAs of the balanced 4-bit decode: 3 on each of GB300's 152 SMs.
+constexpr int kInt4Ctas = 152 * 3;
 
 // Everything the row kernels (rotary positions, 4-bit quantisation, scatter)
 // need.  Strides are elements from one token to the next.
@@ -173,8 +177,10 @@ cudaError_t launch_decode_mma_fp8(const DecodeParams& p, const DecodeMaps& m, in
 // FP8 pools, head_dim 128, on tcgen05 (kind::f8f6f4); per-block 2-D pool maps.
 cudaError_t launch_decode_fp8_umma(const DecodeParams& p, const CUtensorMap& tk,
                                    const CUtensorMap& tv, int grid_x, cudaStream_t s);
-// 4-bit pools (codes in k_pool / v_pool, pairs in k_sz / v_sz).
+// 4-bit pools (codes in k_pool / v_pool, pairs in k_sz / v_sz); part_blocks == 0:
+// balanced over grid_x CTAs, whose cut units the second launch merges.
 cudaError_t launch_decode_int4(const DecodeParams& p, int grid_x, cudaStream_t s);
+cudaError_t launch_decode_int4_merge(const DecodeParams& p, int grid_x, cudaStream_t s);
 cudaError_t launch_decode_reduce(const DecodeParams& p, cudaStream_t s);
 // Self-test of the bounded wait: one block waits on a barrier nothing arrives
 // on, for at most limit_ns, and records kErrTimeout when it gives up.

@@ -25,11 +25,19 @@ def desc(nb=64, kv=2, bs=16, d=128):
 
 def test_sizing_of_the_4_bit_decode(lib):
     d = desc(40000, 8)
-    pb = kvp.kvp_decode_partition_blocks(4, 64, d, 8192, kv_int4=True)
-    assert 16 <= pb <= 1024
-    parts = -(-8192 // pb)
-    assert kvp.kvp_decode_workspace_bytes(4, 64, d, 8192, kv_int4=True) == \
-        4 * 64 * parts * (128 + 2) * 4
+    # the automatic split is balanced: a number of pieces that the heads alone
+    # decide, for each kv head two partial states of 8 heads and a 16-byte note
+    per = 8 * (2 * 8 * (128 + 2) * 4 + 16)
+    n = kvp.kvp_decode_workspace_bytes(4, 64, d, 8192, kv_int4=True)
+    assert n % per == 0 and n > 0
+    assert n == kvp.kvp_decode_workspace_bytes(64, 64, d, 512, kv_int4=True)
+    run = kvp.kvp_decode_partition_blocks(4, 64, d, 8192, kv_int4=True)
+    assert run == -(-4 * 8192 // (n // per))
+    # given partitions, and tables short enough for a single pass
+    assert kvp.kvp_decode_workspace_bytes(4, 64, d, 8192, 512, kv_int4=True) == \
+        4 * 64 * 16 * (128 + 2) * 4
+    assert kvp.kvp_decode_workspace_bytes(4, 64, d, 16, kv_int4=True) == 0
+    assert kvp.kvp_decode_partition_blocks(4, 64, d, 16, kv_int4=True) == 16
     for kind in (3, 5, -1):
         assert lib.kvp_decode_workspace_bytes(4, 64, d, 8192, 0, kind) == 0
         assert lib.kvp_decode_partition_blocks(4, 64, d, 8192, kind) == 0
@@ -134,21 +142,21 @@ def test_tables(lib):
 class Fake:
     """Just enough of a tensor on some GPU for the binding's checks."""
 
-    def __init__(self, device, cuda=True):
-        self.is_cuda, self._d = cuda, device
+    def __init__(self, device):
+        self._d = device
 
     def get_device(self):
         return self._d
 
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     with pytest.raises(ValueError, match="one call"):
         kvp._on_one_device(None, Fake(0), None, Fake(1))
     with pytest.raises(ValueError, match="current device"):
         kvp._on_one_device(None, Fake(1), Fake(1))
     with pytest.raises(ValueError, match="CUDA tensors"):
-        kvp._on_one_device(None, Fake(0), Fake(-1, cuda=False))
+        kvp._on_one_device(None, Fake(0), Fake(-1))
 
     class S:
         device_index, cuda_stream = 1, 5
