@@ -132,10 +132,6 @@ struct DecodeShape {
   size_t ws_bytes;
 };
 
-// 4-bit contexts of up to 16 blocks take one CTA per unit and no merge: the
-// second launch costs more than the split saves there.
-constexpr int kInt4SinglePass = 16;
-
 // Split-context rule.  Each (request, kv head, query group) unit is cut into
 // `parts` partitions of ceil(MB / parts) blocks, run as independent CTAs on
 // GB300's 152 SMs (3 resident decode CTAs per SM for 16-bit tiles, 4 for INT8
@@ -149,11 +145,16 @@ constexpr int kInt4SinglePass = 16;
 constexpr int kSms = 152;
 constexpr double kCtaOverheadBlocks = 4.0;
 constexpr double kReduceCostBlocks = 2.0;
+// 4-bit tables of up to 64 blocks: one CTA per (request, unit) and no merge.  The
+// second launch and the lengths' scan cost 3 us, and a run's start and end in the
+// middle of a piece about 3 more (128 requests of 64 to 1024 tokens, 8 kv heads,
+// head_dim 64: 20 us in one pass, 24 balanced).
+constexpr int kInt4SinglePass = 64;
 
 int resident_ctas(DecodePath path) {
   switch (path) {
     case DecodePath::kMmaInt8: return 4;
-    case DecodePath::kInt4: return 3;
+    case DecodePath::kInt4: return int4_ctas_per_sm(128);
     case DecodePath::kUmmaFp8: return 2;
     default: return 3;
   }
@@ -213,7 +214,7 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
     // balanced: equal pieces of all contexts, a CTA per piece and unit of a
     // request; two partial states of up to 8 heads per CTA and a note
     const int per_request = c.num_kv_heads * s.qgroups;
-    const int pieces = std::max(1, kInt4Ctas / per_request);
+    const int pieces = std::max(1, kSms * int4_ctas_per_sm(c.head_dim) / per_request);
     const long long even = (static_cast<long long>(batch) * max_blocks + pieces - 1) / pieces;
     s.part_blocks = 0;
     s.run_blocks = static_cast<int>(std::min<long long>(std::max(even, 8ll), max_blocks));
@@ -224,7 +225,9 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
     *out = s;
     return KVP_OK;
   }
-  int pb = partition_blocks > 0 ? partition_blocks : auto_partition(s.path, units, max_blocks);
+  int pb = partition_blocks > 0             ? partition_blocks
+           : s.path == DecodePath::kInt4 ? max_blocks
+                                         : auto_partition(s.path, units, max_blocks);
   if (pb >= max_blocks) pb = max_blocks;
   if (pb > kMaxPartBlocks) return KVP_ERR_UNSUPPORTED;  // one partition must fit on chip
   s.part_blocks = pb;

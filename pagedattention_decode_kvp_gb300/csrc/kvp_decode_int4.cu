@@ -51,11 +51,11 @@
 namespace kvp {
 namespace {
 
-constexpr int kStep = 2;                    // blocks a warp takes at a time
-constexpr int kBuf = 3;                     // steps per warp: one in use, two on the way
+constexpr int kStep = 2;  // blocks a warp takes at a time
+constexpr int kBuf = 2;   // steps per warp: one in use, one on the way
 constexpr int kInt4Stages = kStep * kBuf;   // blocks
 constexpr int kTable = 512;                 // table entries of a segment
-constexpr int kMinRun = 8;                  // blocks a balanced CTA takes at least
+constexpr int kMinRun = kStep * kWarps;      // blocks of a piece at least: a step of every warp
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -88,7 +88,7 @@ template <bool kBf16, int D>
 struct Int4Path {
   static constexpr int kD = D;
   static constexpr int kHeads = 8;
-  static constexpr int kElemBytes = 1;  // (no fused append)
+  static constexpr int kCtas = int4_ctas_per_sm(D);
   static constexpr int kGroups = D / 64;
   static constexpr int kCodeBytes = 16 * D / 2;        // K or V codes of a block
   static constexpr int kPairBytes = 16 * kGroups * 4;  // their (s, z) pairs
@@ -100,7 +100,6 @@ struct Int4Path {
   static constexpr uint32_t kOnes = 0x3c003c00u;
 
   struct State {
-    uint32_t qb[kGroups][4][2];  // q operand per k-step
     float o[kGroups][4][4];      // 2^-24 sum a c (0, 1) and 2^-20 sum a c (2, 3)
     float as[kGroups][2];        // sum a
     float zo[kGroups][2];        // sum P (z + 7.5 s), this lane's tokens
@@ -137,8 +136,13 @@ struct Int4Path {
     }
   }
 
+  // The query operand of the K product lives in shared memory, a copy per warp:
+  // for each group and pair of k-steps 4 words per lane.  (In registers it took
+  // the step loop over the 168 that three CTAs leave.)
+  static constexpr int kQueryBytes = kGroups * 2 * 32 * 16;
+
   __device__ __forceinline__ static void init(State& st, const Query& x, float scale_log2,
-                                              int lane) {
+                                              uint4* qs, int lane) {
     const int t4 = lane & 3;
     float big = 0.f;
 #pragma unroll
@@ -156,10 +160,10 @@ struct Int4Path {
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
     const float kappa = big > 0.f ? pow2_to(big, 10) : 1.f;
-    float qs[kGroups];
+    float qsum[kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      qs[g] = 0.f;
+      qsum[g] = 0.f;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint32_t r[4] = {x.raw[g][w].x, x.raw[g][w].y, x.raw[g][w].z, x.raw[g][w].w};
@@ -172,17 +176,16 @@ struct Int4Path {
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          qs[g] += v[e];
+          qsum[g] += v[e];
           v[e] *= kappa;
         }
         // the word's code pairs are (0, 4), 16 (1, 5), (2, 6), 16 (3, 7)
-        st.qb[g][2 * w][0] = dev::pack2<false>(16.f * v[0], 16.f * v[4]);
-        st.qb[g][2 * w][1] = dev::pack2<false>(v[1], v[5]);
-        st.qb[g][2 * w + 1][0] = dev::pack2<false>(16.f * v[2], 16.f * v[6]);
-        st.qb[g][2 * w + 1][1] = dev::pack2<false>(v[3], v[7]);
+        qs[(2 * g + w) * 32 + lane] =
+            make_uint4(dev::pack2<false>(16.f * v[0], 16.f * v[4]), dev::pack2<false>(v[1], v[5]),
+                       dev::pack2<false>(16.f * v[2], 16.f * v[6]), dev::pack2<false>(v[3], v[7]));
       }
-      qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 1);
-      qs[g] += __shfl_xor_sync(0xffffffffu, qs[g], 2);
+      qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 1);
+      qsum[g] += __shfl_xor_sync(0xffffffffu, qsum[g], 2);
     }
     // this lane's score columns are heads 2 t4 and 2 t4 + 1
 #pragma unroll
@@ -191,7 +194,7 @@ struct Int4Path {
       st.f[i] = scale_log2 * 1048576.f / __shfl_sync(0xffffffffu, kappa, src);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        st.qz[g][i] = scale_log2 * __shfl_sync(0xffffffffu, qs[g], src);
+        st.qz[g][i] = scale_log2 * __shfl_sync(0xffffffffu, qsum[g], src);
         st.zo[g][i] = 0.f;
       }
       st.r[i] = 0.f;
@@ -227,65 +230,82 @@ struct Int4Path {
     }
   }
 
-  // Scores of one block relative to the present reference (v = u - r) of this
-  // lane's rows g8, g8 + 8 and heads 2 t4, 2 t4 + 1, and V's pairs of those
+  // Scores of a step's blocks relative to the present reference (v = u - r) of
+  // this lane's rows g8, g8 + 8 and heads 2 t4, 2 t4 + 1, and V's pairs of those
   // tokens.  kTail: only the first `valid` tokens count (other slots may hold
   // anything).
   template <bool kTail>
-  __device__ __forceinline__ static void scores(const State& st, const uint8_t* tile, int valid,
-                                                int lane, float (&v)[4], float (&s0)[kGroups],
-                                                float (&z0)[kGroups], float (&s1)[kGroups],
-                                                float (&z1)[kGroups]) {
+  __device__ __forceinline__ static void scores(const State& st, const uint4* qs,
+                                                const uint8_t* tile, int valid, int lane,
+                                                float (&v)[kStep][4], float (&s0)[kStep][kGroups],
+                                                float (&z0)[kStep][kGroups],
+                                                float (&s1)[kStep][kGroups],
+                                                float (&z1)[kStep][kGroups]) {
     const int g8 = lane >> 2, t4 = lane & 3;
     const int tok0 = 4 * (g8 & 1) + (g8 >> 1), tok1 = tok0 + 8;
-    float ks0[kGroups], kz0[kGroups], ks1[kGroups], kz1[kGroups];
-    load_pairs(tile + 2 * kCodeBytes, tok0, ks0, kz0);
-    load_pairs(tile + 2 * kCodeBytes, tok1, ks1, kz1);
-    float us[4] = {0.f, 0.f, 0.f, 0.f};
-    v[0] = v[2] = -st.r[0];
-    v[1] = v[3] = -st.r[1];
+    float acc[kStep][kGroups][4];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int at = code_piece<D>(tok0, 2 * g + (t4 >> 1)) + 8 * (t4 & 1);
-      const uint2 a = *reinterpret_cast<const uint2*>(tile + at);
-      const uint2 b = *reinterpret_cast<const uint2*>(tile + at + 8 * (D / 2));
-      const uint32_t wa[2] = {a.x, a.y}, wb[2] = {b.x, b.y};
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t wa[kStep][2], wb[kStep][2];
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+        const uint2 x = *reinterpret_cast<const uint2*>(tile + b * kStageBytes + at);
+        const uint2 y =
+            *reinterpret_cast<const uint2*>(tile + b * kStageBytes + at + 8 * (D / 2));
+        wa[b][0] = x.x, wa[b][1] = x.y, wb[b][0] = y.x, wb[b][1] = y.y;
+        acc[b][g][0] = acc[b][g][1] = acc[b][g][2] = acc[b][g][3] = 0.f;
+      }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t x = wa[w], y = wb[w], xs = x >> 8, ys = y >> 8;
-        dev::mma16816<false>(acc, x & kLow, y & kLow, x & kHigh, y & kHigh, st.qb[g][2 * w][0],
-                             st.qb[g][2 * w][1]);
-        dev::mma16816<false>(acc, xs & kLow, ys & kLow, xs & kHigh, ys & kHigh,
-                             st.qb[g][2 * w + 1][0], st.qb[g][2 * w + 1][1]);
+        const uint4 q = qs[(2 * g + w) * 32 + lane];
+#pragma unroll
+        for (int b = 0; b < kStep; ++b) {
+          const uint32_t x = wa[b][w], y = wb[b][w], xs = x >> 8, ys = y >> 8;
+          dev::mma16816<false>(acc[b][g], x & kLow, y & kLow, x & kHigh, y & kHigh, q.x, q.y);
+          dev::mma16816<false>(acc[b][g], xs & kLow, ys & kLow, xs & kHigh, ys & kHigh, q.z, q.w);
+        }
       }
-      us[0] = fmaf(ks0[g], acc[0], us[0]);
-      us[1] = fmaf(ks0[g], acc[1], us[1]);
-      us[2] = fmaf(ks1[g], acc[2], us[2]);
-      us[3] = fmaf(ks1[g], acc[3], us[3]);
-      v[0] = fmaf(kz0[g], st.qz[g][0], v[0]);
-      v[1] = fmaf(kz0[g], st.qz[g][1], v[1]);
-      v[2] = fmaf(kz1[g], st.qz[g][0], v[2]);
-      v[3] = fmaf(kz1[g], st.qz[g][1], v[3]);
     }
-    v[0] = fmaf(us[0], st.f[0], v[0]);
-    v[1] = fmaf(us[1], st.f[1], v[1]);
-    v[2] = fmaf(us[2], st.f[0], v[2]);
-    v[3] = fmaf(us[3], st.f[1], v[3]);
-    load_pairs(tile + 2 * kCodeBytes + kPairBytes, tok0, s0, z0);
-    load_pairs(tile + 2 * kCodeBytes + kPairBytes, tok1, s1, z1);
-    if constexpr (kTail) {
-      const bool in0 = tok0 < valid, in1 = tok1 < valid;
-      v[0] = in0 ? v[0] : -INFINITY;
-      v[1] = in0 ? v[1] : -INFINITY;
-      v[2] = in1 ? v[2] : -INFINITY;
-      v[3] = in1 ? v[3] : -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kStep; ++b) {
+      const uint8_t* pairs = tile + b * kStageBytes + 2 * kCodeBytes;
+      float ks0[kGroups], kz0[kGroups], ks1[kGroups], kz1[kGroups];
+      load_pairs(pairs, tok0, ks0, kz0);
+      load_pairs(pairs, tok1, ks1, kz1);
+      float us[4] = {0.f, 0.f, 0.f, 0.f};
+      v[b][0] = v[b][2] = -st.r[0];
+      v[b][1] = v[b][3] = -st.r[1];
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        s0[g] = in0 ? s0[g] : 0.f;
-        z0[g] = in0 ? z0[g] : 0.f;
-        s1[g] = in1 ? s1[g] : 0.f;
-        z1[g] = in1 ? z1[g] : 0.f;
+        us[0] = fmaf(ks0[g], acc[b][g][0], us[0]);
+        us[1] = fmaf(ks0[g], acc[b][g][1], us[1]);
+        us[2] = fmaf(ks1[g], acc[b][g][2], us[2]);
+        us[3] = fmaf(ks1[g], acc[b][g][3], us[3]);
+        v[b][0] = fmaf(kz0[g], st.qz[g][0], v[b][0]);
+        v[b][1] = fmaf(kz0[g], st.qz[g][1], v[b][1]);
+        v[b][2] = fmaf(kz1[g], st.qz[g][0], v[b][2]);
+        v[b][3] = fmaf(kz1[g], st.qz[g][1], v[b][3]);
+      }
+      v[b][0] = fmaf(us[0], st.f[0], v[b][0]);
+      v[b][1] = fmaf(us[1], st.f[1], v[b][1]);
+      v[b][2] = fmaf(us[2], st.f[0], v[b][2]);
+      v[b][3] = fmaf(us[3], st.f[1], v[b][3]);
+      load_pairs(pairs + kPairBytes, tok0, s0[b], z0[b]);
+      load_pairs(pairs + kPairBytes, tok1, s1[b], z1[b]);
+      if constexpr (kTail) {
+        const bool in0 = tok0 < valid - 16 * b, in1 = tok1 < valid - 16 * b;
+        v[b][0] = in0 ? v[b][0] : -INFINITY;
+        v[b][1] = in0 ? v[b][1] : -INFINITY;
+        v[b][2] = in1 ? v[b][2] : -INFINITY;
+        v[b][3] = in1 ? v[b][3] : -INFINITY;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          s0[b][g] = in0 ? s0[b][g] : 0.f;
+          z0[b][g] = in0 ? z0[b][g] : 0.f;
+          s1[b][g] = in1 ? s1[b][g] : 0.f;
+          z1[b][g] = in1 ? z1[b][g] : 0.f;
+        }
       }
     }
   }
@@ -294,14 +314,11 @@ struct Int4Path {
   // kTail: only the first `valid` of their 32 tokens count.  first: the warp's
   // first pair, which sets the reference.
   template <bool kTail>
-  __device__ __forceinline__ static void consume(State& st, const uint8_t* tile, int valid,
-                                                 bool first, int lane) {
+  __device__ __forceinline__ static void consume(State& st, const uint4* qs, const uint8_t* tile,
+                                                 int valid, bool first, int lane) {
     const int g8 = lane >> 2, t4 = lane & 3;
     float v[kStep][4], s0[kStep][kGroups], z0[kStep][kGroups], s1[kStep][kGroups], z1[kStep][kGroups];
-#pragma unroll
-    for (int b = 0; b < kStep; ++b)
-      scores<kTail>(st, tile + b * kStageBytes, valid - 16 * b, lane, v[b], s0[b], z0[b], s1[b],
-                    z1[b]);
+    scores<kTail>(st, qs, tile, valid, lane, v, s0, z0, s1, z1);
 
     // ---- weights
     float pr[kStep][4], l0, l1;
@@ -439,11 +456,15 @@ struct Int4Path {
   // outputs d = 64 g + 8 g8 ... + 7 of head 2 t4 + i as two 16-byte words, each
   // at a place of its own for all 32 lanes (no two in a bank).
   static constexpr int kParts = 2 * kGroups;  // (group, parity) pairs
-  static constexpr int kMergeFloats = kWarps * (kParts * 256 + 16);
+  // It lies in the last step's place of the warp's ring.
+  static constexpr int kMergeAt = (kBuf - 1) * kStep * kStageBytes;
+  static constexpr int kRingBytes = kInt4Stages * kStageBytes;
+  static_assert((kParts * 256 + 16) * 4 <= kStep * kStageBytes, "the state fits a step's place");
 
-  __device__ __forceinline__ static void finalize(State& st, float* merge, int warp, int lane) {
+  __device__ __forceinline__ static void finalize(State& st, uint8_t* ring, int lane) {
     const int g8 = lane >> 2, t4 = lane & 3;
-    float* ml = merge + kWarps * kParts * 256 + warp * 16;
+    float* mine = reinterpret_cast<float*>(ring + kMergeAt);
+    float* ml = mine + kParts * 256;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float l = st.l[i];
@@ -455,7 +476,7 @@ struct Int4Path {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         const float mid = 7.5f * st.as[g][i];
-        float4* at = reinterpret_cast<float4*>(merge + (warp * kParts + 2 * g + i) * 256) + lane;
+        float4* at = reinterpret_cast<float4*>(mine + (2 * g + i) * 256) + lane;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           at[32 * h] = make_float4(fmaf(st.o[g][2 * h][i], 16777216.f, -mid) + z,
@@ -472,25 +493,27 @@ struct Int4Path {
 
   // Thread `tid` of the first 32 kParts merges 8 outputs of one head: their
   // unnormalised sum, the reference M and the weight L (0 without tokens).
-  __device__ __forceinline__ static void merge8(const float* merge, int tid, float (&o)[8],
+  __device__ __forceinline__ static void merge8(const uint8_t* rings, int tid, float (&o)[8],
                                                 float& M, float& L, int& head, int& d) {
     const int part = tid >> 5, lane = tid & 31;
     head = 2 * (lane & 3) + (part & 1);
     d = 64 * (part >> 1) + 8 * (lane >> 2);
-    const float* ml = merge + kWarps * kParts * 256;
     M = -INFINITY;
     L = 0.f;
+    const float* of[kWarps];  // a warp's state
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (ml[w * 16 + 8 + head] > 0.f) M = fmaxf(M, ml[w * 16 + head]);
+    for (int w = 0; w < kWarps; ++w) {
+      of[w] = reinterpret_cast<const float*>(rings + w * kRingBytes + kMergeAt);
+      if (of[w][kParts * 256 + 8 + head] > 0.f) M = fmaxf(M, of[w][kParts * 256 + head]);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float l = ml[w * 16 + 8 + head];
-      const float f = l > 0.f ? exp2f(ml[w * 16 + head] - M) : 0.f;
+      const float l = of[w][kParts * 256 + 8 + head];
+      const float f = l > 0.f ? exp2f(of[w][kParts * 256 + head] - M) : 0.f;
       L = fmaf(f, l, L);
-      const float4* at = reinterpret_cast<const float4*>(merge + (w * kParts + part) * 256) + lane;
+      const float4* at = reinterpret_cast<const float4*>(of[w] + part * 256) + lane;
       const float4 x = at[0], y = at[32];
       const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -537,6 +560,11 @@ __device__ __forceinline__ int blocks_of(const DecodeParams& p, int n) {
   return n <= 0 || n > p.max_blocks * kBlockSize ? 0 : (n + kBlockSize - 1) / kBlockSize;
 }
 
+__device__ __forceinline__ long long piece_size(long long total, int pieces) {
+  const long long even = (total + pieces - 1) / pieces;
+  return even > kMinRun ? even : kMinRun;
+}
+
 // Sets the walk of piece `index` of `pieces`; false when it has no blocks.
 __device__ __forceinline__ bool find_piece(const DecodeParams& p, int index, int pieces,
                                            Walk& walk) {
@@ -560,9 +588,7 @@ __device__ __forceinline__ bool find_piece(const DecodeParams& p, int index, int
     if (w < warp) at += part[w];
     total += part[w];
   }
-  const long long even = (total + pieces - 1) / pieces;
-  const long long size = even > kMinRun ? even : kMinRun;
-  const long long pos = index * size;
+  const long long size = piece_size(total, pieces), pos = index * size;
   if (pos >= total) return false;
   if (at <= pos && pos < at + mine) {  // one thread's requests hold the piece's start
     int b = b0, nblk;
@@ -619,20 +645,21 @@ __device__ __forceinline__ void next_segment(const DecodeParams& p, Walk& walk, 
 
 template <class Path>
 constexpr size_t int4_smem() {
-  return static_cast<size_t>(Path::kS) * Path::kStageBytes + Path::kMergeFloats * sizeof(float) +
+  return static_cast<size_t>(Path::kS) * Path::kStageBytes + kWarps * Path::kQueryBytes +
          2 * kTable * sizeof(int32_t);
 }
 
 // part_blocks > 0: grid (partitions, units, requests), one run per CTA.
 // part_blocks == 0: balanced, grid units * pieces.
 template <class Path>
-__global__ void __launch_bounds__(kWarps * 32, 3) decode_int4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(const DecodeParams p) {
   constexpr int D = Path::kD, H = Path::kHeads;
   constexpr int kCB = Path::kCodeBytes, kPB = Path::kPairBytes, kSB = Path::kStageBytes;
   constexpr int kPieces = kCB / 16;  // 16-byte pieces of a block's K (or V) codes
   extern __shared__ __align__(128) uint8_t smem[];
-  float* merge = reinterpret_cast<float*>(smem + Path::kS * kSB);
-  int32_t* tables = reinterpret_cast<int32_t*>(merge + Path::kMergeFloats);
+  uint4* qs = reinterpret_cast<uint4*>(smem + Path::kS * kSB);
+  int32_t* tables = reinterpret_cast<int32_t*>(qs + kWarps * (Path::kQueryBytes / 16));
+  qs += threadIdx.x / 32 * (Path::kQueryBytes / 16);
   __shared__ Walk walk;
   __shared__ Segment segs[4];
   const int warp = threadIdx.x >> 5;
@@ -762,7 +789,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_int4_kernel(const Decod
       if (threadIdx.x < 32 * Path::kParts) {
         float o[8], M, L;
         int hh, d;
-        Path::merge8(merge, threadIdx.x, o, M, L, hh, d);
+        Path::merge8(smem, threadIdx.x, o, M, L, hh, d);
         if (run_bad) L = -1.f;  // marks a failed run
         if (hh >= nheads) {
           // (a column without a query head)
@@ -791,10 +818,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_int4_kernel(const Decod
         p.notes[blockIdx.x] =
             make_int4(static_cast<int>(row0), nheads, done_runs, done_flags & kLater ? 1 : 0);
       run_bad = false;
+      __syncthreads();  // the merged states are read: their place is free
     }
     if (nb == 0) break;
     if (threadIdx.x == 0) next_segment(p, walk, segs[(s + 2) & 3]);
-    if (seg.flags & kInit) Path::init(st, query, p.scale_log2, lane);
+    if (seg.flags & kInit) Path::init(st, query, p.scale_log2, qs, lane);
 
     // ---- the segment's blocks
     run_bad |= bad;
@@ -811,9 +839,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_int4_kernel(const Decod
         if (i + (have - 1) * kWarps == nb - 1) valid += tail - kBlockSize;
         const bool first = init && i == warp;
         if (valid == kBlockSize * kStep)
-          Path::template consume<false>(st, ring + at, valid, first, lane);
+          Path::template consume<false>(st, qs, ring + at, valid, first, lane);
         else
-          Path::template consume<true>(st, ring + at, valid, first, lane);
+          Path::template consume<true>(st, qs, ring + at, valid, first, lane);
         at = at == (kBuf - 1) * kStepBytes ? 0 : at + kStepBytes;
         next = next == (kBuf - 1) * kStepBytes ? 0 : next + kStepBytes;
       }
@@ -825,92 +853,141 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_int4_kernel(const Decod
     done_runs = seg.runs;
     cp_async_wait<0>();
     if (done_flags & kMerge) {
-      __syncthreads();  // the merge before this one has been read
-      Path::finalize(st, merge, warp, lane);
+      __syncwarp();  // the ring is read
+      Path::finalize(st, ring, lane);
     }
     bad = __syncthreads_or(table_bad(s + 1)) != 0;
   }
   dev::launch_dependents();
 }
 
-// Merge of the cut contexts: block i takes the one that CTA i started, kSplit
-// warps per head; the rest of it are the first runs (slot 0) of the unit's next
-// pieces.  note: first output row, heads, runs, slot of the first run.
-template <int D, bool kBf16Out, int kSplit>
-__global__ void __launch_bounds__(kSplit * 8 * 32) merge_int4_kernel(const DecodeParams p) {
-  constexpr int E = D / 32, H = 8;
-  __shared__ float s_o[kSplit > 1 ? H : 1][kSplit > 1 ? kSplit : 1][kSplit > 1 ? D : 1];
-  __shared__ float2 s_ml[H][kSplit];
+// One row of a merge: a head's partial states combined run by run.
+template <int E>
+struct Merge {
+  float M, L, o[E];
+  bool bad;
+
+  __device__ __forceinline__ void clear() {
+    M = -INFINITY;
+    L = 0.f;
+    bad = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+  }
+  // Workspace row `prow`, this lane's E outputs; L < 0 marks a failed run.
+  __device__ __forceinline__ void add(const DecodeParams& p, size_t prow, int lane) {
+    const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * prow);
+    float x[E];
+    if constexpr (E == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(p.ws_o + prow * (32 * E) + lane * E);
+      x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(p.ws_o + prow * (32 * E) + lane * E);
+      x[0] = t.x, x[1] = t.y;
+    }
+    bad |= v.y < 0.f;
+    const float mn = fmaxf(M, v.x);
+    const float f0 = exp2f(M - mn), f1 = exp2f(v.x - mn);
+    M = mn;
+    L = fmaf(L, f0, f1 * v.y);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f0, f1 * x[e]);
+  }
+  template <bool kBf16Out>
+  __device__ __forceinline__ void store(const DecodeParams& p, size_t row, int lane) const {
+    const float inv = !bad && L > 0.f ? 1.f / L : 0.f;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e)
+      w[e] = inv > 0.f ? dev::pack2<kBf16Out>(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + row * (32 * E) + lane * E;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(out) = w[0];
+  }
+};
+
+// Merge of the cut contexts, many of them with few runs each: block i takes the
+// one that CTA i started, a warp per head; the rest of it are the first runs
+// (slot 0) of the unit's next pieces.  note: first output row, heads, runs, slot
+// of the first run.
+template <int D, bool kBf16Out>
+__global__ void __launch_bounds__(256) merge_noted_kernel(const DecodeParams p) {
   dev::grid_dependency_wait();
   dev::launch_dependents();
   const int4 note = p.notes[blockIdx.x];
-  if (note.x < 0) return;
-  const int lane = threadIdx.x & 31, hh = (threadIdx.x >> 5) / kSplit,
-            sub = (threadIdx.x >> 5) % kSplit;
-  const int first = blockIdx.x, runs = note.z, units = p.num_kv_heads * p.qgroups;
-  float M = -INFINITY, L = 0.f, acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  bool bad = false;
-  if (hh < note.y) {
+  const int lane = threadIdx.x & 31, hh = threadIdx.x >> 5;
+  if (note.x < 0 || hh >= note.y) return;
+  const int units = p.num_kv_heads * p.qgroups;
+  Merge<D / 32> m;
+  m.clear();
 #pragma unroll 4
-    for (int i = sub; i < runs; i += kSplit) {
-      const size_t prow =
-          (static_cast<size_t>(first + i * units) * 2 + (i == 0 ? note.w : 0)) * H + hh;
-      const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * prow);
-      float x[E];
-      if constexpr (E == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(p.ws_o + prow * D + lane * E);
-        x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
-      } else {
-        const float2 t = *reinterpret_cast<const float2*>(p.ws_o + prow * D + lane * E);
-        x[0] = t.x, x[1] = t.y;
-      }
-      bad |= v.y < 0.f;  // a failed run
-      const float mn = fmaxf(M, v.x);
-      const float f0 = exp2f(M - mn), f1 = exp2f(v.x - mn);
-      M = mn;
-      L = fmaf(L, f0, f1 * v.y);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f0, f1 * x[e]);
-    }
+  for (int i = 0; i < note.z; ++i)
+    m.add(p, (static_cast<size_t>(blockIdx.x + i * units) * 2 + (i == 0 ? note.w : 0)) * 8 + hh,
+          lane);
+  m.template store<kBf16Out>(p, static_cast<size_t>(note.x) + hh, lane);
+}
+
+// The same for few contexts with many runs each: a block per (query head of a
+// unit, unit, request) and 16 warps over the runs.  The request's place among
+// the pieces is found from the lengths again (at most pieces / 16 of them).
+template <int D, bool kBf16Out>
+__global__ void __launch_bounds__(512) merge_long_kernel(const DecodeParams p, int pieces) {
+  constexpr int E = D / 32, W = 16;
+  __shared__ __align__(16) float s_o[W][D];
+  __shared__ float2 s_ml[W];
+  dev::grid_dependency_wait();
+  dev::launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int units = p.num_kv_heads * p.qgroups;
+  const int hh = blockIdx.x, unit = blockIdx.y, b = blockIdx.z;
+  const int head = unit % p.qgroups * p.heads_per_cta;
+  if (head + hh >= p.group) return;
+  long long total = 0, start = 0;
+  for (int i = lane; i < p.batch; i += 32) {
+    const int nblk = blocks_of(p, p.context_lens[i]);
+    total += nblk;
+    if (i < b) start += nblk;
   }
-  if constexpr (kSplit > 1) {
-    if (lane == 0) s_ml[hh][sub] = make_float2(M, bad ? -1.f : L);
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[hh][sub][lane * E + e] = acc[e];
-    __syncthreads();
-    if (sub != 0) return;
-    M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kSplit; ++w) {
-      bad |= s_ml[hh][w].y < 0.f;
-      if (s_ml[hh][w].y > 0.f) M = fmaxf(M, s_ml[hh][w].x);
-    }
-    L = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kSplit; ++w) {
-      if (s_ml[hh][w].y > 0.f) {
-        const float f = exp2f(s_ml[hh][w].x - M);
-        L = fmaf(f, s_ml[hh][w].y, L);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, s_o[hh][w][lane * E + e], acc[e]);
-      }
-    }
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    start += __shfl_xor_sync(0xffffffffu, start, o);
   }
-  if (hh >= note.y) return;
-  const float inv = !bad && L > 0.f ? 1.f / L : 0.f;
-  uint32_t w[E / 2];
+  const int nblk = blocks_of(p, p.context_lens[b]);
+  const long long size = piece_size(total, pieces);
+  const int first = static_cast<int>(start / size);
+  const int runs = static_cast<int>((start + nblk - 1) / size) - first + 1;
+  if (nblk == 0 || runs <= 1) return;  // its rows are final
+  Merge<E> m;
+  m.clear();
+#pragma unroll 4
+  for (int i = warp; i < runs; i += W)
+    m.add(p,
+          (static_cast<size_t>((first + i) * units + unit) * 2 +
+           (i == 0 && start % size != 0 ? 1 : 0)) * 8 + hh,
+          lane);
+  if (lane == 0) s_ml[warp] = make_float2(m.M, m.bad ? -1.f : m.L);
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e)
-    w[e] = inv > 0.f ? dev::pack2<kBf16Out>(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
-  uint16_t* out = static_cast<uint16_t*>(p.out) + (static_cast<size_t>(note.x) + hh) * D + lane * E;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(out) = w[0];
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = m.o[e];
+  __syncthreads();
+  if (warp != 0) return;
+  // one warp's state per lane
+  const float2 v = lane < W ? s_ml[lane] : make_float2(-INFINITY, 0.f);
+  m.clear();
+  m.bad = __any_sync(0xffffffffu, v.y < 0.f);
+  const float M = dev::warp_max(v.y > 0.f ? v.x : -INFINITY);
+  const float f = v.y > 0.f ? exp2f(v.x - M) : 0.f;
+  m.L = dev::warp_sum(f * v.y);
+  const int warps = min(runs, W);
+  for (int w = 0; w < warps; ++w) {
+    const float fw = __shfl_sync(0xffffffffu, f, w);
+#pragma unroll
+    for (int e = 0; e < E; ++e) m.o[e] = fmaf(fw, s_o[w][lane * E + e], m.o[e]);
+  }
+  m.template store<kBf16Out>(
+      p, static_cast<size_t>(b) * p.num_q_heads + unit / p.qgroups * p.group + head + hh, lane);
 }
 
 template <class Path>
@@ -935,21 +1012,21 @@ cudaError_t launch_decode_int4(const DecodeParams& p, int grid_x, cudaStream_t s
   return cudaErrorInvalidValue;
 }
 
-template <int kSplit>
+template <int D, bool kBf16Out>
 static cudaError_t launch_merge(const DecodeParams& p, int grid_x, cudaStream_t s) {
-  const dim3 grid(grid_x), block(kSplit * 8 * 32);
-  if (p.head_dim == 64)
-    return p.q_bf16 ? launch_pdl(merge_int4_kernel<64, true, kSplit>, grid, block, 0, s, p)
-                    : launch_pdl(merge_int4_kernel<64, false, kSplit>, grid, block, 0, s, p);
-  return p.q_bf16 ? launch_pdl(merge_int4_kernel<128, true, kSplit>, grid, block, 0, s, p)
-                  : launch_pdl(merge_int4_kernel<128, false, kSplit>, grid, block, 0, s, p);
+  // A context spans pieces / batch runs when all are alike.  From 4 on a block
+  // per head beats a warp per head (57 runs: 7.7 us with four warps a head).
+  const int units = p.num_kv_heads * p.qgroups, pieces = grid_x / units;
+  if (pieces >= 8 * p.batch)
+    return launch_pdl(merge_long_kernel<D, kBf16Out>, dim3(p.heads_per_cta, units, p.batch),
+                      dim3(512), 0, s, p, pieces);
+  return launch_pdl(merge_noted_kernel<D, kBf16Out>, dim3(grid_x), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_decode_int4_merge(const DecodeParams& p, int grid_x, cudaStream_t s) {
-  // A context spans pieces / batch runs when all are alike: from 8 on, four
-  // warps share a head.
-  const int pieces = grid_x / (p.num_kv_heads * p.qgroups);
-  return pieces >= 8 * p.batch ? launch_merge<4>(p, grid_x, s) : launch_merge<1>(p, grid_x, s);
+  if (p.head_dim == 64)
+    return p.q_bf16 ? launch_merge<64, true>(p, grid_x, s) : launch_merge<64, false>(p, grid_x, s);
+  return p.q_bf16 ? launch_merge<128, true>(p, grid_x, s) : launch_merge<128, false>(p, grid_x, s);
 }
 
 }  // namespace kvp

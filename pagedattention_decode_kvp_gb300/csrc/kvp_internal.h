@@ -67,8 +67,10 @@ struct DecodeParams {
   int4* notes;                  // 4-bit balanced decode (part_blocks == 0): one per CTA
 };
 
-// CTAs of the balanced 4-bit decode: 3 on each of GB300's 152 SMs.
-constexpr int kInt4Ctas = 152 * 3;
+// Resident CTAs of the 4-bit decode per SM: its step loop takes 168 registers at
+// head_dim 128 (with 128 it spills: 119 us against 107 for 57 contexts of 9200
+// tokens) and 128 at head_dim 64 (4 CTAs 70 us, 3 CTAs 76, 32 x 32 heads of 4096).
+constexpr int int4_ctas_per_sm(int head_dim) { return head_dim == 128 ? 3 : 4; }
 
 // Everything the row kernels (rotary positions, 4-bit quantisation, scatter)
 // need.  Strides are elements from one token to the next.

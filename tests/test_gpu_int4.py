@@ -235,9 +235,11 @@ HEADS = [(1, 1), (2, 1), (6, 2), (8, 1), (5, 5), (12, 1), (16, 2), (17, 1)]
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Hq,kv", HEADS)
-@pytest.mark.parametrize("pb", [0, 3, 8])
-def test_decode_int4_shapes(dtype, D, Hq, kv, pb):
-    c = Case([1, 15, 16, 17, 100, 257, 530, 0, 48], Hq, kv, D, dtype, seed=Hq + D, max_blocks=40)
+@pytest.mark.parametrize("pb,max_blocks", [(0, 40), (3, 40), (8, 40), (0, 70)])
+def test_decode_int4_shapes(dtype, D, Hq, kv, pb, max_blocks):
+    """One pass (tables of up to 64 blocks), given partitions, balanced pieces."""
+    c = Case([1, 15, 16, 17, 100, 257, 530, 0, 48], Hq, kv, D, dtype, seed=Hq + D,
+             max_blocks=max_blocks)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     out = c.run(pb, status)
     assert kvp.kvp_read_status(status) == kvp.KVP_OK
@@ -334,6 +336,16 @@ def test_decode_int4_queries_of_any_size(dtype, factor):
     c.check(c.run())
 
 
+def test_decode_int4_bad_id_in_one_piece_of_a_long_context():
+    c = Case([4000, 4000], 8, 2, 128, torch.float16, seed=18)
+    good = c.run()
+    c.tables[0, 200] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = c.run(0, status)
+    assert kvp.kvp_read_status(status) == kvp.KVP_ERR_BAD_BLOCK
+    assert torch.count_nonzero(out[0]) == 0 and torch.equal(out[1], good[1])
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_decode_int4_long_context(dtype):
     c = Case([20011], 8, 1, 128, dtype, seed=31)
@@ -353,12 +365,52 @@ def test_decode_int4_split_phases_and_repeats_give_the_same_bits():
     assert torch.equal(out, whole)
 
 
-@pytest.mark.parametrize("pb", [0, 2])
-def test_decode_int4_bad_table_or_length_zeroes_the_rows(pb):
-    c = Case([100, 40, 70], 8, 2, 64, torch.float16, seed=8, max_blocks=7)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D,Hq,kv,B", [(128, 16, 1, 9), (64, 8, 8, 40), (128, 32, 32, 3),
+                                       (64, 921, 307, 2)])
+def test_decode_int4_balanced_pieces(dtype, D, Hq, kv, B):
+    """Ragged contexts whose pieces cut some of them once, some often and some
+    not at all, with empty ones between; more kv heads than pieces."""
+    lens = [(700 * (i % 3) + 37 * i * i) % 1500 for i in range(B)]
+    lens[0], lens[-1] = 1999, 1
+    if B > 4:
+        lens[2] = lens[3] = 0
+        lens[4] = 16
+    c = Case(lens, Hq, kv, D, dtype, seed=B, max_blocks=126)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = c.run(0, status)
+    assert kvp.kvp_read_status(status) == kvp.KVP_OK
+    c.check(out)
+    assert torch.equal(out, c.run(0))
+
+
+@pytest.mark.parametrize("lens", [[1040], [8 * 16], [8 * 16 + 1, 7], [129, 0, 2000, 0],
+                                  [16] * 200, [1] * 500, [40] * 130 + [3000] + [40] * 7])
+def test_decode_int4_balanced_edges(lens):
+    """Pieces that end with a context, one-block contexts, more requests than
+    threads of a CTA, one long context among short ones."""
+    c = Case(lens, 2, 1, 128, torch.float16, seed=len(lens), max_blocks=190)
+    c.check(c.run())
+
+
+def test_decode_int4_workspace_is_all_that_is_written():
+    """The balanced decode writes its workspace only; what lies behind stays."""
+    c = Case([3000, 10, 500], 16, 2, 128, torch.bfloat16, seed=3)
+    n = c.workspace().numel()
+    ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((5,) + c.q.shape[1:], 9.0, dtype=c.q.dtype, device="cuda")
+    kvp.kvp_attention_decode_int4(out[1:4], c.q.cuda(), *c.pools, c.tables.cuda(), c.lens.cuda(),
+                                  c.scale, workspace=ws[:n])
+    c.check(out[1:4])
+    assert (ws[n:] == 0x5A).all() and (out[0] == 9).all() and (out[4] == 9).all()
+
+
+@pytest.mark.parametrize("pb,max_blocks", [(0, 7), (2, 7), (0, 90)])
+def test_decode_int4_bad_table_or_length_zeroes_the_rows(pb, max_blocks):
+    c = Case([100, 40, 70], 8, 2, 64, torch.float16, seed=8, max_blocks=max_blocks)
     good = c.run(pb)
-    for b, entry, value, length in ((0, 6, 10 ** 6, 100), (1, 0, -3, 40), (2, 0, 0, 113),
-                                    (0, 0, 0, -1)):
+    for b, entry, value, length in ((0, 6, 10 ** 6, 100), (1, 0, -3, 40),
+                                    (2, 0, 0, 16 * max_blocks + 1), (0, 0, 0, -1)):
         was = c.tables[b, entry].clone(), c.lens[b].clone()
         c.lens[b] = length
         if length == int(was[1]):

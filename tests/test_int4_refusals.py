@@ -36,8 +36,9 @@ def test_sizing_of_the_4_bit_decode(lib):
     # given partitions, and tables short enough for a single pass
     assert kvp.kvp_decode_workspace_bytes(4, 64, d, 8192, 512, kv_int4=True) == \
         4 * 64 * 16 * (128 + 2) * 4
-    assert kvp.kvp_decode_workspace_bytes(4, 64, d, 16, kv_int4=True) == 0
-    assert kvp.kvp_decode_partition_blocks(4, 64, d, 16, kv_int4=True) == 16
+    assert kvp.kvp_decode_workspace_bytes(4, 64, d, 64, kv_int4=True) == 0
+    assert kvp.kvp_decode_partition_blocks(4, 64, d, 64, kv_int4=True) == 64
+    assert kvp.kvp_decode_workspace_bytes(4, 64, d, 65, kv_int4=True) > 0
     for kind in (3, 5, -1):
         assert lib.kvp_decode_workspace_bytes(4, 64, d, 8192, 0, kind) == 0
         assert lib.kvp_decode_partition_blocks(4, 64, d, 8192, kind) == 0
