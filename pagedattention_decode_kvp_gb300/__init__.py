@@ -13,6 +13,7 @@ Block manager: :class:`BlockManager` wraps the host allocator (``kvp_bm_*``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -38,6 +39,7 @@ KVP_PHASE_REDUCE = 2
 KVP_PHASE_ALL = 3
 KVP_DECODE_MERGE_RUNS = 8  # or'ed into `phases`: one copy per run of consecutive blocks
 BLOCK_SIZE = 16
+_ONE = (1,)
 
 
 class kvp_cache_desc(ctypes.Structure):
@@ -429,27 +431,28 @@ def kvp_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, 
 
 
 # ------------------------------------------------------------------ 4-bit cache
+# The calls below are short on the GPU, so their checks are written to cost
+# little: one expression tells whether everything is in order, and only where it
+# is not are the arguments gone through one by one for the error.
 def _on_one_device(stream, *ts) -> int:
     """CUDA tensors of one device, which is the current one (kernels launch
-    there); returns the stream to use.  (These calls are short: the checks are
-    written to cost less than the launch.)"""
-    torch = _torch()
+    there); returns the stream to use."""
     dev = None
     for t in ts:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
-            if dev is not None:
-                raise ValueError(f"tensors on cuda:{dev} and cuda:{d} in one call")
-            dev = d
-    if dev != torch._C._cuda_getDevice():
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
+                if dev is not None:
+                    raise ValueError(f"tensors on cuda:{dev} and cuda:{d} in one call")
+                dev = d
+    c = _torch()._C
+    if dev != c._cuda_getDevice():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is "
-                         f"cuda:{torch._C._cuda_getDevice()}")
+                         f"cuda:{c._cuda_getDevice()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return c._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError(f"tensors on cuda:{dev}, but the stream is of cuda:{stream.device_index}")
     return stream.cuda_stream
@@ -472,26 +475,65 @@ def _extents(t, name, dims):
     return t.shape
 
 
+@functools.lru_cache(maxsize=256)
+def _desc(nb, hkv, bs, d) -> kvp_cache_desc:
+    return kvp_cache_desc(nb, hkv, bs, d)
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_desc(rotary_dim, sections, interleaved) -> kvp_rope_desc:
+    if not 1 <= len(sections) <= 4:
+        raise ValueError(f"1 to 4 axes are allowed, sections has {len(sections)}")
+    return kvp_rope_desc(rotary_dim, len(sections), (ctypes.c_int32 * 4)(*sections), interleaved)
+
+
 def cache_desc_int4(k_cache) -> kvp_cache_desc:
     """kvp_cache_desc of a 4-bit pool's codes [NB, Hkv, block_size, D / 2] (uint8)."""
     if k_cache.dim() != 4:
         raise ValueError("4-bit pools are [num_blocks, num_kv_heads, block_size, head_dim / 2]")
     nb, hkv, bs, half = k_cache.shape
-    return kvp_cache_desc(nb, hkv, bs, 2 * half)
+    return _desc(nb, hkv, bs, 2 * half)
 
 
-def _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype=None) -> kvp_cache_desc:
-    torch = _torch()
+def _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype) -> kvp_cache_desc:
+    u8 = _torch().uint8
+    codes = k_cache.shape
     d = cache_desc_int4(k_cache)
-    codes = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim // 2)
-    _need(k_cache, "k_cache", torch.uint8, codes)
-    _need(v_cache, "v_cache", torch.uint8, codes)
-    if d.head_dim in (64, 128):  # the library refuses others
-        pairs = codes[:3] + (d.head_dim // 64, 2)
-        dtype = k_scale_zero.dtype if dtype is None else dtype
-        _need(k_scale_zero, "k_scale_zero", dtype, pairs)
-        _need(v_scale_zero, "v_scale_zero", dtype, pairs)
+    pairs = codes[:3] + (d.head_dim // 64, 2)
+    if not (k_cache.dtype is u8 and v_cache.dtype is u8 and v_cache.shape == codes and
+            k_scale_zero.dtype is dtype and v_scale_zero.dtype is dtype and
+            k_scale_zero.shape == pairs and v_scale_zero.shape == pairs and
+            k_cache.is_contiguous() and v_cache.is_contiguous() and
+            k_scale_zero.is_contiguous() and v_scale_zero.is_contiguous()):
+        _need(k_cache, "k_cache", u8, codes)
+        _need(v_cache, "v_cache", u8, codes)
+        if d.head_dim in (64, 128):  # the library refuses others
+            _need(k_scale_zero, "k_scale_zero", dtype, pairs)
+            _need(v_scale_zero, "v_scale_zero", dtype, pairs)
     return d
+
+
+def _int4_rows(name, stream, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
+               slot_mapping, status):
+    """Checks and call of the two entry points that move rows [T, Hkv, D]."""
+    lib = load_library()
+    s = _on_one_device(stream, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
+                       slot_mapping, status)
+    dtype, i32 = key.dtype, _torch().int32
+    code = _dtype_code(key)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype)
+    T, = _extents(slot_mapping, "slot_mapping", 1)
+    rows = (T, d.num_kv_heads, d.head_dim)
+    if not (slot_mapping.dtype is i32 and value.dtype is dtype and key.shape == rows and
+            value.shape == rows and slot_mapping.is_contiguous() and key.is_contiguous() and
+            value.is_contiguous()):
+        _need(slot_mapping, "slot_mapping", i32, (T,))
+        _need(key, "key", dtype, rows)
+        _need(value, "value", dtype, rows)
+    _check(getattr(lib, name)(
+        key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
+        _ptr(status), s), name)
 
 
 def kvp_append_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot_mapping, *,
@@ -499,40 +541,16 @@ def kvp_append_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, sl
     """Quantise key/value [T, Hkv, D] (fp16/bf16) to 4 bits with one (scale, zero)
     pair per 64 elements and scatter them: codes into uint8 pools
     [NB, Hkv, bs, D/2], pairs into [NB, Hkv, bs, D/64, 2] of key's dtype."""
-    lib = load_library()
-    s = _on_one_device(stream, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
-                       slot_mapping, status)
-    code = _dtype_code(key)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
-    T, = _extents(slot_mapping, "slot_mapping", 1)
-    _need(slot_mapping, "slot_mapping", _torch().int32, (T,))
-    rows = (T, d.num_kv_heads, d.head_dim)
-    _need(key, "key", key.dtype, rows)
-    _need(value, "value", key.dtype, rows)
-    _check(lib.kvp_append_int4(key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(),
-                               v_cache.data_ptr(), k_scale_zero.data_ptr(),
-                               v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
-                               _ptr(status), s), "kvp_append_int4")
+    _int4_rows("kvp_append_int4", stream, key, value, k_cache, v_cache, k_scale_zero,
+               v_scale_zero, slot_mapping, status)
 
 
 def kvp_read_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot_mapping, *,
                   status=None, stream=None) -> None:
     """key/value [T, Hkv, D] = the values held in 4 bits at slot_mapping [T]
     (rows of negative slots are left as they are)."""
-    lib = load_library()
-    s = _on_one_device(stream, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
-                       slot_mapping, status)
-    code = _dtype_code(key)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
-    T, = _extents(slot_mapping, "slot_mapping", 1)
-    _need(slot_mapping, "slot_mapping", _torch().int32, (T,))
-    rows = (T, d.num_kv_heads, d.head_dim)
-    _need(key, "key", key.dtype, rows)
-    _need(value, "value", key.dtype, rows)
-    _check(lib.kvp_read_int4(key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(),
-                             v_cache.data_ptr(), k_scale_zero.data_ptr(),
-                             v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
-                             _ptr(status), s), "kvp_read_int4")
+    _int4_rows("kvp_read_int4", stream, key, value, k_cache, v_cache, k_scale_zero,
+               v_scale_zero, slot_mapping, status)
 
 
 def kvp_copy_blocks_int4(k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, *, status=None,
@@ -540,7 +558,8 @@ def kvp_copy_blocks_int4(k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, *,
     """Copy block pairs[i, 0] onto pairs[i, 1] in 4-bit pools (codes and pairs)."""
     lib = load_library()
     s = _on_one_device(stream, k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, status)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero)
+    _dtype_code(k_scale_zero)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, k_scale_zero.dtype)
     _need(pairs, "pairs", _torch().int32, (_extents(pairs, "pairs", 2)[0], 2))
     _check(lib.kvp_copy_blocks_int4(k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
@@ -557,64 +576,76 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
     lib = load_library()
     s = _on_one_device(stream, out, q, k_cache, v_cache, k_scale_zero, v_scale_zero, block_tables,
                        context_lens, workspace, status)
+    dtype, i32 = q.dtype, _torch().int32
     code = _dtype_code(q)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, q.dtype)
+    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype)
     B, Hq, _ = _extents(q, "q", 3)
-    rows = (B, Hq, d.head_dim)
-    _need(q, "q", q.dtype, rows)
-    _need(out, "out", q.dtype, rows)
-    i32 = _torch().int32
     MB = _extents(block_tables, "block_tables", 2)[1]
-    _need(block_tables, "block_tables", i32, (B, MB))
-    _need(context_lens, "context_lens", i32, (B,))
+    rows = (B, Hq, d.head_dim)
+    if not (q.shape == rows and out.shape == rows and out.dtype is dtype and
+            block_tables.dtype is i32 and context_lens.dtype is i32 and
+            block_tables.shape[0] == B and context_lens.shape == (B,) and
+            q.is_contiguous() and out.is_contiguous() and block_tables.is_contiguous() and
+            context_lens.is_contiguous()):
+        _need(q, "q", dtype, rows)
+        _need(out, "out", dtype, rows)
+        _need(block_tables, "block_tables", i32, (B, MB))
+        _need(context_lens, "context_lens", i32, (B,))
     ws, ws_bytes = None, 0
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("tensors passed to the GPU entry points must be contiguous")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     _check(lib.kvp_attention_decode_int4(
         out.data_ptr(), q.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(),
-        k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), block_tables.data_ptr(),
-        MB, context_lens.data_ptr(), B, Hq, float(scale), d, int(partition_blocks), ws, ws_bytes, int(phases), _ptr(status), s),
-        "kvp_attention_decode_int4")
+        k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), block_tables.data_ptr(), MB,
+        context_lens.data_ptr(), B, Hq, scale, d, partition_blocks, ws, ws_bytes, phases,
+        _ptr(status), s), "kvp_attention_decode_int4")
 
 
 # ------------------------------------------------------------------ rotary append
-def _rows(t, name, dtype, T, heads, dim) -> int:
+def _rows(t, name, dtype, shape) -> int:
     """Element stride between the tokens of t [T, heads, dim], whose rows are
     contiguous and lie behind one another (a slice of a projection's output)."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (T, heads, dim):
-        raise ValueError(f"{name} must have shape {(T, heads, dim)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     st, sh, sd = t.stride()
+    T, heads, dim = shape
     if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return st if T > 1 else heads * dim
 
 
-def _rope_args(q_out, q, key, value, kv_heads, dim, cos_sin, positions, slot_mapping, sections,
-               interleaved):
+def _rope_args(q_out, q, key, value, d, cos_sin, positions, slot_mapping, sections, interleaved):
     torch = _torch()
+    i32 = torch.int32
     T, = _extents(slot_mapping, "slot_mapping", 1)
-    _need(slot_mapping, "slot_mapping", torch.int32, (T,))
     P, R = _extents(cos_sin, "cos_sin", 2)
-    _need(cos_sin, "cos_sin", torch.float32, (P, R))
-    A = positions.shape[0] if positions.dim() == 2 else 1
-    _need(positions, "positions", torch.int32, (A, T) if positions.dim() == 2 else (T,))
-    sections = (R // 2,) if sections is None else sections
-    if len(sections) != A or A > 4:
-        raise ValueError(f"positions has {A} axes (1 to 4 are allowed), sections {len(sections)}")
-    rope = kvp_rope_desc(R, A, (ctypes.c_int32 * 4)(*sections), 1 if interleaved else 0)
-    ks = _rows(key, "key", key.dtype, T, kv_heads, dim)
-    vs = _rows(value, "value", key.dtype, T, kv_heads, dim)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    if q is None:
+    sections = (R // 2,) if sections is None else tuple(sections)
+    if not (slot_mapping.dtype is i32 and positions.dtype is i32 and
+            cos_sin.dtype is torch.float32 and positions.shape == (len(sections), T) and
+            slot_mapping.is_contiguous() and positions.is_contiguous() and
+            cos_sin.is_contiguous()):
+        _need(slot_mapping, "slot_mapping", i32, (T,))
+        _need(cos_sin, "cos_sin", torch.float32, (P, R))
+        one = positions.dim() == 1 and len(sections) == 1
+        if not one and (positions.dim() != 2 or positions.shape[0] != len(sections)):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, sections "
+                             f"{len(sections)} axes")
+        _need(positions, "positions", i32, (T,) if one else (len(sections), T))
+    rope = _rope_desc(R, sections, 1 if interleaved else 0)
+    dtype, kv, dim = key.dtype, d.num_kv_heads, d.head_dim
+    ks = _rows(key, "key", dtype, (T, kv, dim))
+    vs = _rows(value, "value", dtype, (T, kv, dim))
+    if q is None or q_out is None:
+        if q is not q_out:
+            raise ValueError("q and q_out go together")
         return T, 0, rope, P, (None, 0, None, 0, key.data_ptr(), ks, value.data_ptr(), vs)
-    Hq = q.shape[1] if q.dim() == 3 else 0
-    qs = _rows(q, "q", key.dtype, T, Hq, dim)
-    qo = _rows(q_out, "q_out", key.dtype, T, Hq, dim)
+    Hq = _extents(q, "q", 3)[1]
+    qs = _rows(q, "q", dtype, (T, Hq, dim))
+    qo = _rows(q_out, "q_out", dtype, (T, Hq, dim))
     return T, Hq, rope, P, (q_out.data_ptr(), qo, q.data_ptr(), qs, key.data_ptr(), ks,
                             value.data_ptr(), vs)
 
@@ -634,13 +665,16 @@ def kvp_rope_append(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, 
     lib = load_library()
     s = _on_one_device(stream, q_out, q, key, value, k_cache, v_cache, cos_sin, positions,
                        slot_mapping, status)
+    dtype = key.dtype
     code = _dtype_code(key)
-    d = cache_desc(k_cache)
-    pool = (d.num_blocks, d.num_kv_heads, d.block_size, d.head_dim)
-    _need(k_cache, "k_cache", key.dtype, pool)
-    _need(v_cache, "v_cache", key.dtype, pool)
-    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d.num_kv_heads, d.head_dim, cos_sin,
-                                      positions, slot_mapping, sections, interleaved)
+    pool = _extents(k_cache, "k_cache", 4)
+    d = _desc(*pool)
+    if not (k_cache.dtype is dtype and v_cache.dtype is dtype and v_cache.shape == pool and
+            k_cache.is_contiguous() and v_cache.is_contiguous()):
+        _need(k_cache, "k_cache", dtype, pool)
+        _need(v_cache, "v_cache", dtype, pool)
+    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d, cos_sin, positions, slot_mapping,
+                                      sections, interleaved)
     _check(lib.kvp_rope_append(*rows, k_cache.data_ptr(), v_cache.data_ptr(), cos_sin.data_ptr(),
                                P, positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, rope, d,
                                code, _ptr(status), s), "kvp_rope_append")
@@ -656,8 +690,8 @@ def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v
                        cos_sin, positions, slot_mapping, status)
     code = _dtype_code(key)
     d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
-    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d.num_kv_heads, d.head_dim, cos_sin,
-                                      positions, slot_mapping, sections, interleaved)
+    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d, cos_sin, positions, slot_mapping,
+                                      sections, interleaved)
     _check(lib.kvp_rope_append_int4(*rows, k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
                                     cos_sin.data_ptr(), P, positions.data_ptr(),
@@ -666,6 +700,13 @@ def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v
 
 
 # ------------------------------------------------------------------ device-side tables
+def _i32_vectors(**named):
+    """Each (tensor, length) a contiguous int32 vector."""
+    i32 = _torch().int32
+    for name, (t, n) in named.items():
+        _need(t, name, i32, (n,))
+
+
 def kvp_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_count,
                       context_lens_out, free_count_out, slot_mapping, query_start,
                       positions=None, *, status=None, stream=None) -> None:
@@ -683,24 +724,31 @@ def kvp_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_co
     B, MB = _extents(block_tables, "block_tables", 2)
     T, = _extents(slot_mapping, "slot_mapping", 1)
     NB, = _extents(free_blocks, "free_blocks", 1)
-    per_request = (B,)
-    _need(block_tables, "block_tables", i32, (B, MB))
-    _need(context_lens, "context_lens", i32, per_request)
-    _need(new_lens, "new_lens", i32, per_request)
-    _need(context_lens_out, "context_lens_out", i32, per_request)
-    _need(free_blocks, "free_blocks", i32, (NB,))
-    _need(free_count, "free_count", i32, (1,))
-    _need(free_count_out, "free_count_out", i32, (1,))
-    _need(query_start, "query_start", i32, (B + 1,))
-    _need(slot_mapping, "slot_mapping", i32, (T,))
+    per = (B,)
+    if not (block_tables.dtype is i32 and context_lens.dtype is i32 and new_lens.dtype is i32 and
+            context_lens_out.dtype is i32 and free_blocks.dtype is i32 and
+            free_count.dtype is i32 and free_count_out.dtype is i32 and
+            query_start.dtype is i32 and slot_mapping.dtype is i32 and
+            context_lens.shape == per and new_lens.shape == per and
+            context_lens_out.shape == per and free_count.shape == _ONE and
+            free_count_out.shape == _ONE and query_start.shape == (B + 1,) and
+            block_tables.is_contiguous() and context_lens.is_contiguous() and
+            new_lens.is_contiguous() and context_lens_out.is_contiguous() and
+            free_blocks.is_contiguous() and query_start.is_contiguous() and
+            slot_mapping.is_contiguous()):
+        _need(block_tables, "block_tables", i32, (B, MB))
+        _i32_vectors(context_lens=(context_lens, B), new_lens=(new_lens, B),
+                     context_lens_out=(context_lens_out, B), free_blocks=(free_blocks, NB),
+                     free_count=(free_count, 1), free_count_out=(free_count_out, 1),
+                     query_start=(query_start, B + 1), slot_mapping=(slot_mapping, T))
     if positions is not None:
         _need(positions, "positions", i32, (T,))
     _check(lib.kvp_extend_tables(block_tables.data_ptr(), MB, context_lens.data_ptr(),
                                  new_lens.data_ptr(), B, free_blocks.data_ptr(),
-                                 free_count.data_ptr(), NB,
-                                 context_lens_out.data_ptr(), free_count_out.data_ptr(),
-                                 slot_mapping.data_ptr(), T, query_start.data_ptr(),
-                                 _ptr(positions), _ptr(status), s), "kvp_extend_tables")
+                                 free_count.data_ptr(), NB, context_lens_out.data_ptr(),
+                                 free_count_out.data_ptr(), slot_mapping.data_ptr(), T,
+                                 query_start.data_ptr(), _ptr(positions), _ptr(status), s),
+           "kvp_extend_tables")
 
 
 def kvp_release_tables(block_tables, context_lens, finished, free_blocks, free_count,
@@ -713,19 +761,24 @@ def kvp_release_tables(block_tables, context_lens, finished, free_blocks, free_c
     i32 = _torch().int32
     B, MB = _extents(block_tables, "block_tables", 2)
     NB, = _extents(free_blocks, "free_blocks", 1)
-    per_request = (B,)
-    _need(block_tables, "block_tables", i32, (B, MB))
-    _need(context_lens, "context_lens", i32, per_request)
-    _need(finished, "finished", i32, per_request)
-    _need(context_lens_out, "context_lens_out", i32, per_request)
-    _need(free_blocks, "free_blocks", i32, (NB,))
-    _need(free_count, "free_count", i32, (1,))
-    _need(free_count_out, "free_count_out", i32, (1,))
+    per = (B,)
+    if not (block_tables.dtype is i32 and context_lens.dtype is i32 and finished.dtype is i32 and
+            context_lens_out.dtype is i32 and free_blocks.dtype is i32 and
+            free_count.dtype is i32 and free_count_out.dtype is i32 and
+            context_lens.shape == per and finished.shape == per and
+            context_lens_out.shape == per and free_count.shape == _ONE and
+            free_count_out.shape == _ONE and block_tables.is_contiguous() and
+            context_lens.is_contiguous() and finished.is_contiguous() and
+            context_lens_out.is_contiguous() and free_blocks.is_contiguous()):
+        _need(block_tables, "block_tables", i32, (B, MB))
+        _i32_vectors(context_lens=(context_lens, B), finished=(finished, B),
+                     context_lens_out=(context_lens_out, B), free_blocks=(free_blocks, NB),
+                     free_count=(free_count, 1), free_count_out=(free_count_out, 1))
     _check(lib.kvp_release_tables(block_tables.data_ptr(), MB, context_lens.data_ptr(),
                                   finished.data_ptr(), B, free_blocks.data_ptr(),
-                                  free_count.data_ptr(), NB,
-                                  context_lens_out.data_ptr(), free_count_out.data_ptr(),
-                                  _ptr(status), s), "kvp_release_tables")
+                                  free_count.data_ptr(), NB, context_lens_out.data_ptr(),
+                                  free_count_out.data_ptr(), _ptr(status), s),
+           "kvp_release_tables")
 
 
 def kvp_selftest_wait_timeout(status, limit_ns, stream=None):

@@ -8,12 +8,14 @@
 // Both are all-or-nothing: everything is checked before anything is written.
 //
 // The work is a scan over the requests and a few words per token: latency is
-// all there is to save, so a call is one launch.  A cluster of up to 8 CTAs
-// (a hardware barrier instead of a second launch) shares the tokens; each CTA
-// scans all requests by itself -- 16 at most per thread, read from L2 -- and
-// keeps the offsets in shared memory, where a token finds its request by
-// bisection.  The barrier between the checks and the writes also lets lengths
-// and counts be updated in place.
+// all there is to save.  One launch of one CTA does a decode step; above 512
+// requests or tokens it is a larger CTA, then a cluster of up to 8 (a hardware
+// barrier instead of a second launch) whose CTAs each scan all requests -- 16 at
+// most per thread, read from L2 -- and share the rest.  The offsets lie in shared
+// memory, where a token finds its request by bisection.  The barrier between the
+// checks and the writes also lets lengths and counts be updated in place.  Above
+// 16384 tokens the slots are written by a second launch that fills the GPU, from
+// the first one's outputs alone (tables, lengths and query offsets).
 #include <cooperative_groups.h>
 
 #include "kvp_device.cuh"
@@ -24,13 +26,15 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
-constexpr int kPerThread = kMaxTableBatch / kThreads;
-static_assert(kMaxTableBatch % kThreads == 0, "whole requests per thread");
+constexpr int kFillThreads = 256, kFillTokens = 1024;  // of the second launch
+constexpr int kFusedTokens = 16384;                    // slots the first launch writes itself
 
-// Exclusive prefix sums of two counts over the CTA's threads; totals in *sum.
+// Exclusive prefix sums of two counts over the CTA's kThreads threads; totals in
+// *sum.
+template <int kThreads>
 __device__ __forceinline__ longlong2 block_scan(longlong2 v, longlong2* sum) {
-  __shared__ longlong2 part[kThreads / 32];
+  constexpr int kW = kThreads / 32;
+  __shared__ longlong2 part[kW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   longlong2 s = v;
 #pragma unroll
@@ -44,27 +48,22 @@ __device__ __forceinline__ longlong2 block_scan(longlong2 v, longlong2* sum) {
   }
   if (lane == 31) part[warp] = s;
   __syncthreads();
-  longlong2 before = make_longlong2(0, 0), all = make_longlong2(0, 0);
-  {
-    longlong2 w = part[lane];  // kThreads / 32 == 32 warps
+  longlong2 w = lane < kW ? part[lane] : make_longlong2(0, 0);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, w.x, o);
-      const long long y = __shfl_up_sync(0xffffffffu, w.y, o);
-      if (lane >= o) {
-        w.x += x;
-        w.y += y;
-      }
+  for (int o = 1; o < kW; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, w.x, o);
+    const long long y = __shfl_up_sync(0xffffffffu, w.y, o);
+    if (lane >= o) {
+      w.x += x;
+      w.y += y;
     }
-    all.x = __shfl_sync(0xffffffffu, w.x, 31);
-    all.y = __shfl_sync(0xffffffffu, w.y, 31);
-    const int prev = warp > 0 ? warp - 1 : 0;
-    before.x = __shfl_sync(0xffffffffu, w.x, prev);
-    before.y = __shfl_sync(0xffffffffu, w.y, prev);
-    if (warp == 0) before = make_longlong2(0, 0);
   }
-  *sum = all;
-  return make_longlong2(before.x + s.x - v.x, before.y + s.y - v.y);
+  sum->x = __shfl_sync(0xffffffffu, w.x, kW - 1);
+  sum->y = __shfl_sync(0xffffffffu, w.y, kW - 1);
+  const int prev = warp > 0 ? warp - 1 : 0;
+  const long long bx = __shfl_sync(0xffffffffu, w.x, prev);
+  const long long by = __shfl_sync(0xffffffffu, w.y, prev);
+  return make_longlong2((warp > 0 ? bx : 0) + s.x - v.x, (warp > 0 ? by : 0) + s.y - v.y);
 }
 
 // Largest b in [0, n) with start[b] <= x (start is non-decreasing, start[0] = 0).
@@ -78,6 +77,21 @@ __device__ __forceinline__ int find_request(const int32_t* start, int n, int x) 
   return lo;
 }
 
+// Largest b in [0, n) with start[b] <= x, by a warp: 32 places a round.
+__device__ __forceinline__ int warp_find_request(const int32_t* start, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const unsigned at = __ballot_sync(0xffffffffu, i < n && start[lo + i] <= x);
+    const int k = __popc(at) - 1;  // lane 0's place always is
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
 // The first error of the cluster's CTAs (0: none).  Every CTA's reads of the
 // arrays a later phase rewrites are behind this barrier.
 __device__ __forceinline__ int cluster_error(int mine) {
@@ -86,6 +100,10 @@ __device__ __forceinline__ int cluster_error(int mine) {
   if (threadIdx.x == 0) err = 0;
   __syncthreads();
   if (mine != 0) atomicCAS(&err, 0, mine);
+  if (cl.num_blocks() == 1) {
+    __syncthreads();
+    return err;
+  }
   cl.sync();
   int e = 0;
   for (unsigned r = 0; r < cl.num_blocks() && e == 0; ++r) e = *cl.map_shared_rank(&err, r);
@@ -93,6 +111,10 @@ __device__ __forceinline__ int cluster_error(int mine) {
   return e;
 }
 
+// Blocks that hold n tokens.
+__device__ __forceinline__ int blocks_for(int n) { return (n + kBlockSize - 1) / kBlockSize; }
+
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TableParams p) {
   extern __shared__ int32_t smem[];
   int32_t* tok0 = smem;                   // [batch] first new token
@@ -106,44 +128,32 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablePara
   const long long most = static_cast<long long>(p.max_blocks) * kBlockSize;
 
   int err = 0;
-  // ---- this thread's run of requests
+  // ---- this thread's run of requests, read once for the sums and once more
+  // (from L1) for the offsets
   const int per = (p.batch + kThreads - 1) / kThreads;
-  const int b0 = threadIdx.x * per;
-  int n_of[kPerThread], new_of[kPerThread];
+  const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+  const int count = *p.free_count;
   longlong2 mine = make_longlong2(0, 0);
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = b0 + i;
-    n_of[i] = new_of[i] = 0;
-    if (i < per && b < p.batch) {
-      n_of[i] = p.context_lens[b];
-      new_of[i] = p.new_lens[b];
-      if (n_of[i] < 0 || new_of[i] < 0 ||
-          static_cast<long long>(n_of[i]) + new_of[i] > most) {
-        err = kErrBadBlock;
-        n_of[i] = new_of[i] = 0;
-      }
-      mine.x += new_of[i];
-      mine.y += (n_of[i] + new_of[i] + kBlockSize - 1) / kBlockSize -
-                (n_of[i] + kBlockSize - 1) / kBlockSize;
+  for (int b = b0; b < b1; ++b) {
+    const int n = p.context_lens[b], k = p.new_lens[b];
+    if (n < 0 || k < 0 || static_cast<long long>(n) + k > most) {
+      err = kErrBadBlock;
+    } else {
+      mine.x += k;
+      mine.y += blocks_for(n + k) - blocks_for(n);
     }
   }
-  const int count = *p.free_count;
   longlong2 sum;
-  longlong2 at = block_scan(mine, &sum);
+  longlong2 at = block_scan<kThreads>(mine, &sum);
   if (sum.x > p.num_tokens || count < 0 || count > p.num_blocks) err = kErrBadBlock;
-  else if (sum.y > count) err = KVP_ERR_OOM;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = b0 + i;
-    if (i < per && b < p.batch) {
-      tok0[b] = static_cast<int32_t>(at.x);
-      blk0[b] = static_cast<int32_t>(at.y);
-      len[b] = n_of[i];
-      at.x += new_of[i];
-      at.y += (n_of[i] + new_of[i] + kBlockSize - 1) / kBlockSize -
-              (n_of[i] + kBlockSize - 1) / kBlockSize;
-    }
+  else if (sum.y > count && err == 0) err = KVP_ERR_OOM;
+  for (int b = b0; b < b1; ++b) {  // (wrong lengths give wrong offsets, which nothing uses)
+    const int n = p.context_lens[b], k = p.new_lens[b];
+    tok0[b] = static_cast<int32_t>(at.x);
+    blk0[b] = static_cast<int32_t>(at.y);
+    len[b] = n;
+    at.x += k;
+    at.y += blocks_for(n + k) - blocks_for(n);
   }
   err = __syncthreads_or(err == kErrBadBlock) ? kErrBadBlock
                                               : (__syncthreads_or(err) ? KVP_ERR_OOM : 0);
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablePara
       *p.free_count_out = count;
     }
     for (int b = first; b <= p.batch; b += stride) p.query_start[b] = 0;
-    for (int t = first; t < p.num_tokens; t += stride) {
+    for (int t = first; t < (p.num_tokens > kFusedTokens ? 0 : p.num_tokens); t += stride) {
       p.slot_mapping[t] = -1;
       if (p.positions != nullptr) p.positions[t] = 0;
     }
@@ -193,16 +203,16 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablePara
   }
   for (int j = first; j < blocks; j += stride) {
     const int b = find_request(blk0, p.batch, j);
-    const int i = (len[b] + kBlockSize - 1) / kBlockSize + j - blk0[b];
+    const int i = blocks_for(len[b]) + j - blk0[b];
     p.block_tables[static_cast<size_t>(b) * p.max_blocks + i] = p.free_blocks[count - 1 - j];
   }
+  if (p.num_tokens > kFusedTokens) return;
   for (int t = first; t < p.num_tokens; t += stride) {
     int slot = -1, pos = 0;
     if (t < tokens) {
       const int b = find_request(tok0, p.batch, t);
       pos = len[b] + t - tok0[b];
-      const int i = pos / kBlockSize;
-      const int have = (len[b] + kBlockSize - 1) / kBlockSize;
+      const int i = pos / kBlockSize, have = blocks_for(len[b]);
       const int id = i < have ? p.block_tables[static_cast<size_t>(b) * p.max_blocks + i]
                               : p.free_blocks[count - 1 - (blk0[b] + i - have)];
       slot = id * kBlockSize + pos % kBlockSize;
@@ -212,6 +222,60 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablePara
   }
 }
 
+// Slots and positions of many tokens, from what the first launch wrote: request
+// b's new tokens are query_start[b] .. query_start[b + 1] - 1, the last ones of
+// its context_lens_out[b].  A CTA takes kFillTokens of them; its first and last
+// request are found by two warps, and the offsets between them come on chip.
+__global__ void __launch_bounds__(kFillThreads) fill_slots_kernel(const TableParams p) {
+  __shared__ int32_t start[kFillTokens + 1], before[kFillTokens];
+  __shared__ int range[2];
+  dev::grid_dependency_wait();
+  dev::launch_dependents();
+  const int t0 = blockIdx.x * kFillTokens, t1 = min(t0 + kFillTokens, p.num_tokens);
+  const int tokens = p.query_start[p.batch];
+  const int warp = threadIdx.x >> 5;
+  if (t0 < tokens && warp < 2) {
+    const int b = warp_find_request(p.query_start, p.batch,
+                                    warp == 0 ? t0 : min(t1, tokens) - 1);
+    if ((threadIdx.x & 31) == 0) range[warp] = b;
+  }
+  __syncthreads();
+  int b0 = 0, n = 0;
+  if (t0 < tokens) {
+    b0 = range[0];
+    n = range[1] - b0 + 1;
+  }
+  // (requests without new tokens can make the range longer than the tokens)
+  const bool on_chip = n <= kFillTokens;
+  if (on_chip) {
+    for (int i = threadIdx.x; i < n; i += kFillThreads) {
+      const int s = p.query_start[b0 + i];
+      start[i] = s;
+      before[i] = p.context_lens_out[b0 + i] - (p.query_start[b0 + i + 1] - s);
+    }
+  }
+  __syncthreads();
+  for (int t = t0 + threadIdx.x; t < t1; t += kFillThreads) {
+    int slot = -1, pos = 0;
+    if (t < tokens) {
+      int b;
+      if (on_chip) {
+        const int i = find_request(start, n, t);
+        b = b0 + i;
+        pos = before[i] + t - start[i];
+      } else {
+        b = b0 + find_request(p.query_start + b0, n, t);
+        pos = p.context_lens_out[b] - (p.query_start[b + 1] - t);
+      }
+      slot = p.block_tables[static_cast<size_t>(b) * p.max_blocks + pos / kBlockSize] * kBlockSize +
+             pos % kBlockSize;
+    }
+    p.slot_mapping[t] = slot;
+    if (p.positions != nullptr) p.positions[t] = pos;
+  }
+}
+
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) release_tables_kernel(const TableParams p) {
   extern __shared__ int32_t smem[];
   int32_t* blk0 = smem;  // [batch] first released block
@@ -224,32 +288,21 @@ __global__ void __launch_bounds__(kThreads) release_tables_kernel(const TablePar
 
   int err = 0;
   const int per = (p.batch + kThreads - 1) / kThreads;
-  const int b0 = threadIdx.x * per;
-  int nb[kPerThread];
-  longlong2 mine = make_longlong2(0, 0);
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = b0 + i;
-    nb[i] = 0;
-    if (i < per && b < p.batch) {
-      const int n = p.context_lens[b];
-      if (n < 0 || n > most) err = kErrBadBlock;
-      else if (p.finished[b] != 0) nb[i] = (n + kBlockSize - 1) / kBlockSize;
-      mine.y += nb[i];
-    }
-  }
+  const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
   const int count = *p.free_count;
+  longlong2 mine = make_longlong2(0, 0);
+  for (int b = b0; b < b1; ++b) {
+    const int n = p.context_lens[b];
+    if (n < 0 || n > most) err = kErrBadBlock;
+    else if (p.finished[b] != 0) mine.y += blocks_for(n);
+  }
   longlong2 sum;
-  longlong2 at = block_scan(mine, &sum);
+  longlong2 at = block_scan<kThreads>(mine, &sum);
   if (count < 0 || count > p.num_blocks) err = kErrBadBlock;
   else if (count + sum.y > p.num_blocks && err == 0) err = KVP_ERR_REFCOUNT;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = b0 + i;
-    if (i < per && b < p.batch) {
-      blk0[b] = static_cast<int32_t>(at.y);
-      at.y += nb[i];
-    }
+  for (int b = b0; b < b1; ++b) {
+    blk0[b] = static_cast<int32_t>(at.y);
+    if (p.finished[b] != 0) at.y += blocks_for(p.context_lens[b]);
   }
   err = __syncthreads_or(err == kErrBadBlock) ? kErrBadBlock
                                               : (__syncthreads_or(err) ? KVP_ERR_REFCOUNT : 0);
@@ -280,18 +333,20 @@ __global__ void __launch_bounds__(kThreads) release_tables_kernel(const TablePar
     p.context_lens_out[b] = p.finished[b] != 0 ? 0 : p.context_lens[b];
 }
 
-cudaError_t launch_tables(void (*kernel)(TableParams), const TableParams& p, long long items,
-                          int arrays, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(arrays) * kMaxTableBatch * sizeof(int32_t);
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem);
+// One launch of `threads` threads per CTA for about `items` words of work, with
+// `arrays` words per request in shared memory: one CTA up to two items a thread,
+// then a cluster of as many as the items fill, up to the portable 8.
+cudaError_t launch_tables(void (*kernel)(TableParams), int threads, const TableParams& p,
+                          long long items, int arrays, cudaStream_t s) {
+  const cudaError_t e =
+      ensure_smem_attr(reinterpret_cast<const void*>(kernel),
+                       static_cast<size_t>(arrays) * kMaxTableBatch * sizeof(int32_t));
   if (e != cudaSuccess) return e;
-  // one CTA up to two items a thread, then as many as the items fill, up to
-  // the 8 of a portable cluster
   unsigned ctas = 1;
-  while (ctas < 8 && items > static_cast<long long>(ctas) * 2 * kThreads) ctas *= 2;
+  while (ctas < 8 && items > static_cast<long long>(ctas) * 2 * threads) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(arrays) * p.batch * sizeof(int32_t);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -309,15 +364,23 @@ cudaError_t launch_tables(void (*kernel)(TableParams), const TableParams& p, lon
 }  // namespace
 
 cudaError_t launch_extend_tables(const TableParams& p, cudaStream_t s) {
-  return launch_tables(&extend_tables_kernel, p,
-                       static_cast<long long>(p.num_tokens) + p.batch, 3, s);
+  const bool fused = p.num_tokens <= kFusedTokens;
+  const long long items =
+      p.batch + (fused ? p.num_tokens : p.num_tokens / kBlockSize);  // slots, or table entries
+  const cudaError_t e = items <= 512 ? launch_tables(&extend_tables_kernel<256>, 256, p, items, 3, s)
+                                     : launch_tables(&extend_tables_kernel<1024>, 1024, p, items,
+                                                     3, s);
+  if (e != cudaSuccess || fused) return e;
+  return launch_pdl(fill_slots_kernel, dim3((p.num_tokens - 1) / kFillTokens + 1),
+                    dim3(kFillThreads), 0, s, p);
 }
 
 cudaError_t launch_release_tables(const TableParams& p, cudaStream_t s) {
-  // the blocks that come back are only known on the device; a quarter of the
+  // the blocks that come back are only known on the device; an eighth of the
   // requests at a quarter of the table's width is a busy step
-  return launch_tables(&release_tables_kernel, p,
-                       static_cast<long long>(p.batch) * (1 + p.max_blocks / 16), 1, s);
+  const long long items = static_cast<long long>(p.batch) * (1 + p.max_blocks / 32);
+  return items <= 512 ? launch_tables(&release_tables_kernel<256>, 256, p, items, 1, s)
+                      : launch_tables(&release_tables_kernel<1024>, 1024, p, items, 1, s);
 }
 
 }  // namespace kvp

@@ -117,6 +117,48 @@ def test_extend_a_prompt_across_clusters():
             g["starts"].tolist(), g["pos"].tolist()) == want
 
 
+@pytest.mark.parametrize("B", [3, 700, 5000])
+def test_extend_many_tokens(B):
+    """More tokens than the planning launch lists itself: requests without new
+    tokens between the others, a request longer than a CTA's share, padding
+    behind."""
+    rnd = random.Random(B)
+    lens = [rnd.randint(0, 40) for _ in range(B)]
+    new = [rnd.choice([0, 0, 0, 1, 5, 30000 // B]) for _ in range(B)]
+    new[B // 2] = 4000
+    T = max(sum(new), 16385) + 1500
+    MB = -(-(max(new) + 40) // 16)
+    p = Plan(lens, MB, sum(-(-(n + k) // 16) for n, k in zip(lens, new)) + 3, seed=B)
+    g = p.gpu(T)
+    lo, co = p.extend(new)
+    want = plain64.extend(p.tables, lens, new, p.free, p.count, T)
+    assert kvp.kvp_read_status(g["status"]) == kvp.KVP_OK
+    got = (g["tables"].tolist(), lo.tolist(), int(co), g["slots"].tolist(), g["starts"].tolist(),
+           g["pos"].tolist())
+    for a, b in zip(got, want):
+        assert a == b
+    # and nothing of it when a block is missing
+    p.count = 0
+    g = p.gpu(T)
+    lo, co = p.extend(new, in_place=True)
+    assert kvp.kvp_read_status(g["status"]) == kvp.KVP_ERR_OOM
+    assert lo.tolist() == lens and (g["slots"] == -1).all() and (g["pos"] == 0).all()
+    assert (g["starts"] == 0).all() and g["tables"].tolist() == p.tables
+
+
+def test_extend_long_runs_of_requests_without_new_tokens():
+    """A CTA's first and last request lie further apart than it has tokens."""
+    B, T = 12000, 17000
+    lens, new = [3] * B, [0] * B
+    new[1], new[B - 2], new[B - 1] = 700, 700, 15500
+    p = Plan(lens, 1000, B + 1100)
+    g = p.gpu(T)
+    lo, co = p.extend(new)
+    want = plain64.extend(p.tables, lens, new, p.free, p.count, T)
+    assert g["slots"].tolist() == want[3] and g["pos"].tolist() == want[5]
+    assert g["starts"].tolist() == want[4] and lo.tolist() == want[1]
+
+
 def test_extend_without_positions_or_tokens_or_requests():
     p = Plan([16, 3], 4, 9)
     g = p.gpu(4)
