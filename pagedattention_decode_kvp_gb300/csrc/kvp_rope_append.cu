@@ -30,7 +30,7 @@
 namespace kvp {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
 // Two 16-byte chunks of a row, as packed 16-bit pairs.
 struct RowPair {
@@ -148,88 +148,152 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 }
 
 // Codes of 8 elements (element e in bits 4e .. 4e + 3).  With d = x - z, the
-// FMA d * (1/s) + 1.5 * 2^23 rounds the quotient once to an integer held in the
-// low mantissa bits.  d * (1/s) is within 15 * 2^-22 of the IEEE quotient, so
-// both round alike unless the fraction is within 1e-4 of a half; such an
-// element takes the quotient itself.  So does every element when s or 1/s
-// leaves the normal range (`exact`), where that bound does not hold.
-__device__ __forceinline__ uint32_t quantise8_u4(const float (&x)[8], float s, float z) {
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  constexpr float kBand = 0.5f - 1.0e-4f;
-  const bool exact = s > 0.f && !(s >= 1.17549435e-38f && s <= 8.5070592e37f);
-  const float inv = (s > 0.f && !exact) ? __frcp_rn(s) : 0.f;
-  uint32_t word = 0u - 0x4b400000u * 0x11111111u;  // minus every element's magic bits
-  float far = 0.f;
-  uint32_t k[8];
-  float d[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    d[e] = __fsub_rn(x[e], z);
-    const float m = __fmaf_rn(d[e], inv, kMagic);
-    far = fmaxf(far, fabsf(__fmaf_rn(d[e], inv, kMagic - m)));
-    k[e] = __float_as_uint(fminf(m, kMagic + 15.f));
-  }
-  if (far > kBand || exact) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      k[e] = __float_as_uint(__fadd_rn(kMagic, fminf(rintf(__fdiv_rn(d[e], s)), 15.f)));
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) word += k[e] << (4 * e);
-  return word;
+// product d * (1/s) is taken with 1/s made 2^-21 smaller and 2^-21 larger; adding
+// 1.5 * 2^23 rounds each to an integer held in the low mantissa bits.  The two
+// bracket the IEEE quotient (1/s and the brackets' own roundings move them by
+// less than 2^-22), so where they agree that integer is the quotient's; where
+// they do not -- ties, nearly -- the quotient itself decides.  A negative s stands
+// for -s with quotients for all elements (see store_rows_int4).
+struct Bracket {
+  float lo, hi;  // 1/s, less and more
+};
+
+__device__ __forceinline__ Bracket bracket(float inv) {
+  return {inv * (1.f - 0x1p-21f), inv * (1.f + 0x1p-21f)};
 }
 
-// Quantise the row shared by the D / 16 lanes of `mask` and write its codes and
-// (scale, zero) pairs.
+// Nibbles of 8 words' low bytes.
+__device__ __forceinline__ uint32_t pack_nibbles(const uint32_t (&k)[8]) {
+  const uint32_t even = dev::prmt(dev::prmt(k[0], k[2], 0x0040u), dev::prmt(k[4], k[6], 0x0040u),
+                                  0x5410u);
+  const uint32_t odd = dev::prmt(dev::prmt(k[1], k[3], 0x0040u), dev::prmt(k[5], k[7], 0x0040u),
+                                 0x5410u);
+  return odd * 16u + even;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t quantise8_u4(const uint4& raw, float s, float z, Bracket b) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  const uint64_t nz2 = dev::f2pack(-z, -z), magic2 = dev::f2pack(kMagic, kMagic);
+  const uint64_t lo2 = dev::f2pack(b.lo, b.lo), hi2 = dev::f2pack(b.hi, b.hi);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  const uint64_t minus2 = dev::f2pack(-1.f, -1.f);
+  uint32_t k[8];
+  uint64_t more2[4], sum2 = 0;  // n - m >= 0: 1 where the brackets do not agree
+  float d[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = dev::unpack2<kBf16>(w[i]);
+    const uint64_t d2 = dev::fadd2(dev::f2pack(x.x, x.y), nz2);
+    const float2 du = dev::f2unpack(d2);
+    const float2 mu = dev::f2unpack(dev::ffma2(d2, lo2, magic2));
+    more2[i] = dev::ffma2(dev::f2pack(mu.x, mu.y), minus2, dev::ffma2(d2, hi2, magic2));
+    sum2 = dev::fadd2(sum2, more2[i]);
+    d[2 * i] = du.x;
+    d[2 * i + 1] = du.y;
+    k[2 * i] = __float_as_uint(mu.x);
+    k[2 * i + 1] = __float_as_uint(mu.y);
+  }
+  const float2 sum = dev::f2unpack(sum2);
+  if (sum.x + sum.y > 0.f || s < 0.f) {
+    const bool slow = s < 0.f;
+    const float sa = fabsf(s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 u = dev::f2unpack(more2[e / 2]);
+      if ((e % 2 == 0 ? u.x : u.y) > 0.f || slow)
+        k[e] = __float_as_uint(kMagic + fminf(rintf(__fdiv_rn(d[e], sa)), 15.f));
+    }
+  }
+  return pack_nibbles(k);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t min8(const uint4& r) {
+  return min2<kBf16>(min2<kBf16>(r.x, r.y), min2<kBf16>(r.z, r.w));
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t max8(const uint4& r) {
+  return max2<kBf16>(max2<kBf16>(r.x, r.y), max2<kBf16>(r.z, r.w));
+}
+
+// Smallest and largest of a row's groups over this lane's chunks: of group 0 in
+// the low half, of group 1 in the high one.
 template <bool kBf16, int D>
-__device__ __forceinline__ void store_row_int4(const RowPair& r, const LaneChunks& k, int c,
-                                               uint32_t mask, uint8_t* codes, uint32_t* sz) {
-  constexpr int L = D / 16;
-  uint32_t mna = min2<kBf16>(min2<kBf16>(r.a.x, r.a.y), min2<kBf16>(r.a.z, r.a.w));
-  uint32_t mnb = min2<kBf16>(min2<kBf16>(r.b.x, r.b.y), min2<kBf16>(r.b.z, r.b.w));
-  uint32_t mxa = max2<kBf16>(max2<kBf16>(r.a.x, r.a.y), max2<kBf16>(r.a.z, r.a.w));
-  uint32_t mxb = max2<kBf16>(max2<kBf16>(r.b.x, r.b.y), max2<kBf16>(r.b.z, r.b.w));
-  uint32_t lo, hi;  // smallest and largest: of group 0 in the low half, of group 1 in the high
+__device__ __forceinline__ void row_range(const RowPair& r, const LaneChunks& k, uint32_t& lo,
+                                          uint32_t& hi) {
+  uint32_t mna = min8<kBf16>(r.a), mnb = min8<kBf16>(r.b);
+  uint32_t mxa = max8<kBf16>(r.a), mxb = max8<kBf16>(r.b);
   if constexpr (D == 64) {
     lo = min2<kBf16>(mna, mnb);
     hi = max2<kBf16>(mxa, mxb);
     lo = min2<kBf16>(lo, __byte_perm(lo, lo, 0x1032));
     hi = max2<kBf16>(hi, __byte_perm(hi, hi, 0x1032));
   } else {
-    constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
+    constexpr uint32_t kInf = (kBf16 ? 0x7f80u : 0x7c00u) * 0x10001u, kSign = 0x80008000u;
     mna = min2<kBf16>(mna, __byte_perm(mna, mna, 0x1032));
     mnb = min2<kBf16>(mnb, __byte_perm(mnb, mnb, 0x1032));
     mxa = max2<kBf16>(mxa, __byte_perm(mxa, mxa, 0x1032));
     mxb = max2<kBf16>(mxb, __byte_perm(mxb, mxb, 0x1032));
     const uint32_t in_a = (k.a * 8 < 64) ? 0x0000ffffu : 0xffff0000u;
     const uint32_t in_b = (k.b * 8 < 64) ? 0x0000ffffu : 0xffff0000u;
-    lo = min2<kBf16>((mna & in_a) | ((kInf * 0x10001u) & ~in_a),
-                     (mnb & in_b) | ((kInf * 0x10001u) & ~in_b));
-    hi = max2<kBf16>((mxa & in_a) | (((kInf | 0x8000u) * 0x10001u) & ~in_a),
-                     (mxb & in_b) | (((kInf | 0x8000u) * 0x10001u) & ~in_b));
+    lo = min2<kBf16>((mna & in_a) | (kInf & ~in_a), (mnb & in_b) | (kInf & ~in_b));
+    hi = max2<kBf16>((mxa & in_a) | ((kInf | kSign) & ~in_a),
+                     (mxb & in_b) | ((kInf | kSign) & ~in_b));
   }
+}
+
+// Quantise a K and a V row, shared by the D / 16 lanes whose `c` count from 0, and
+// write codes and (scale, zero) pairs.  All lanes of the warp call it; `store`
+// tells whether this lane's rows exist.  The rows have 2 D / 64 groups, and the
+// divisions for a group -- the scale and its reciprocal -- are done by one lane
+// each and passed round.
+template <bool kBf16, int D>
+__device__ __forceinline__ void store_rows_int4(const RowPair& x, const RowPair& y,
+                                                const LaneChunks& k, int c, bool store,
+                                                const RowParams& p, size_t srow) {
+  constexpr int L = D / 16, kG = D / 64;
+  uint32_t lo[2], hi[2];  // K, V
+  row_range<kBf16, D>(x, k, lo[0], hi[0]);
+  row_range<kBf16, D>(y, k, lo[1], hi[1]);
 #pragma unroll
   for (int o = L / 2; o >= 1; o >>= 1) {
-    lo = min2<kBf16>(lo, __shfl_xor_sync(mask, lo, o));
-    hi = max2<kBf16>(hi, __shfl_xor_sync(mask, hi, o));
-  }
-  const float2 z = dev::unpack2<kBf16>(lo), top = dev::unpack2<kBf16>(hi);
-  const uint32_t sp = dev::pack2<kBf16>(__fdiv_rn(__fsub_rn(top.x, z.x), 15.f),
-                                        __fdiv_rn(__fsub_rn(top.y, z.y), 15.f));
-  const float2 s = dev::unpack2<kBf16>(sp);
-  float x[8];
-  const bool ga = D > 64 && k.a * 8 >= 64, gb = D > 64 && k.b * 8 >= 64;
-  unpack8<kBf16>(r.a, x);
-  *reinterpret_cast<uint32_t*>(codes + k.a * 4) = quantise8_u4(x, ga ? s.y : s.x, ga ? z.y : z.x);
-  unpack8<kBf16>(r.b, x);
-  *reinterpret_cast<uint32_t*>(codes + k.b * 4) = quantise8_u4(x, gb ? s.y : s.x, gb ? z.y : z.x);
-  if (c == 0) {
-    if constexpr (D == 64) {
-      sz[0] = __byte_perm(sp, lo, 0x5410);
-    } else {
-      *reinterpret_cast<uint2*>(sz) =
-          make_uint2(__byte_perm(sp, lo, 0x5410), __byte_perm(sp, lo, 0x7632));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lo[i] = min2<kBf16>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      hi[i] = max2<kBf16>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
     }
+  }
+  // lane c: group c % kG of K (c / kG even) or V
+  const bool of_v = (c / kG) % 2 != 0, high = kG == 2 && c % 2 != 0;
+  const uint32_t my_lo = of_v ? lo[1] : lo[0], my_hi = of_v ? hi[1] : hi[0];
+  const float2 zz = dev::unpack2<kBf16>(my_lo), tt = dev::unpack2<kBf16>(my_hi);
+  const float range = high ? __fsub_rn(tt.y, zz.y) : __fsub_rn(tt.x, zz.x);
+  const uint32_t sp = dev::pack2<kBf16>(__fdiv_rn(range, 15.f), 0.f);
+  const float s = dev::unpack2<kBf16>(sp).x;
+  // Below the 16-bit type's normal range the scale's own rounding can push codes
+  // past 15, and outside [2^-126, 2^126] the brackets do not hold: such groups
+  // take the quotients (a negative scale is passed round).
+  const bool fits = s >= (kBf16 ? 0x1p-126f : 0x1p-14f) && s <= 0x1p126f;
+  const float inv = fits ? __fdiv_rn(1.f, s) : 0.f;
+  const float signed_s = fits ? s : -s;
+  if (store && c < 2 * kG) {
+    const uint32_t pair = __byte_perm(sp, my_lo, high ? 0x7610 : 0x5410);
+    (of_v ? p.v_sz : p.k_sz)[srow * kG + c % kG] = pair;
+  }
+  const int base = (threadIdx.x & 31) - c;
+  const int ga = kG == 2 && k.a * 8 >= 64 ? 1 : 0, gb = kG == 2 && k.b * 8 >= 64 ? 1 : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // K and V, chunks a and b
+    const int g = i % 2 == 0 ? ga : gb;
+    const float2 z = dev::unpack2<kBf16>(lo[i / 2]);
+    const float in = __shfl_sync(0xffffffffu, inv, base + i / 2 * kG + g);
+    const float sc = __shfl_sync(0xffffffffu, signed_s, base + i / 2 * kG + g);
+    const RowPair& r = i < 2 ? x : y;
+    const uint32_t word =
+        quantise8_u4<kBf16>(i % 2 == 0 ? r.a : r.b, sc, g ? z.y : z.x, bracket(in));
+    uint8_t* codes = static_cast<uint8_t*>(i < 2 ? p.k_cache : p.v_cache) + srow * (D / 2);
+    if (store) *reinterpret_cast<uint32_t*>(codes + (i % 2 == 0 ? k.a : k.b) * 4) = word;
   }
 }
 
@@ -264,9 +328,10 @@ __device__ __forceinline__ void load_angles(const RowParams& p, const int (&pos)
 // token.  A slot takes the token's units r, r + step, ...: query rows first,
 // then (K, V) row pairs of the kv heads; gridDim.y CTAs share a token's units.
 template <bool kBf16, int D, bool kRope, bool kInt4>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kRowThreads, kRope ? 6 : 8) row_kernel(const RowParams p) {
   constexpr int L = D / 16;
   constexpr int kSlots = kRowThreads / L;
+  constexpr int kWarpRows = 32 / L;  // row slots of a warp, all on one token (row_lanes >= 8)
   dev::grid_dependency_wait();
   dev::launch_dependents();
   const int c = threadIdx.x % L;
@@ -326,87 +391,106 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const RowParams p) {
         }
       }
     }
-    // back to this slot's first unit at or past the query rows
-    r = unit0 >= nq ? unit0 : unit0 + (nq - unit0 + step - 1) / step * step;
+    // back to the first unit at which one of the warp's slots is past the query rows
+    const int last = unit0 + kWarpRows - 1 - (threadIdx.x & 31) / L;
+    r = last >= nq ? unit0 : unit0 + (nq - last + step - 1) / step * step;
   }
-  const uint32_t mask = ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
+  // K and V rows.  A warp's row slots lie on one token, so all its lanes come
+  // here together; the loop runs until the warp's first slot is done.
   const uint16_t* kr = p.key + t * p.k_stride;
   const uint16_t* vr = p.value + t * p.v_stride;
-  for (; r < nq + p.num_kv_heads; r += step) {
+  const int lead = (threadIdx.x & 31) / L;  // this lane's slot in the warp
+  for (; r - lead < nq + p.num_kv_heads; r += step) {
     const int h = r - nq;
-    RowPair x = load_pair(kr + h * D, k.a, k.b);
-    const RowPair y = load_pair(vr + h * D, k.a, k.b);
+    const bool live = h >= 0 && h < p.num_kv_heads;
+    const int hc = min(max(h, 0), p.num_kv_heads - 1);  // (lanes without a row redo one)
+    RowPair x = load_pair(kr + hc * D, k.a, k.b);
+    const RowPair y = load_pair(vr + hc * D, k.a, k.b);
     if constexpr (kRope) rotate<kBf16>(x, k, p.interleaved != 0, cs, sn);
     const size_t srow =
         (static_cast<size_t>(slot / kBlockSize) * p.num_kv_heads + h) * kBlockSize +
         slot % kBlockSize;
     if constexpr (kInt4) {
-      store_row_int4<kBf16, D>(x, k, c, mask, static_cast<uint8_t*>(p.k_cache) + srow * (D / 2),
-                               p.k_sz + srow * (D / 64));
-      store_row_int4<kBf16, D>(y, k, c, mask, static_cast<uint8_t*>(p.v_cache) + srow * (D / 2),
-                               p.v_sz + srow * (D / 64));
-    } else {
+      store_rows_int4<kBf16, D>(x, y, k, c, live, p, srow);
+    } else if (live) {
       store_pair(static_cast<uint16_t*>(p.k_cache) + srow * D, k.a, k.b, x);
       store_pair(static_cast<uint16_t*>(p.v_cache) + srow * D, k.a, k.b, y);
     }
   }
 }
 
-// Values of 16 codes (8 bytes) with one (scale, zero) pair, as two 16-byte
-// chunks: s * c is exact in float32 (11 + 4 bits), so the FMA rounds s * c + z
-// once to float32 before the 16-bit rounding.
+// Values of 8 codes with their (scale, zero) pair, as a 16-byte chunk.  A code
+// moved to the bottom of a word under the exponent of 2^23 is 2^23 + c; s * c is
+// exact in float32 (11 + 4 bits), so the FMA rounds s * c + z once to float32
+// before the 16-bit rounding.
 template <bool kBf16>
-__device__ __forceinline__ void dequant16(uint2 w, uint32_t sz, uint4 (&out)[2]) {
+__device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sz) {
   const float2 f = dev::unpack2<kBf16>(sz);
-  const uint32_t word[2] = {w.x, w.y};
+  const uint64_t s2 = dev::f2pack(f.x, f.x), z2 = dev::f2pack(f.y, f.y);
+  const uint64_t base2 = dev::f2pack(-8388608.f, -8388608.f);
+  uint32_t v[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      x[e] = __fmaf_rn(f.x, static_cast<float>((word[i] >> (4 * e)) & 15u), f.y);
-    out[i] = pack8<kBf16>(x);
+  for (int e = 0; e < 4; ++e) {
+    const float a = __uint_as_float(((w >> (8 * e)) & 15u) | 0x4b000000u);
+    const float b = __uint_as_float(((w >> (8 * e + 4)) & 15u) | 0x4b000000u);
+    const float2 x = dev::f2unpack(dev::ffma2(dev::fadd2(dev::f2pack(a, b), base2), s2, z2));
+    v[e] = dev::pack2<kBf16>(x.x, x.y);
   }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// One lane per 16 elements of a row of K and of V: grid.x over tokens, the
-// heads of a token over its lanes.
+// A warp per token and 512 / D heads: lane (head, c) of L = D / 16 lanes per head
+// writes the 16-byte chunks c and c + L of K and of V, so that a store covers
+// whole sectors.
 template <bool kBf16, int D>
-__global__ void __launch_bounds__(256) read_int4_kernel(
+__global__ void __launch_bounds__(128) read_int4_kernel(
     uint4* __restrict__ key, uint4* __restrict__ value, const uint8_t* __restrict__ kc,
     const uint8_t* __restrict__ vc, const uint32_t* __restrict__ ksz,
     const uint32_t* __restrict__ vsz, const int32_t* __restrict__ slots, int num_tokens,
     int num_kv_heads, int num_slots, int32_t* status) {
-  constexpr int L = D / 16;
+  constexpr int L = D / 16, kHeads = 32 / L;
   dev::grid_dependency_wait();
   dev::launch_dependents();
-  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long row = i / L;  // token * Hkv + head
-  const int c = static_cast<int>(i % L);
-  const long long t = row / num_kv_heads;
-  const int h = static_cast<int>(row % num_kv_heads);
+  const int lane = threadIdx.x & 31, c = lane % L;
+  const long long t = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (t >= num_tokens) return;
   const int slot = slots[t];
-  if (slot < 0) return;  // padding token: the row is left as it is
-  uint4 k2[2], v2[2];
-  if (slot >= num_slots) {
-    if (h == 0 && c == 0) dev::set_status(status, kErrBadBlock);
-    k2[0] = k2[1] = v2[0] = v2[1] = make_uint4(0u, 0u, 0u, 0u);
-  } else {
-    const size_t srow = (static_cast<size_t>(slot / kBlockSize) * num_kv_heads + h) * kBlockSize +
-                        slot % kBlockSize;
-    const int g = c / 4;  // 64 elements are 4 lanes
-    dequant16<kBf16>(*reinterpret_cast<const uint2*>(kc + srow * (D / 2) + c * 8),
-                     ksz[srow * (D / 64) + g], k2);
-    dequant16<kBf16>(*reinterpret_cast<const uint2*>(vc + srow * (D / 2) + c * 8),
-                     vsz[srow * (D / 64) + g], v2);
+  if (slot < 0) return;  // padding token: the rows are left as they are
+  const bool bad = slot >= num_slots;
+  if (bad && blockIdx.y == 0 && lane == 0) dev::set_status(status, kErrBadBlock);
+  const size_t row0 =
+      bad ? 0
+          : static_cast<size_t>(slot / kBlockSize) * num_kv_heads * kBlockSize + slot % kBlockSize;
+  uint4* ko = key + t * num_kv_heads * (D / 8) + c;
+  uint4* vo = value + t * num_kv_heads * (D / 8) + c;
+  const int h = blockIdx.y * kHeads + lane / L;
+  if (h < num_kv_heads) {
+    uint4 k2[2], v2[2];
+    if (bad) {
+      k2[0] = k2[1] = v2[0] = v2[1] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const size_t srow = row0 + static_cast<size_t>(h) * kBlockSize;
+      const uint32_t* kw = reinterpret_cast<const uint32_t*>(kc + srow * (D / 2)) + c;
+      const uint32_t* vw = reinterpret_cast<const uint32_t*>(vc + srow * (D / 2)) + c;
+      const uint32_t w[4] = {kw[0], kw[L], vw[0], vw[L]};
+      uint2 kp, vp;  // pairs of chunk c and of chunk c + L
+      if constexpr (D == 128) {
+        kp = *reinterpret_cast<const uint2*>(ksz + srow * 2);
+        vp = *reinterpret_cast<const uint2*>(vsz + srow * 2);
+      } else {
+        kp.x = kp.y = ksz[srow];
+        vp.x = vp.y = vsz[srow];
+      }
+      k2[0] = dequant8<kBf16>(w[0], kp.x);
+      k2[1] = dequant8<kBf16>(w[1], kp.y);
+      v2[0] = dequant8<kBf16>(w[2], vp.x);
+      v2[1] = dequant8<kBf16>(w[3], vp.y);
+    }
+    ko[h * (D / 8)] = k2[0];
+    ko[h * (D / 8) + L] = k2[1];
+    vo[h * (D / 8)] = v2[0];
+    vo[h * (D / 8) + L] = v2[1];
   }
-  uint4* ko = key + static_cast<size_t>(row) * (D / 8) + c * 2;
-  uint4* vo = value + static_cast<size_t>(row) * (D / 8) + c * 2;
-  ko[0] = k2[0];
-  ko[1] = k2[1];
-  vo[0] = v2[0];
-  vo[1] = v2[1];
 }
 
 template <bool kBf16, int D, bool kRope, bool kInt4>
@@ -450,12 +534,12 @@ cudaError_t launch_read_int4(void* key, void* value, bool bf16, const uint8_t* k
                              const int32_t* slots, int num_tokens, const kvp_cache_desc& c,
                              int32_t* status, cudaStream_t s) {
   if (num_tokens == 0) return cudaSuccess;
-  const long long lanes = static_cast<long long>(num_tokens) * c.num_kv_heads * (c.head_dim / 16);
-  const dim3 grid(static_cast<unsigned>((lanes + 255) / 256));
+  const int groups = (c.num_kv_heads * (c.head_dim / 16) + 31) / 32;  // of heads, a warp each
+  const dim3 grid(static_cast<unsigned>((num_tokens - 1) / 4 + 1), static_cast<unsigned>(groups));
   const int nslots = c.num_blocks * kBlockSize;
 #define KVP_READ_CASE(BF, DD)                                                                   \
   if (bf16 == BF && c.head_dim == DD)                                                           \
-    return launch_pdl(read_int4_kernel<BF, DD>, grid, dim3(256), 0, s, static_cast<uint4*>(key), \
+    return launch_pdl(read_int4_kernel<BF, DD>, grid, dim3(128), 0, s, static_cast<uint4*>(key), \
                       static_cast<uint4*>(value), kc, vc, static_cast<const uint32_t*>(ksz),    \
                       static_cast<const uint32_t*>(vsz), slots, num_tokens, c.num_kv_heads,     \
                       nslots, status);
