@@ -621,14 +621,16 @@ __device__ __forceinline__ bool find_piece(const DecodeParams& p, int index, int
     walk.n = p.context_lens[b];
     walk.nblk = nblk;
     walk.blk0 = static_cast<int>(pos - at);
-    walk.left = walk.flags = 0;
+    walk.left = walk.flags = walk.runs = 0;
   }
   __syncthreads();
   return true;
 }
 
-// One thread: the walk's next segment.
-__device__ __forceinline__ void next_segment(const DecodeParams& p, Walk& walk, Segment& seg) {
+// One thread: the walk's next segment.  `ahead` is the length of the context
+// behind walk.b, fetched by the call before.
+__device__ __forceinline__ void next_segment(const DecodeParams& p, Walk& walk, Segment& seg,
+                                             int& ahead) {
   int flags = walk.flags & ~kInit;
   if (walk.left == 0) {
     if (walk.pos >= walk.end) {
@@ -637,16 +639,26 @@ __device__ __forceinline__ void next_segment(const DecodeParams& p, Walk& walk, 
     }
     flags = (flags & kLater) | kInit;
     if (walk.blk0 == walk.nblk) {
-      do {
+      walk.n = ahead;
+      walk.nblk = blocks_of(p, ahead);
+      ++walk.b;
+      while (walk.nblk == 0) {
         walk.n = p.context_lens[++walk.b];
         walk.nblk = blocks_of(p, walk.n);
-      } while (walk.nblk == 0);
+      }
       walk.blk0 = 0;
+      ahead = p.context_lens[min(walk.b + 1, p.batch - 1)];
     }
     walk.left = static_cast<int>(
         min(static_cast<long long>(walk.nblk - walk.blk0), walk.end - walk.pos));
-    if (walk.blk0 == 0) flags |= walk.left == walk.nblk ? kWhole : kStart;
-    walk.runs = static_cast<int>((walk.pos + walk.nblk - 1) / walk.size) - walk.index + 1;
+    if (walk.blk0 == 0) {
+      if (walk.left == walk.nblk) {
+        flags |= kWhole;
+      } else {
+        flags |= kStart;
+        walk.runs = static_cast<int>((walk.pos + walk.nblk - 1) / walk.size) - walk.index + 1;
+      }
+    }
   }
   seg.b = walk.b;
   seg.blk0 = walk.blk0;
@@ -717,12 +729,14 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
       walk.n = n;
       walk.nblk = nblk;
       walk.blk0 = blk0;
-      walk.index = walk.left = walk.flags = 0;
+      walk.index = walk.left = walk.flags = walk.runs = 0;
     }
   }
+  int ahead = 0;
   if (threadIdx.x == 0) {
-    next_segment(p, walk, segs[0]);
-    next_segment(p, walk, segs[1]);
+    ahead = p.context_lens[min(walk.b + 1, p.batch - 1)];
+    next_segment(p, walk, segs[0], ahead);
+    next_segment(p, walk, segs[1], ahead);
   }
   __syncthreads();
 
@@ -838,7 +852,7 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
       __syncthreads();  // the merged states are read: their place is free
     }
     if (nb == 0) break;
-    if (threadIdx.x == 0) next_segment(p, walk, segs[(s + 2) & 3]);
+    if (threadIdx.x == 0) next_segment(p, walk, segs[(s + 2) & 3], ahead);
     if (seg.flags & kInit) Path::init(st, query, p.scale_log2, qs, lane);
 
     // ---- the segment's blocks
