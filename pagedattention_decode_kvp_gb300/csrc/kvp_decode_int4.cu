@@ -50,9 +50,9 @@
 //   * Blocks come by cp.async, 16 bytes per lane (5 instructions a block at
 //     D = 128 where an elected lane's bulk copies, barriers and fences took 64),
 //     each warp through a ring of its own that needs no barrier at all.
-// Rows t of the score fragment hold tokens in the order 4 (t % 2) + t / 2 (+ 8
-// in the upper half), and the two groups of a row change places in every other
-// pair of rows, so that neither the K nor the V loads meet in a bank.
+//   * The matrix loads (ldmatrix) bring a group's 64 codes of 16 tokens in one
+//     instruction, K as it lies and V transposed: for V that also sets the codes
+//     of two tokens side by side as the product wants them.
 #include "kvp_decode.cuh"
 
 namespace kvp {
@@ -85,10 +85,12 @@ __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Byte that 16-byte piece c of token row r takes in a block's code tile.
+// Byte that 16-byte piece c of token row r takes in a block's code tile: the
+// pieces of a row change places so that one piece of 8 rows lies in 8 different
+// groups of banks (a matrix load reads just that).
 template <int D>
 __device__ __forceinline__ int code_piece(int r, int c) {
-  const int swap = D == 128 ? 2 * (((r >> 1) ^ (r >> 2)) & 1) : 0;
+  const int swap = D == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
   return r * (D / 2) + ((c ^ swap) << 4);
 }
 
@@ -124,7 +126,7 @@ struct Int4Path {
     return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
   }
 
-  // This lane's 16 elements per group of query head g8.
+  // This lane's 16 elements per group of query head g8: 64 g + 32 w + 8 t4 ...
   struct Query {
     uint4 raw[kGroups][2];
   };
@@ -140,7 +142,7 @@ struct Int4Path {
       for (int w = 0; w < 2; ++w) {
         x.raw[g][w] = make_uint4(0u, 0u, 0u, 0u);
         if (g8 < nheads)
-          x.raw[g][w] = *reinterpret_cast<const uint4*>(q + 64 * g + 16 * t4 + 8 * w);
+          x.raw[g][w] = *reinterpret_cast<const uint4*>(q + 64 * g + 32 * w + 8 * t4);
       }
     }
   }
@@ -239,6 +241,13 @@ struct Int4Path {
     }
   }
 
+  // The row this lane addresses when the warp loads a group's codes of a tile as
+  // four 8 x 16-byte matrices: tokens 0-7 and 8-15 of its first piece, then of
+  // its second.
+  __device__ __forceinline__ static uint32_t matrix_at(int g, int lane) {
+    return code_piece<D>(lane & 15, 2 * g + (lane >> 4));
+  }
+
   // Scores of a step's blocks relative to the present reference (v = u - r) of
   // this lane's rows g8, g8 + 8 and heads 2 t4, 2 t4 + 1, and V's pairs of those
   // tokens.  kTail: only the first `valid` tokens count (other slots may hold
@@ -250,19 +259,15 @@ struct Int4Path {
                                                 float (&z0)[kStep][kGroups],
                                                 float (&s1)[kStep][kGroups],
                                                 float (&z1)[kStep][kGroups]) {
-    const int g8 = lane >> 2, t4 = lane & 3;
-    const int tok0 = 4 * (g8 & 1) + (g8 >> 1), tok1 = tok0 + 8;
+    const int tok0 = lane >> 2, tok1 = tok0 + 8;
     float acc[kStep][kGroups][4];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const int at = code_piece<D>(tok0, 2 * g + (t4 >> 1)) + 8 * (t4 & 1);
-      uint32_t wa[kStep][2], wb[kStep][2];
+      uint32_t wa[kStep][2], wb[kStep][2];  // of tokens g8 and g8 + 8: elements 64 g + 32 w + 8 t4 ...
 #pragma unroll
       for (int b = 0; b < kStep; ++b) {
-        const uint2 x = *reinterpret_cast<const uint2*>(tile + b * kStageBytes + at);
-        const uint2 y =
-            *reinterpret_cast<const uint2*>(tile + b * kStageBytes + at + 8 * (D / 2));
-        wa[b][0] = x.x, wa[b][1] = x.y, wb[b][0] = y.x, wb[b][1] = y.y;
+        dev::ldsm_x4(dev::smem_addr(tile + b * kStageBytes) + matrix_at(g, lane), wa[b][0], wb[b][0],
+                     wa[b][1], wb[b][1]);
         acc[b][g][0] = acc[b][g][1] = acc[b][g][2] = acc[b][g][3] = 0.f;
       }
 #pragma unroll
@@ -325,7 +330,6 @@ struct Int4Path {
   template <bool kTail>
   __device__ __forceinline__ static void consume(State& st, const uint4* qs, const uint8_t* tile,
                                                  int valid, bool first, int lane) {
-    const int g8 = lane >> 2, t4 = lane & 3;
     float v[kStep][4], s0[kStep][kGroups], z0[kStep][kGroups], s1[kStep][kGroups], z1[kStep][kGroups];
     scores<kTail>(st, qs, tile, valid, lane, v, s0, z0, s1, z1);
 
@@ -380,22 +384,21 @@ struct Int4Path {
     for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
       for (int b = 0; b < kStep; ++b) {
-        const uint8_t* vc = tile + b * kStageBytes + kCodeBytes;
         const uint32_t b0 = dev::movm_t(ap[b][g][0]);
         const uint32_t b1 = dev::movm_t(ap[b][g][1]);
-        uint32_t w[4];  // this lane's 8 codes of tokens t4, t4 + 4, t4 + 8, t4 + 12
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = *reinterpret_cast<const uint32_t*>(
-              vc + code_piece<D>(t4 + 4 * i, 2 * g + (g8 >> 2)) + 4 * (g8 & 3));
+        // transposed, a lane gets 4 codes, 64 g + 32 h + 4 g8 ..., of tokens 2 t4
+        // and 2 t4 + 1 (x), 2 t4 + 8 and 2 t4 + 9 (y): the product's operand pairs
+        uint32_t x[2], y[2];
+        dev::ldsm_x4_t(dev::smem_addr(tile + b * kStageBytes + kCodeBytes) + matrix_at(g, lane), x[0],
+                       y[0], x[1], y[1]);
         dev::mma16816<false>(st.as[g], kOnes, kOnes, kOnes, kOnes, b0, b1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // codes 0-3, then 4-7, of each token's word
-          const uint32_t x = dev::prmt(w[0], w[1], h == 0 ? 0x5410u : 0x7632u);
-          const uint32_t y = dev::prmt(w[2], w[3], h == 0 ? 0x5410u : 0x7632u);
-          const uint32_t xs = x >> 8, ys = y >> 8;
-          dev::mma16816<false>(st.o[g][2 * h], x & kLow, x & kHigh, y & kLow, y & kHigh, b0, b1);
-          dev::mma16816<false>(st.o[g][2 * h + 1], xs & kLow, xs & kHigh, ys & kLow, ys & kHigh, b0, b1);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t xs = x[h] >> 8, ys = y[h] >> 8;
+          dev::mma16816<false>(st.o[g][2 * h], x[h] & kLow, x[h] & kHigh, y[h] & kLow, y[h] & kHigh,
+                               b0, b1);
+          dev::mma16816<false>(st.o[g][2 * h + 1], xs & kLow, xs & kHigh, ys & kLow, ys & kHigh, b0,
+                               b1);
         }
       }
     }
@@ -469,9 +472,9 @@ struct Int4Path {
     }
   }
 
-  // The warp's state for the merge: per (group, head parity) and lane, the 8
-  // outputs d = 64 g + 8 g8 ... + 7 of head 2 t4 + i as two 16-byte words, each
-  // at a place of its own for all 32 lanes (no two in a bank).
+  // The warp's state for the merge: per (group, head parity i) and lane, outputs
+  // 64 g + 32 h + 4 g8 ... + 3 of head 2 t4 + i, a 16-byte word for each h, at a
+  // place of its own for all 32 lanes (no two in a bank).
   static constexpr int kParts = 2 * kGroups;  // (group, parity) pairs
   // It lies in the last step's place of the warp's ring.
   static constexpr int kMergeAt = (kBuf - 1) * kStep * kStageBytes;
@@ -508,13 +511,14 @@ struct Int4Path {
     }
   }
 
-  // Thread `tid` of the first 32 kParts merges 8 outputs of one head: their
-  // unnormalised sum, the reference M and the weight L (0 without tokens).
+  // Thread `tid` of the first 32 kParts merges 8 outputs of one head, d ... d + 3
+  // and d + 32 ... d + 35: their unnormalised sum, the reference M and the weight
+  // L (0 without tokens).
   __device__ __forceinline__ static void merge8(const uint8_t* rings, int tid, float (&o)[8],
                                                 float& M, float& L, int& head, int& d) {
     const int part = tid >> 5, lane = tid & 31;
     head = 2 * (lane & 3) + (part & 1);
-    d = 64 * (part >> 1) + 8 * (lane >> 2);
+    d = 64 * (part >> 1) + 4 * (lane >> 2);
     M = -INFINITY;
     L = 0.f;
     const float* of[kWarps];  // a warp's state
@@ -832,8 +836,9 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
             const float x = L > 0.f ? o[2 * e] * inv : 0.f, y = L > 0.f ? o[2 * e + 1] * inv : 0.f;
             w[e] = p.q_bf16 ? dev::pack2<true>(x, y) : dev::pack2<false>(x, y);
           }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row0 + hh) * D + d) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          uint2* to = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row0 + hh) * D + d);
+          to[0] = make_uint2(w[0], w[1]);
+          to[8] = make_uint2(w[2], w[3]);
         } else {
           const size_t prow =
               balanced ? (static_cast<size_t>(blockIdx.x) * 2 + (done_flags & kLater ? 1 : 0)) * H +
@@ -841,7 +846,7 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
                        : (row0 + hh) * p.max_parts + blockIdx.x;
           float4* to = reinterpret_cast<float4*>(p.ws_o + prow * D + d);
           to[0] = make_float4(o[0], o[1], o[2], o[3]);
-          to[1] = make_float4(o[4], o[5], o[6], o[7]);
+          to[8] = make_float4(o[4], o[5], o[6], o[7]);
           if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + 2 * prow) = make_float2(M, L);
         }
       }
