@@ -192,7 +192,9 @@ kvp_status kvp_copy_blocks(void* k_cache, void* v_cache, float* k_scale, float* 
  * decode would use for these sizes when its `partition_blocks` argument is 0.
  * Long contexts are split into partitions that run as independent CTAs and are
  * merged by a reduce pass (flash-decoding); a return value >= max_blocks_per_seq
- * means single-pass (no workspace needed).  Returns 0 on invalid sizes.
+ * means single-pass (no workspace needed).  Returns 0 on invalid sizes.  The
+ * automatic 4-bit decode cuts all contexts together into equal pieces: the value
+ * is then a piece's blocks when every context fills its table.
  * kv_8bit: 0 for the fp16/bf16 decodes, 1 for the INT8 decode, 2 for the FP8
  * decode, 4 for the 4-bit decode (the decodes run differently shaped CTAs).
  */
@@ -204,7 +206,10 @@ int32_t kvp_decode_partition_blocks(int32_t batch, int32_t num_q_heads, kvp_cach
  * sizes (0 when every request fits one partition).  partition_blocks as for the
  * decode (0 = automatic).  The workspace holds, per (request, query head,
  * partition), the partition's running max, sum and unnormalised output in
- * float32; it needs no initialisation and is fully rewritten by each call.
+ * float32 (the automatic 4-bit decode: two partial states per CTA, a size that
+ * the heads alone decide); it needs no initialisation and is fully rewritten by
+ * each call.  Calls that may run at the same time -- on two streams, or from two
+ * captured graphs -- need a workspace each.
  * kv_8bit: 0 for the fp16/bf16 decodes, 1 for the INT8 decode, 2 for the FP8
  * decode, 4 for the 4-bit decode; other values answer 0.
  */
@@ -308,8 +313,10 @@ kvp_status kvp_attention_decode_fp8(void* out, const void* q, kvp_dtype q_dtype,
  *   zero = min x;  scale = (max x - min x) / 15 rounded to `dtype`;
  *   code = scale > 0 ? min(15, rint((x - zero) / scale)) : 0
  * (round half to even).  Results are bit-exact with that definition for finite
- * rows whose range max x - min x is finite.  key, value: [num_tokens, Hkv, D]
- * of `dtype`, 16-byte aligned.  Slots and errors as kvp_append.
+ * rows whose range max x - min x is finite; a row with an infinity or NaN gets
+ * unspecified codes and pairs (other rows are not touched by it).  key, value:
+ * [num_tokens, Hkv, D] of `dtype`, 16-byte aligned; at most 65535 kv heads.
+ * Slots and errors as kvp_append.
  */
 kvp_status kvp_append_int4(const void* key, const void* value, kvp_dtype dtype, uint8_t* k_cache,
                            uint8_t* v_cache, void* k_scale_zero, void* v_scale_zero,
@@ -321,10 +328,10 @@ kvp_status kvp_append_int4(const void* key, const void* value, kvp_dtype dtype, 
  * dequantize of "KV Cache 优化与显存管理", 三, for 4-bit codes):
  *   key[t, h, :] = code * scale + zero of slot_mapping[t] (V likewise),
  * rounded once to float32 and once to `dtype`.  key, value: [num_tokens, Hkv, D],
- * 16-byte aligned; rows of a negative slot are left as they are.  A slot may be
- * named several times.  E.g. to lay a 4-bit prefix out as 16-bit blocks for
- * kvp_attention_prefill.  Device errors: KVP_ERR_BAD_BLOCK for slot >= NB * bs
- * (that token's rows are written as zeros).
+ * 16-byte aligned, at most 65535 kv heads; rows of a negative slot are left as
+ * they are.  A slot may be named several times.  E.g. to lay a 4-bit prefix out
+ * as 16-bit blocks for kvp_attention_prefill.  Device errors: KVP_ERR_BAD_BLOCK
+ * for slot >= NB * bs (that token's rows are written as zeros).
  */
 kvp_status kvp_read_int4(void* key, void* value, kvp_dtype dtype, const uint8_t* k_cache,
                          const uint8_t* v_cache, const void* k_scale_zero,
@@ -340,10 +347,13 @@ kvp_status kvp_copy_blocks_int4(uint8_t* k_cache, uint8_t* v_cache, void* k_scal
 /*
  * kvp_attention_decode_int4 -- as kvp_attention_decode over 4-bit pools:
  * K_i = code * scale + zero (V likewise), products with the codes in fp16 with
- * float32 accumulation; q, out and the pairs are of `dtype`.  Workspace from
- * kvp_decode_workspace_bytes with kv_8bit = 4.  KVP_DECODE_MERGE_RUNS is
- * accepted and changes nothing (blocks are fetched one by one).  Arguments
- * otherwise as kvp_attention_decode.
+ * float32 accumulation; q, out and the pairs are of `dtype`, scales not negative
+ * (as the appends write them), elements of q below 2^115 in size.  out must not
+ * overlap q.  A weight softmax_i * scale is rounded to fp16 before its product
+ * with the codes.  Workspace from kvp_decode_workspace_bytes with kv_8bit = 4;
+ * pools need 16-byte alignment only.  KVP_DECODE_MERGE_RUNS is accepted and
+ * changes nothing (blocks are fetched one by one).  Arguments otherwise as
+ * kvp_attention_decode.
  */
 kvp_status kvp_attention_decode_int4(void* out, const void* q, kvp_dtype dtype,
                                      const uint8_t* k_cache, const uint8_t* v_cache,
@@ -376,7 +386,8 @@ typedef struct {
  * rounded to float32, the results once to `dtype`):
  *   x' = x c - y s,   y' = y c + x s.
  * q, q_out: num_q_heads heads of D elements per token, q_stride / q_out_stride
- * elements from one token to the next; q_out may be q (same stride).  With
+ * elements from one token to the next; q_out may be q (same stride), and must
+ * not overlap q, key or value otherwise.  At most 65535 heads in all.  With
  * num_q_heads = 0 both may be NULL.  key, value: Hkv heads per token, k_stride /
  * v_stride apart -- so q, key and value may be slices of one projection's output.
  * All rows and pools 16-byte aligned, strides multiples of 8 elements.
@@ -413,8 +424,8 @@ kvp_status kvp_rope_append_int4(void* q_out, int64_t q_out_stride, const void* q
  * (e.g. captured in a graph).  The free blocks are a stack in device memory:
  * free_blocks[0 .. *free_count) of num_blocks entries, the last one on top.
  * Every block belongs to one request (no shared prefixes, no reference counts:
- * those stay with the host block manager).  At most 16384 requests
- * (KVP_ERR_UNSUPPORTED above).  Blocks hold 16 tokens.
+ * those stay with the host block manager).  At most 16384 requests and 2^30
+ * slots a call (KVP_ERR_UNSUPPORTED above).  Blocks hold 16 tokens.
  * ---------------------------------------------------------------------- */
 
 /*

@@ -217,7 +217,8 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
     const int pieces = std::max(1, kSms * int4_ctas_per_sm(c.head_dim) / per_request);
     const long long even = (static_cast<long long>(batch) * max_blocks + pieces - 1) / pieces;
     s.part_blocks = 0;
-    s.run_blocks = static_cast<int>(std::min<long long>(std::max(even, 8ll), max_blocks));
+    // (below the table's width: a context can always be cut)
+    s.run_blocks = static_cast<int>(std::min<long long>(std::max(even, 8ll), max_blocks - 1));
     s.max_parts = pieces * per_request;
     s.ws_bytes = static_cast<size_t>(s.max_parts) *
                  (2 * kHeadsPerCta * (static_cast<size_t>(c.head_dim) + 2) * sizeof(float) +
@@ -315,7 +316,7 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
     maps.merged = merge_runs && sh.path != DecodePath::kUmmaFp8;  // (per-block fetch only)
     kvp_status r = KVP_OK;
     if (int4) {
-      // whole tiles by untiled bulk copies: no maps
+      // (fetched by plain copies: no maps)
     } else if (maps.merged) {
       const int runs[3] = {1, 2, 4};
       for (int i = 0; i < 3 && r == KVP_OK; ++i) {
@@ -434,7 +435,8 @@ kvp_status rope_append_common(void* q_out, int64_t q_out_stride, const void* q, 
     by4 = by4 && rope.sections[a] % 4 == 0;
   }
   if (pairs != rope.rotary_dim / 2) return KVP_ERR_INVALID_ARG;
-  if (static_cast<long long>(num_q_heads) + c.num_kv_heads > 65535) return KVP_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_q_heads) + c.num_kv_heads > kMaxRowHeads)
+    return KVP_ERR_UNSUPPORTED;
   if (num_tokens == 0) return KVP_OK;
   if (!key || !value || !kc || !vc || !cos_sin || !positions || !slots) return KVP_ERR_INVALID_ARG;
   if (num_q_heads > 0 && (!q || !q_out)) return KVP_ERR_INVALID_ARG;
@@ -447,6 +449,7 @@ kvp_status rope_append_common(void* q_out, int64_t q_out_stride, const void* q, 
       (num_q_heads > 0 && (!stride_ok(q_stride, num_q_heads, c.head_dim) ||
                            !stride_ok(q_out_stride, num_q_heads, c.head_dim))))
     return KVP_ERR_INVALID_ARG;
+  if (q == q_out && q_stride != q_out_stride && num_tokens > 1) return KVP_ERR_INVALID_ARG;
   RowParams p{};
   p.q = static_cast<const uint16_t*>(q);
   p.q_out = static_cast<uint16_t*>(q_out);
@@ -697,6 +700,7 @@ kvp_status kvp_append_int4(const void* key, const void* value, kvp_dtype dtype, 
   const kvp_status ds = check_desc(cache);
   if (ds != KVP_OK) return ds;
   if (num_tokens < 0 || (dtype != KVP_F16 && dtype != KVP_BF16)) return KVP_ERR_INVALID_ARG;
+  if (cache.num_kv_heads > kMaxRowHeads) return KVP_ERR_UNSUPPORTED;
   if (num_tokens == 0) return KVP_OK;
   if (!key || !value || !slot_mapping || !aligned(key, 16) || !aligned(value, 16) ||
       !int4_pools_ok(k_cache, v_cache, k_scale_zero, v_scale_zero))
@@ -727,9 +731,7 @@ kvp_status kvp_read_int4(void* key, void* value, kvp_dtype dtype, const uint8_t*
   const kvp_status ds = check_desc(cache);
   if (ds != KVP_OK) return ds;
   if (num_tokens < 0 || (dtype != KVP_F16 && dtype != KVP_BF16)) return KVP_ERR_INVALID_ARG;
-  if (static_cast<long long>(num_tokens) * cache.num_kv_heads * (cache.head_dim / 16) >
-      256ll * 0x7fffffffll)
-    return KVP_ERR_UNSUPPORTED;
+  if (cache.num_kv_heads > kMaxRowHeads) return KVP_ERR_UNSUPPORTED;
   if (num_tokens == 0) return KVP_OK;
   if (!key || !value || !slot_mapping || !aligned(key, 16) || !aligned(value, 16) ||
       !int4_pools_ok(k_cache, v_cache, k_scale_zero, v_scale_zero))
@@ -811,8 +813,8 @@ kvp_status kvp_extend_tables(int32_t* block_tables, int32_t max_blocks_per_seq,
   KVP_NVTX_RANGE("kvp_extend_tables");
   if (batch < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || num_tokens < 0)
     return KVP_ERR_INVALID_ARG;
-  if (batch > kMaxTableBatch || num_blocks > 0x7fffffff / kBlockSize ||
-      max_blocks_per_seq > 0x7fffffff / kBlockSize)
+  if (batch > kMaxTableBatch || num_tokens > kMaxTableTokens ||
+      num_blocks > 0x7fffffff / kBlockSize || max_blocks_per_seq > 0x7fffffff / kBlockSize)
     return KVP_ERR_UNSUPPORTED;
   if (!free_blocks || !free_count || !free_count_out || !query_start) return KVP_ERR_INVALID_ARG;
   if (batch > 0 && (!block_tables || !context_lens || !new_lens || !context_lens_out))

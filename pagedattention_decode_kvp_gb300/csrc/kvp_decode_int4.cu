@@ -578,7 +578,7 @@ struct Walk {
 };
 
 __device__ __forceinline__ int blocks_of(const DecodeParams& p, int n) {
-  return n <= 0 || n > p.max_blocks * kBlockSize ? 0 : (n + kBlockSize - 1) / kBlockSize;
+  return n <= 0 || (n - 1) / kBlockSize >= p.max_blocks ? 0 : (n - 1) / kBlockSize + 1;
 }
 
 __device__ __forceinline__ long long piece_size(long long total, int pieces) {

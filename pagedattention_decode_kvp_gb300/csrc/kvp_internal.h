@@ -72,6 +72,10 @@ struct DecodeParams {
 // tokens) and 128 at head_dim 64 (4 CTAs 70 us, 3 CTAs 76, 32 x 32 heads of 4096).
 constexpr int int4_ctas_per_sm(int head_dim) { return head_dim == 128 ? 3 : 4; }
 
+// Heads of a token (query heads included) that the row kernels take: 32-bit
+// offsets within its rows.
+constexpr int kMaxRowHeads = 65535;
+
 // Everything the row kernels (rotary positions, 4-bit quantisation, scatter)
 // need.  Strides are elements from one token to the next.
 struct RowParams {
@@ -97,8 +101,10 @@ struct RowParams {
   int32_t row_lanes;            // rows of one token a CTA works on at a time (set at launch)
 };
 
-// Requests one table call handles (its offsets live in shared memory).
+// Requests one table call handles (its offsets live in shared memory), and slots
+// it lists (their indexes stay clear of 2^31 by a CTA's share).
 constexpr int kMaxTableBatch = 16384;
+constexpr int kMaxTableTokens = 1 << 30;
 
 // Device-side block tables: extend (all fields) and release (no new_lens,
 // slot_mapping, query_start, positions).

@@ -479,3 +479,94 @@ def test_decode_int4_in_two_captured_graphs():
     torch.cuda.synchronize()
     for (_, out, _), w in zip(graphs, want):
         assert torch.equal(out, w)
+
+
+def test_decode_int4_balanced_in_two_captured_graphs():
+    """The same for the automatic split, whose pieces leave notes for the merge."""
+    cases = [Case([3000, 50, 0, 1777], 8, 1, 128, torch.float16, seed=s, max_blocks=200)
+             for s in (43, 44)]
+    want = [c.run() for c in cases]
+    graphs = []
+    for c in cases:
+        out, q, t, n, ws = (torch.zeros_like(want[0]), c.q.cuda(), c.tables.cuda(), c.lens.cuda(),
+                            c.workspace())
+        assert ws is not None
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kvp.kvp_attention_decode_int4(out, q, *c.pools, t, n, c.scale, workspace=ws)
+        graphs.append((g, out, (q, t, n, ws)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for (g, out, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                out.zero_()
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, out, _), w in zip(graphs, want):
+        assert torch.equal(out, w)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_int4_entry_points_use_the_stream(given):
+    """On a side stream behind a long wait, current or passed as `stream`: inputs
+    that arrive on that stream are seen."""
+    T, kv, D, NB = 300, 2, 128, 30
+    x = randn((T, kv, D), torch.float16, 1).cuda()
+    slots = torch.randperm(NB * 16, generator=gen(2))[:T].to(torch.int32).cuda()
+    pairs = torch.tensor([[0, NB], [3, NB + 1]], dtype=torch.int32, device="cuda")
+    tables = torch.arange(NB, dtype=torch.int32, device="cuda")[None]
+    lens = torch.full((1,), NB * 16, dtype=torch.int32, device="cuda")
+    q = randn((1, 4, D), torch.float16, 3).cuda()
+
+    def run(late, side):
+        kc, vc, ks, vs = (t.cuda() for t in empty_pools(NB + 2, kv, D, torch.float16))
+        for t in (kc, vc, ks, vs):
+            t.zero_()
+        key, ko, vo = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x)
+        out = torch.zeros_like(q)
+        kw = dict(stream=side) if given and late else {}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            if late:
+                torch.cuda._sleep(20_000_000)
+            key.copy_(x)
+            if kw:
+                with torch.cuda.stream(torch.cuda.default_stream()):
+                    calls(key, kc, vc, ks, vs, ko, vo, out, kw)
+            else:
+                calls(key, kc, vc, ks, vs, ko, vo, out, kw)
+        torch.cuda.synchronize()
+        return kc, vc, ks, vs, ko, vo, out
+
+    def calls(key, kc, vc, ks, vs, ko, vo, out, kw):
+        kvp.kvp_append_int4(key, key, kc, vc, ks, vs, slots, **kw)
+        kvp.kvp_copy_blocks_int4(kc, vc, ks, vs, pairs, **kw)
+        kvp.kvp_read_int4(ko, vo, kc, vc, ks, vs, slots, **kw)
+        kvp.kvp_attention_decode_int4(out, q, kc, vc, ks, vs, tables, lens, 0.1, **kw)
+
+    want = run(False, torch.cuda.default_stream())
+    assert want[-1].abs().max() > 0
+    for a, b in zip(run(True, torch.cuda.Stream()), want):
+        assert torch.equal(bits(a) if a.is_floating_point() else a,
+                           bits(b) if b.is_floating_point() else b)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_append_int4_infinities_stay_in_their_rows(dtype):
+    T, kv, D, NB = 70, 3, 128, 6
+    x, y = randn((T, kv, D), dtype, 5), randn((T, kv, D), dtype, 6)
+    for i, v in enumerate((float("inf"), -float("inf"), float("nan"))):
+        x[7 * i, i, 3 + 40 * i] = v
+        y[7 * i + 1, i, 90 - 40 * i] = v
+    kc, vc, ks, vs = (t.cuda() for t in empty_pools(NB, kv, D, dtype))
+    slots = torch.arange(T, dtype=torch.int32)
+    kvp.kvp_append_int4(x.cuda(), y.cuda(), kc, vc, ks, vs, slots.cuda())
+    for rows, codes, pairs in ((x, kc, ks), (y, vc, vs)):
+        c, s = plain64.quantise4(rows.nan_to_num(0, 0, 0))
+        fine = rows.isfinite().all(-1)
+        codes, pairs = codes.cpu(), pairs.cpu()
+        assert torch.equal(codes[slots.long() // 16, :, slots.long() % 16][fine],
+                           plain64.pack4(c)[fine])
+        assert torch.equal(bits(pairs[slots.long() // 16, :, slots.long() % 16])[fine],
+                           bits(s)[fine])

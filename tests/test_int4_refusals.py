@@ -140,6 +140,33 @@ def test_tables(lib):
     assert ext(slots=None) == INVALID and ext(starts=None) == INVALID and ext(T=-1) == INVALID
 
 
+def test_sizes_past_32_bit_offsets(lib):
+    wide = desc(1, 65536)
+    for name in ("kvp_append_int4", "kvp_read_int4"):
+        assert getattr(lib, name)(A, A, 0, A, A, A, A, A, 1, wide, None, None) == UNSUPPORTED
+    assert lib.kvp_extend_tables(A, 8, A, A, 2, A, A, 50, A, A, A, 2 ** 30 + 1, A, None, None,
+                                 None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_rope_append_onto_q_with_another_stride(lib, int4):
+    pools = (A,) * (4 if int4 else 2)
+    f = lib.kvp_rope_append_int4 if int4 else lib.kvp_rope_append
+    assert f(A, 1024, A, 1032, A, 256, A, 256, *pools, A, 100, A, A, 3, 8, rope(), desc(), 0, None,
+             None) == INVALID
+
+
+def test_a_decode_that_needs_a_workspace_never_reads_as_single_pass(lib):
+    """kvp_decode_partition_blocks at or above the table's width means no workspace."""
+    for batch in (1, 3, 57, 1000, 65535):
+        for mb in (1, 64, 65, 100, 9000):
+            for hq, kv in ((8, 8), (64, 8), (1, 1), (1024, 1024)):
+                d = desc(1000, kv)
+                single = kvp.kvp_decode_partition_blocks(batch, hq, d, mb, kv_int4=True) >= mb
+                assert single == (kvp.kvp_decode_workspace_bytes(batch, hq, d, mb,
+                                                                 kv_int4=True) == 0)
+
+
 class Fake:
     """Just enough of a tensor on some GPU for the binding's checks."""
 
