@@ -38,14 +38,17 @@
 //     their place the sum came out 1e-6 too small, as if products were cut off
 //     where a normal operand's would be, and that is 5e-4 of the centred output
 //     at 4096 tokens per warp.)
-//   * The sums stay in the tensor core's accumulators, which truncate: a sum of
-//     codes loses half a step of its size at every product, and over a long
-//     context that adds up.  So the centre is taken out of the sums every 8
-//     steps; what is left grows with the square root of the tokens.  Measured on
-//     4096 tokens per warp, against float64: 2.3e-4 of the output, which is the
-//     rounding of a; 2.9e-4 without it (1.1e-3 with equal weights at 8192); the
-//     same 2.3e-4 with products added in the lanes, which takes 17 more
-//     instructions a block (107 us where this takes 104, 57 contexts of 9200).
+//   * The sums stay in the tensor core's accumulators, which truncate: every
+//     product takes up to a step of its size off a sum, always towards zero, and
+//     over a long context that adds up.  So every 8 steps the centre is taken out
+//     of the sums twice over: they go to the other side of zero and come back,
+//     and what truncation takes on one side it gives on the other.  (The first
+//     step's sums go to -4 times themselves, half of what 8 steps add.)  Against
+//     float64, root mean square over the output, fp16, four contexts of 131072
+//     tokens: 3.07e-4, of which the output's own rounding is 2.1e-4 and that of a
+//     the same again; 3.2e-4 with sums taken back to zero only, and 4.4e-4
+//     against 3.5e-4 for a million tokens.  (The rest of a in a second product
+//     would be 8 more tensor instructions a block to the 18.)
 //   * z's part, sum_t P_t (z_t + 7.5 s_t), is float32 on the lanes.
 //   * Blocks come by cp.async, 16 bytes per lane (5 instructions a block at
 //     D = 128 where an elected lane's bulk copies, barriers and fences took 64),
@@ -112,7 +115,7 @@ struct Int4Path {
   struct State {
     float o[kGroups][4][4];      // 2^-24 sum a c (0, 1) and 2^-20 sum a c (2, 3), centred
                                  // but for the a in `as`
-    float as[kGroups][4];        // sum a, in every row
+    float as[kGroups][4];        // sum a less what was taken out, in every row
     float zo[kGroups][2];        // sum P (z + 7.5 s), this lane's tokens
     float qz[kGroups][2];        // scale log2(e) Q_g
     float f[2];                  // scale log2(e) 2^20 / kappa
@@ -404,19 +407,19 @@ struct Int4Path {
     }
   }
 
-  // Take the centre out of the sums (see above).
-  __device__ __forceinline__ static void centre(State& st) {
+  // Take the centre out of the sums, and `back` times more of it (see above).
+  __device__ __forceinline__ static void centre(State& st, float back) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float even = -7.5f * 5.9604645e-8f * st.as[g][i], odd = 16.f * even;
+        const float even = -7.5f * 5.9604645e-8f * (1.f + back) * st.as[g][i], odd = 16.f * even;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           st.o[g][j][i] += even;
           st.o[g][j][i + 2] += odd;
         }
-        st.as[g][i] = st.as[g][i + 2] = 0.f;
+        st.as[g][i] = st.as[g][i + 2] = -back * st.as[g][i];
       }
     }
   }
@@ -878,7 +881,7 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
           Path::template consume<false>(st, qs, ring + at, valid, first, lane);
         else
           Path::template consume<true>(st, qs, ring + at, valid, first, lane);
-        if (i / kStride % kCentre == kCentre - 1) Path::centre(st);
+        if (i / kStride % kCentre == 0) Path::centre(st, first ? kCentre / 2 : 1);
         at = at == (kBuf - 1) * kStepBytes ? 0 : at + kStepBytes;
         next = next == (kBuf - 1) * kStepBytes ? 0 : next + kStepBytes;
       }
