@@ -13,8 +13,13 @@
 // contexts together (see Walk), or a partition of the size the caller asks for.
 //
 // A block is 2 (8 D + 32 D / 64) bytes = 2304 at D = 128, little over half of
-// an INT8 block, while a warp has the same 32 D codes to widen: the kernel is
-// bound by issue slots before HBM, so everything here saves instructions.
+// an INT8 block, while a warp has the same 32 D codes to widen: unlike the 8-bit
+// decodes the kernel fills over half of the issue slots at HBM's pace, so
+// everything here saves instructions (257 a block).  Measured, D = 128: 57
+// contexts of 9200 tokens, 8 kv heads, 103 us (0.87 of the measured copy
+// bandwidth), 32 of 4096 with 32 kv heads 110 us (0.81), 64 of 512 to 8192 66 us
+// (0.67: a start of about 6 us, a refill of the ring at every run, the merge's
+// 3 us); its ring alone, without the arithmetic, takes 91 us of the 103.
 //   * A code left where it lies is already a number: the fp16 bit pattern
 //     0x000c is the subnormal c 2^-24 and 0x00c0 is 16 c 2^-24, both exact
 //     tensor-core operands.  So one AND turns two codes into an operand pair,
@@ -568,8 +573,8 @@ struct Segment {
 // CTA walks the end of one context, whole ones, and the start of another.  The
 // CTAs of a piece's units are neighbours and walk the same blocks at the same
 // time, which keeps the tiles of a block's kv heads together on their way
-// through the DRAM (units one after the other in one line instead: 99 us where
-// this took 82, contexts of 512 to 8192 tokens, 64 x 8 heads).  Only a piece's
+// through the DRAM (with the units one after the other in one line, contexts of
+// 512 to 8192 tokens and 64 x 8 heads took 99 us instead of the 82 of that time).  Only a piece's
 // first and last run can be partial; their states go to the CTA's two workspace
 // slots, and the CTA that starts a cut context leaves a note for the merge.
 struct Walk {
@@ -971,7 +976,7 @@ __global__ void __launch_bounds__(256) merge_noted_kernel(const DecodeParams p) 
 
 // The same for few contexts with many runs each: a block per (query head of a
 // unit, unit, request) and 16 warps over the runs.  The request's place among
-// the pieces is found from the lengths again (at most pieces / 16 of them).
+// the pieces is found from the lengths again (pieces / 8 of them at most).
 template <int D, bool kBf16Out>
 __global__ void __launch_bounds__(512) merge_long_kernel(const DecodeParams p, int pieces) {
   constexpr int E = D / 32, W = 16;
@@ -1054,10 +1059,12 @@ cudaError_t launch_decode_int4(const DecodeParams& p, int grid_x, cudaStream_t s
 
 template <int D, bool kBf16Out>
 static cudaError_t launch_merge(const DecodeParams& p, int grid_x, cudaStream_t s) {
-  // A context spans pieces / batch runs when all are alike.  From 4 on a block
-  // per head beats a warp per head (57 runs: 7.7 us with four warps a head).
+  // A context spans pieces / batch runs when all are alike.  A block per head
+  // against a warp per head, in us: 114 runs 5 and 23 (4 contexts of one kv head),
+  // 57 runs 4 and 11 (one context, 8 kv heads), 14 runs 3.8 and 5.4; 11 runs 6 and
+  // 4 (40 contexts of one kv head), 7 runs 6.5 and 4.4, one or two runs 30 and 3.
   const int units = p.num_kv_heads * p.qgroups, pieces = grid_x / units;
-  if (pieces >= 8 * p.batch)
+  if (pieces >= 12 * p.batch)
     return launch_pdl(merge_long_kernel<D, kBf16Out>, dim3(p.heads_per_cta, units, p.batch),
                       dim3(512), 0, s, p, pieces);
   return launch_pdl(merge_noted_kernel<D, kBf16Out>, dim3(grid_x), dim3(256), 0, s, p);

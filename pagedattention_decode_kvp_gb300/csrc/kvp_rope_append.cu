@@ -23,7 +23,14 @@
 // Bound by HBM for prompts and by latency for a step.  D / 16 lanes share a
 // row; a lane holds two 16-byte chunks, chosen so that both elements of every
 // split-half pair are its own, and uses its 8 (cos, sin) pairs for every head
-// of the token it works on.
+// of the token it works on.  Measured, prompts of 33098 tokens, 32 kv heads of
+// 128 (shares of the measured copy bandwidth): rotation with a 16-bit append 242
+// us (0.96 to 1.0), 4-bit append 140 us (0.71), read-back 110 us (0.90);
+// rotation with a 4-bit append, 8191 tokens of 64 + 8 heads, 56 us (0.79).  The
+// quantiser is what holds the 4-bit appends: 419 instructions for four K and four
+// V rows fill 67% of the issue slots, and neither more CTAs per SM (139 us with
+// 9, 142 with 10, spilling) nor the next rows' loads ahead of the arithmetic
+// (138 us at 6 CTAs, 150 at 8) change that.  A step of 64 tokens takes 2.9 us.
 #include "kvp_device.cuh"
 #include "kvp_internal.h"
 
@@ -324,9 +331,10 @@ __device__ __forceinline__ void load_angles(const RowParams& p, const int (&pos)
   }
 }
 
-// One CTA: 256 / L row slots (L = D / 16 lanes each), row_lanes of them on one
-// token.  A slot takes the token's units r, r + step, ...: query rows first,
-// then (K, V) row pairs of the kv heads; gridDim.y CTAs share a token's units.
+// One CTA: kRowThreads / L row slots (L = D / 16 lanes each), row_lanes of them
+// on one token.  A slot takes the token's units r, r + step, ...: query rows
+// first, then (K, V) row pairs of the kv heads; gridDim.y CTAs share a token's
+// units.
 template <bool kBf16, int D, bool kRope, bool kInt4>
 __global__ void __launch_bounds__(kRowThreads, kRope ? 6 : 8) row_kernel(const RowParams p) {
   constexpr int L = D / 16;
@@ -441,7 +449,7 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sz) {
 
 // A warp per token and 512 / D heads: lane (head, c) of L = D / 16 lanes per head
 // writes the 16-byte chunks c and c + L of K and of V, so that a store covers
-// whole sectors.
+// whole sectors (32 bytes a lane in a row instead: 128 us where this takes 110).
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(128) read_int4_kernel(
     uint4* __restrict__ key, uint4* __restrict__ value, const uint8_t* __restrict__ kc,
@@ -498,7 +506,10 @@ cudaError_t launch_rows(RowParams p, cudaStream_t s) {
   constexpr int kSlots = kRowThreads / (D / 16);
   const long long units = (kRope ? p.num_q_heads : 0) + p.num_kv_heads;
   // Many tokens: 8 slots per token, so a lane uses its angles for several
-  // heads.  Few: all of a CTA's slots on one token, and CTAs side by side.
+  // heads.  Few: all of a CTA's slots on one token, and CTAs side by side.  The
+  // step lies where four CTAs per SM have work: rotation of 64 + 8 heads of 128
+  // into 4 bits, 128 tokens 6.5 and 5.0 us, 256 tokens 6.5 and 6.8, 4096 tokens 31
+  // and 59; 16 + 8 heads of 64, 512 tokens 5.2 and 4.7, 1024 tokens 5.3 and 6.9.
   const bool many = p.num_tokens * units >= 152 * 4 * kSlots;
   p.row_lanes = many ? 8 : kSlots;
   const long long per_cta = kSlots / p.row_lanes;
