@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "kvp_internal.h"
+#include "kvp_serve.h"
 
 using namespace kvp;
 
@@ -123,7 +124,8 @@ kvp_status make_q_map(CUtensorMap* map, const void* q, int num_tokens, int num_q
 }
 
 struct DecodeShape {
-  DecodePath path;
+  DecodePath path = DecodePath::kMma;  // of 16- and 8-bit pools
+  bool int4 = false;                   // 4-bit pools
   int heads_per_cta;
   int qgroups;
   int part_blocks;  // 0: balanced (4-bit pools)
@@ -154,7 +156,6 @@ constexpr int kInt4SinglePass = 64;
 int resident_ctas(DecodePath path) {
   switch (path) {
     case DecodePath::kMmaInt8: return 4;
-    case DecodePath::kInt4: return int4_ctas_per_sm(128);
     case DecodePath::kUmmaFp8: return 2;
     default: return 3;
   }
@@ -193,7 +194,7 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
   const int G = num_q_heads / c.num_kv_heads;
   DecodeShape s;
   if (kv_8bit == 4) {
-    s.path = DecodePath::kInt4;
+    s.int4 = true;
     s.heads_per_cta = G < kHeadsPerCta ? G : kHeadsPerCta;
   } else if (kv_8bit == 2 && c.head_dim == 128) {
     s.path = DecodePath::kUmmaFp8;  // FP8 codes straight into the tensor core
@@ -210,7 +211,7 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
   }
   s.qgroups = (G + s.heads_per_cta - 1) / s.heads_per_cta;
   const long long units = static_cast<long long>(batch) * c.num_kv_heads * s.qgroups;
-  if (s.path == DecodePath::kInt4 && partition_blocks == 0 && max_blocks > kInt4SinglePass) {
+  if (s.int4 && partition_blocks == 0 && max_blocks > kInt4SinglePass) {
     // balanced: equal pieces of all contexts, a CTA per piece and unit of a
     // request; two partial states of up to 8 heads per CTA and a note
     const int per_request = c.num_kv_heads * s.qgroups;
@@ -226,9 +227,9 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
     *out = s;
     return KVP_OK;
   }
-  int pb = partition_blocks > 0             ? partition_blocks
-           : s.path == DecodePath::kInt4 ? max_blocks
-                                         : auto_partition(s.path, units, max_blocks);
+  int pb = partition_blocks > 0 ? partition_blocks
+           : s.int4             ? max_blocks
+                                : auto_partition(s.path, units, max_blocks);
   if (pb >= max_blocks) pb = max_blocks;
   if (pb > kMaxPartBlocks) return KVP_ERR_UNSUPPORTED;  // one partition must fit on chip
   s.part_blocks = pb;
@@ -272,13 +273,16 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
   if (sh.ws_bytes > 0 && (ws == nullptr || ws_bytes < sh.ws_bytes || !aligned(ws, 16)))
     return KVP_ERR_INVALID_ARG;
 
-  DecodeParams p{};
+  Int4DecodeParams p{};
   p.out = out;
   p.q = q;
-  p.k_scale = int4 ? nullptr : static_cast<const float*>(ks);
-  p.v_scale = int4 ? nullptr : static_cast<const float*>(vs);
-  p.k_sz = int4 ? ks : nullptr;
-  p.v_sz = int4 ? vs : nullptr;
+  if (int4) {
+    p.k_sz = ks;
+    p.v_sz = vs;
+  } else {
+    p.k_scale = static_cast<const float*>(ks);
+    p.v_scale = static_cast<const float*>(vs);
+  }
   p.block_tables = tables;
   p.context_lens = lens;
   p.ws_o = static_cast<float*>(ws);
@@ -310,14 +314,14 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
   if (static_cast<long long>(c.num_kv_heads) * sh.qgroups > 65535 || batch > 65535)
     return KVP_ERR_UNSUPPORTED;
 
-  if (phases & KVP_PHASE_PARTIAL) {
+  if ((phases & KVP_PHASE_PARTIAL) && int4) {
+    if (launch_decode_int4(p, sh.max_parts, s) != cudaSuccess) return KVP_ERR_CUDA;
+  } else if (phases & KVP_PHASE_PARTIAL) {
     const int eb = int8 ? 1 : 2;
     DecodeMaps maps;
     maps.merged = merge_runs && sh.path != DecodePath::kUmmaFp8;  // (per-block fetch only)
     kvp_status r = KVP_OK;
-    if (int4) {
-      // (fetched by plain copies: no maps)
-    } else if (maps.merged) {
+    if (maps.merged) {
       const int runs[3] = {1, 2, 4};
       for (int i = 0; i < 3 && r == KVP_OK; ++i) {
         r = make_pool_run_map(&maps.runs.k[i], kc, c, eb, runs[i]);
@@ -338,9 +342,6 @@ kvp_status decode_common(void* out, const void* q, bool q_bf16, int kv_kind, con
         break;
       case DecodePath::kUmmaFp8:
         e = launch_decode_fp8_umma(p, maps.k, maps.v, sh.max_parts, s);
-        break;
-      case DecodePath::kInt4:
-        e = launch_decode_int4(p, sh.max_parts, s);
         break;
       default:
         e = kv_kind == 3 ? launch_decode_mma_fp8(p, maps, sh.max_parts, s)

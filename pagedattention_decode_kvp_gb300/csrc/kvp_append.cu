@@ -11,6 +11,7 @@
 // per 16-byte chunk, rows of a block contiguous so every warp access coalesces.
 #include "kvp_device.cuh"
 #include "kvp_internal.h"
+#include "kvp_serve.h"
 
 namespace kvp {
 namespace {

@@ -62,6 +62,7 @@
 //     instruction, K as it lies and V transposed: for V that also sets the codes
 //     of two tokens side by side as the product wants them.
 #include "kvp_decode.cuh"
+#include "kvp_serve.h"
 
 namespace kvp {
 namespace {
@@ -139,7 +140,7 @@ struct Int4Path {
     uint4 raw[kGroups][2];
   };
 
-  __device__ __forceinline__ static void load_query(Query& x, const DecodeParams& p, int b,
+  __device__ __forceinline__ static void load_query(Query& x, const Int4DecodeParams& p, int b,
                                                     int head0, int nheads, int lane) {
     const int g8 = lane >> 2, t4 = lane & 3;
     const uint16_t* q = static_cast<const uint16_t*>(p.q) +
@@ -585,7 +586,7 @@ struct Walk {
   int flags, runs;
 };
 
-__device__ __forceinline__ int blocks_of(const DecodeParams& p, int n) {
+__device__ __forceinline__ int blocks_of(const Int4DecodeParams& p, int n) {
   return n <= 0 || (n - 1) / kBlockSize >= p.max_blocks ? 0 : (n - 1) / kBlockSize + 1;
 }
 
@@ -595,7 +596,7 @@ __device__ __forceinline__ long long piece_size(long long total, int pieces) {
 }
 
 // Sets the walk of piece `index` of `pieces`; false when it has no blocks.
-__device__ __forceinline__ bool find_piece(const DecodeParams& p, int index, int pieces,
+__device__ __forceinline__ bool find_piece(const Int4DecodeParams& p, int index, int pieces,
                                            Walk& walk) {
   __shared__ long long part[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -641,7 +642,7 @@ __device__ __forceinline__ bool find_piece(const DecodeParams& p, int index, int
 
 // One thread: the walk's next segment.  `ahead` is the length of the context
 // behind walk.b, fetched by the call before.
-__device__ __forceinline__ void next_segment(const DecodeParams& p, Walk& walk, Segment& seg,
+__device__ __forceinline__ void next_segment(const Int4DecodeParams& p, Walk& walk, Segment& seg,
                                              int& ahead) {
   int flags = walk.flags & ~kInit;
   if (walk.left == 0) {
@@ -693,7 +694,7 @@ constexpr size_t int4_smem() {
 // part_blocks > 0: grid (partitions, units, requests), one run per CTA.
 // part_blocks == 0: balanced, grid units * pieces.
 template <class Path>
-__global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(const Int4DecodeParams p) {
   constexpr int D = Path::kD, H = Path::kHeads;
   constexpr int kCB = Path::kCodeBytes, kPB = Path::kPairBytes, kSB = Path::kStageBytes;
   constexpr int kPieces = kCB / 16;  // 16-byte pieces of a block's K (or V) codes
@@ -920,7 +921,7 @@ struct Merge {
     for (int e = 0; e < E; ++e) o[e] = 0.f;
   }
   // Workspace row `prow`, this lane's E outputs; L < 0 marks a failed run.
-  __device__ __forceinline__ void add(const DecodeParams& p, size_t prow, int lane) {
+  __device__ __forceinline__ void add(const Int4DecodeParams& p, size_t prow, int lane) {
     const float2 v = *reinterpret_cast<const float2*>(p.ws_ml + 2 * prow);
     float x[E];
     if constexpr (E == 4) {
@@ -939,7 +940,7 @@ struct Merge {
     for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f0, f1 * x[e]);
   }
   template <bool kBf16Out>
-  __device__ __forceinline__ void store(const DecodeParams& p, size_t row, int lane) const {
+  __device__ __forceinline__ void store(const Int4DecodeParams& p, size_t row, int lane) const {
     const float inv = !bad && L > 0.f ? 1.f / L : 0.f;
     uint32_t w[E / 2];
 #pragma unroll
@@ -958,7 +959,7 @@ struct Merge {
 // (slot 0) of the unit's next pieces.  note: first output row, heads, runs, slot
 // of the first run.
 template <int D, bool kBf16Out>
-__global__ void __launch_bounds__(256) merge_noted_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(256) merge_noted_kernel(const Int4DecodeParams p) {
   dev::grid_dependency_wait();
   dev::launch_dependents();
   const int4 note = p.notes[blockIdx.x];
@@ -978,7 +979,7 @@ __global__ void __launch_bounds__(256) merge_noted_kernel(const DecodeParams p) 
 // unit, unit, request) and 16 warps over the runs.  The request's place among
 // the pieces is found from the lengths again (pieces / 8 of them at most).
 template <int D, bool kBf16Out>
-__global__ void __launch_bounds__(512) merge_long_kernel(const DecodeParams p, int pieces) {
+__global__ void __launch_bounds__(512) merge_long_kernel(const Int4DecodeParams p, int pieces) {
   constexpr int E = D / 32, W = 16;
   __shared__ __align__(16) float s_o[W][D];
   __shared__ float2 s_ml[W];
@@ -1036,7 +1037,7 @@ __global__ void __launch_bounds__(512) merge_long_kernel(const DecodeParams p, i
 }
 
 template <class Path>
-cudaError_t launch_int4(const DecodeParams& p, int grid_x, cudaStream_t s) {
+cudaError_t launch_int4(const Int4DecodeParams& p, int grid_x, cudaStream_t s) {
   constexpr size_t smem = int4_smem<Path>();
   const cudaError_t e =
       ensure_smem_attr(reinterpret_cast<const void*>(&decode_int4_kernel<Path>), smem);
@@ -1048,7 +1049,7 @@ cudaError_t launch_int4(const DecodeParams& p, int grid_x, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_decode_int4(const DecodeParams& p, int grid_x, cudaStream_t s) {
+cudaError_t launch_decode_int4(const Int4DecodeParams& p, int grid_x, cudaStream_t s) {
   const bool bf = p.q_bf16 != 0;
   if (!bf && p.head_dim == 64) return launch_int4<Int4Path<false, 64>>(p, grid_x, s);
   if (!bf && p.head_dim == 128) return launch_int4<Int4Path<false, 128>>(p, grid_x, s);
@@ -1058,7 +1059,7 @@ cudaError_t launch_decode_int4(const DecodeParams& p, int grid_x, cudaStream_t s
 }
 
 template <int D, bool kBf16Out>
-static cudaError_t launch_merge(const DecodeParams& p, int grid_x, cudaStream_t s) {
+static cudaError_t launch_merge(const Int4DecodeParams& p, int grid_x, cudaStream_t s) {
   // A context spans pieces / batch runs when all are alike.  A block per head
   // against a warp per head, in us: 114 runs 5 and 23 (4 contexts of one kv head),
   // 57 runs 4 and 11 (one context, 8 kv heads), 14 runs 3.8 and 5.4; 11 runs 6 and
@@ -1070,7 +1071,7 @@ static cudaError_t launch_merge(const DecodeParams& p, int grid_x, cudaStream_t 
   return launch_pdl(merge_noted_kernel<D, kBf16Out>, dim3(grid_x), dim3(256), 0, s, p);
 }
 
-cudaError_t launch_decode_int4_merge(const DecodeParams& p, int grid_x, cudaStream_t s) {
+cudaError_t launch_decode_int4_merge(const Int4DecodeParams& p, int grid_x, cudaStream_t s) {
   if (p.head_dim == 64)
     return p.q_bf16 ? launch_merge<64, true>(p, grid_x, s) : launch_merge<64, false>(p, grid_x, s);
   return p.q_bf16 ? launch_merge<128, true>(p, grid_x, s) : launch_merge<128, false>(p, grid_x, s);

@@ -32,7 +32,7 @@
 // 9, 142 with 10, spilling) nor the next rows' loads ahead of the arithmetic
 // (138 us at 6 CTAs, 150 at 8) change that.  A step of 64 tokens takes 2.9 us.
 #include "kvp_device.cuh"
-#include "kvp_internal.h"
+#include "kvp_serve.h"
 
 namespace kvp {
 namespace {

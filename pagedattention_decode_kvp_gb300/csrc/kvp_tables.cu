@@ -19,11 +19,11 @@
 // Measured, a release and an extend together: 64 requests of one token each 9 us,
 // 1000 of them 14, 1024 requests with prompts, 524291 slots, 21 (37 with the
 // slots in the cluster's launch; 64 requests with 64003 slots 13.6 against 12.9,
-// and a second launch for 1000 slots costs 5); 16384 requests 130, the scans.
+// and a second launch for 1000 slots costs 5); 16384 requests 131
 #include <cooperative_groups.h>
 
 #include "kvp_device.cuh"
-#include "kvp_internal.h"
+#include "kvp_serve.h"
 
 namespace kvp {
 namespace {
