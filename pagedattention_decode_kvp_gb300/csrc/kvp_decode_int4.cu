@@ -7,7 +7,7 @@
 //         Q_g = sum_{d in g} q_d,
 //   out_d = sum_t p_t (s_tg c_td + z_tg) / sum_t p_t,   p_t = 2^(u_t - m).
 // A CTA walks blocks of one kv head for up to 8 of its query heads: each of its
-// 4 warps streams its own 16-token blocks, two at a time, through a ring of
+// 4 warps streams its own 16-token blocks, a few at a time, through a ring of
 // stages, and the warps' states are merged at the end of a context.  Which blocks
 // a CTA walks: a whole context where tables are short, else an equal piece of all
 // contexts together (see Walk), or a partition of the size the caller asks for.
@@ -67,12 +67,10 @@
 namespace kvp {
 namespace {
 
-constexpr int kStep = 2;      // blocks a warp takes at a time
 constexpr int kBuf = 2;       // steps per warp: one in use, one on the way
 constexpr int kCentre = 8;    // steps between two centrings of the sums
-constexpr int kInt4Stages = kStep * kBuf;   // blocks
 constexpr int kTable = 512;                 // table entries of a segment
-constexpr int kMinRun = kStep * kWarps;      // blocks of a piece at least: a step of every warp
+constexpr int kMinRun = 2 * kWarps;          // blocks of a piece at least
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -108,11 +106,17 @@ struct Int4Path {
   static constexpr int kD = D;
   static constexpr int kHeads = 8;
   static constexpr int kCtas = int4_ctas_per_sm(D);
+  // Blocks a warp takes at a time: as many as the registers hold, for every
+  // product and table look-up waits on few others (D = 128, 32 x 32 heads of 4096
+  // tokens: one block 121 us, two 110, three 114, spilling; D = 64, four contexts
+  // of 131072: two blocks 69 us, three 66, four 66, spilling).
+  static constexpr int kStep = D == 128 ? 2 : 3;
+  static constexpr int kStages = kStep * kBuf;  // blocks
   static constexpr int kGroups = D / 64;
   static constexpr int kCodeBytes = 16 * D / 2;        // K or V codes of a block
   static constexpr int kPairBytes = 16 * kGroups * 4;  // their (s, z) pairs
   static constexpr int kStageBytes = 2 * (kCodeBytes + kPairBytes);
-  static constexpr int kS = kWarps * kInt4Stages;
+  static constexpr int kS = kWarps * kStages;
   static_assert(kStageBytes % 128 == 0, "stages stay aligned for 16-byte copies");
 
   static constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // code pairs of a word
@@ -333,9 +337,9 @@ struct Int4Path {
     }
   }
 
-  // Two blocks, kStageBytes apart (each: K codes, V codes, K pairs, V pairs).
-  // kTail: only the first `valid` of their 32 tokens count.  first: the warp's
-  // first pair, which sets the reference.
+  // A step's blocks, kStageBytes apart (each: K codes, V codes, K pairs, V pairs).
+  // kTail: only the first `valid` of their tokens count.  first: the warp's first
+  // step, which sets the reference.
   template <bool kTail>
   __device__ __forceinline__ static void consume(State& st, const uint4* qs, const uint8_t* tile,
                                                  int valid, bool first, int lane) {
@@ -388,7 +392,7 @@ struct Int4Path {
       }
     }
 
-    // ---- values: both blocks' products, straight into the sums
+    // ---- values: the blocks' products, straight into the sums
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
@@ -430,7 +434,7 @@ struct Int4Path {
     }
   }
 
-  // Rare: move the reference so that the pair's largest a lies in [8, 16),
+  // Rare: move the reference so that the step's largest a lies in [8, 16),
   // never down.  v is relative to the old one on entry, to the new one on exit.
   __device__ __forceinline__ static void reference(State& st, float (&v)[kStep][4],
                                                    const float (&s0)[kStep][kGroups],
@@ -487,7 +491,7 @@ struct Int4Path {
   static constexpr int kParts = 2 * kGroups;  // (group, parity) pairs
   // It lies in the last step's place of the warp's ring.
   static constexpr int kMergeAt = (kBuf - 1) * kStep * kStageBytes;
-  static constexpr int kRingBytes = kInt4Stages * kStageBytes;
+  static constexpr int kRingBytes = kStages * kStageBytes;
   static_assert((kParts * 256 + 16) * 4 <= kStep * kStageBytes, "the state fits a step's place");
 
   __device__ __forceinline__ static void finalize(State& st, uint8_t* ring, int lane) {
@@ -757,7 +761,7 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
   // of the pairs' pieces on the first lanes.
   constexpr int kPairPieces = kPB / 16;
   const bool is_v = lane >= kPairPieces;
-  uint8_t* ring = smem + warp * kInt4Stages * kSB;
+  uint8_t* ring = smem + warp * Path::kStages * kSB;
   constexpr int kRowPieces = D / 32;
   const uint32_t code_at =
       dev::smem_addr(ring) + code_piece<D>(lane / kRowPieces, lane % kRowPieces);
@@ -766,7 +770,7 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
   const uint8_t* vc = static_cast<const uint8_t*>(p.v_pool) + lane * 16;
   const uint8_t* pairs = static_cast<const uint8_t*>(is_v ? p.v_sz : p.k_sz) +
                          (lane - (is_v ? kPairPieces : 0)) * 16;
-  constexpr int kStride = kStep * kWarps, kStepBytes = kStep * kSB;
+  constexpr int kStep = Path::kStep, kStride = kStep * kWarps, kStepBytes = kStep * kSB;
 
   // A segment's slice of the block table comes on chip during the segment
   // before ("踩坑一"), entry by entry; each thread checks those it fetched.
