@@ -130,6 +130,8 @@ _lib = None
 def load_library():
     """Load libkvp.so (once).  Raises RuntimeError if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -158,6 +160,7 @@ def kvp_version() -> int:
 
 
 # ------------------------------------------------------------------ marshalling
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -435,19 +438,17 @@ def kvp_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, 
 # little: one expression tells whether everything is in order, and only where it
 # is not are the arguments gone through one by one for the error.
 def _on_one_device(stream, *ts) -> int:
-    """CUDA tensors of one device, which is the current one (kernels launch
-    there); returns the stream to use."""
-    dev = None
-    for t in ts:
-        if t is not None:
-            d = t.get_device()
-            if d != dev:
-                if d < 0:
-                    raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
-                if dev is not None:
-                    raise ValueError(f"tensors on cuda:{dev} and cuda:{d} in one call")
-                dev = d
+    """CUDA tensors (the first one is there) of the current device, where kernels
+    launch; returns the stream to use."""
     c = _torch()._C
+    dev = ts[0].get_device()
+    if dev < 0:
+        raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            if t.get_device() < 0:
+                raise ValueError("tensors passed to the GPU entry points must be CUDA tensors")
+            raise ValueError(f"tensors on cuda:{dev} and cuda:{t.get_device()} in one call")
     if dev != c._cuda_getDevice():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is "
                          f"cuda:{c._cuda_getDevice()}")
@@ -470,9 +471,10 @@ def _need(t, name, dtype, shape):
 
 def _extents(t, name, dims):
     """Shape of a tensor of that many dimensions."""
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(shape)}")
+    return shape
 
 
 @functools.lru_cache(maxsize=256)
@@ -487,19 +489,28 @@ def _rope_desc(rotary_dim, sections, interleaved) -> kvp_rope_desc:
     return kvp_rope_desc(rotary_dim, len(sections), (ctypes.c_int32 * 4)(*sections), interleaved)
 
 
+@functools.lru_cache(maxsize=256)
+def _int4_sizes(codes):
+    """Of pools whose codes have that shape: the descriptor, the pairs' shape, kv
+    heads and head_dim."""
+    if len(codes) != 4:
+        raise ValueError("4-bit pools are [num_blocks, num_kv_heads, block_size, head_dim / 2]")
+    nb, hkv, bs, half = codes
+    return kvp_cache_desc(nb, hkv, bs, 2 * half), (nb, hkv, bs, half // 32, 2), hkv, 2 * half
+
+
 def cache_desc_int4(k_cache) -> kvp_cache_desc:
     """kvp_cache_desc of a 4-bit pool's codes [NB, Hkv, block_size, D / 2] (uint8)."""
-    if k_cache.dim() != 4:
-        raise ValueError("4-bit pools are [num_blocks, num_kv_heads, block_size, head_dim / 2]")
+    _int4_sizes(k_cache.shape)
     nb, hkv, bs, half = k_cache.shape
-    return _desc(nb, hkv, bs, 2 * half)
+    return kvp_cache_desc(nb, hkv, bs, 2 * half)
 
 
-def _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype) -> kvp_cache_desc:
+def _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype):
+    """Checks the pools; returns descriptor, kv heads and head_dim."""
     u8 = _torch().uint8
     codes = k_cache.shape
-    d = cache_desc_int4(k_cache)
-    pairs = codes[:3] + (d.head_dim // 64, 2)
+    d, pairs, kv, dim = _int4_sizes(codes)
     if not (k_cache.dtype is u8 and v_cache.dtype is u8 and v_cache.shape == codes and
             k_scale_zero.dtype is dtype and v_scale_zero.dtype is dtype and
             k_scale_zero.shape == pairs and v_scale_zero.shape == pairs and
@@ -507,10 +518,10 @@ def _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype) -> kvp_cach
             k_scale_zero.is_contiguous() and v_scale_zero.is_contiguous()):
         _need(k_cache, "k_cache", u8, codes)
         _need(v_cache, "v_cache", u8, codes)
-        if d.head_dim in (64, 128):  # the library refuses others
+        if dim in (64, 128):  # the library refuses others
             _need(k_scale_zero, "k_scale_zero", dtype, pairs)
             _need(v_scale_zero, "v_scale_zero", dtype, pairs)
-    return d
+    return d, kv, dim
 
 
 def _int4_rows(name, stream, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
@@ -521,9 +532,9 @@ def _int4_rows(name, stream, key, value, k_cache, v_cache, k_scale_zero, v_scale
                        slot_mapping, status)
     dtype, i32 = key.dtype, _torch().int32
     code = _dtype_code(key)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype)
+    d, kv, dim = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype)
     T, = _extents(slot_mapping, "slot_mapping", 1)
-    rows = (T, d.num_kv_heads, d.head_dim)
+    rows = (T, kv, dim)
     if not (slot_mapping.dtype is i32 and value.dtype is dtype and key.shape == rows and
             value.shape == rows and slot_mapping.is_contiguous() and key.is_contiguous() and
             value.is_contiguous()):
@@ -559,7 +570,7 @@ def kvp_copy_blocks_int4(k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, *,
     lib = load_library()
     s = _on_one_device(stream, k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, status)
     _dtype_code(k_scale_zero)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, k_scale_zero.dtype)
+    d, _, _ = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, k_scale_zero.dtype)
     _need(pairs, "pairs", _torch().int32, (_extents(pairs, "pairs", 2)[0], 2))
     _check(lib.kvp_copy_blocks_int4(k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
@@ -578,10 +589,10 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
                        context_lens, workspace, status)
     dtype, i32 = q.dtype, _torch().int32
     code = _dtype_code(q)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype)
+    d, _, dim = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, dtype)
     B, Hq, _ = _extents(q, "q", 3)
     MB = _extents(block_tables, "block_tables", 2)[1]
-    rows = (B, Hq, d.head_dim)
+    rows = (B, Hq, dim)
     if not (q.shape == rows and out.shape == rows and out.dtype is dtype and
             block_tables.dtype is i32 and context_lens.dtype is i32 and
             block_tables.shape[0] == B and context_lens.shape == (B,) and
@@ -618,7 +629,8 @@ def _rows(t, name, dtype, shape) -> int:
     return st if T > 1 else heads * dim
 
 
-def _rope_args(q_out, q, key, value, d, cos_sin, positions, slot_mapping, sections, interleaved):
+def _rope_args(q_out, q, key, value, kv, dim, cos_sin, positions, slot_mapping, sections,
+               interleaved):
     torch = _torch()
     i32 = torch.int32
     T, = _extents(slot_mapping, "slot_mapping", 1)
@@ -636,7 +648,7 @@ def _rope_args(q_out, q, key, value, d, cos_sin, positions, slot_mapping, sectio
                              f"{len(sections)} axes")
         _need(positions, "positions", i32, (T,) if one else (len(sections), T))
     rope = _rope_desc(R, sections, 1 if interleaved else 0)
-    dtype, kv, dim = key.dtype, d.num_kv_heads, d.head_dim
+    dtype = key.dtype
     ks = _rows(key, "key", dtype, (T, kv, dim))
     vs = _rows(value, "value", dtype, (T, kv, dim))
     if q is None or q_out is None:
@@ -663,7 +675,7 @@ def kvp_rope_append(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, 
     (contiguous heads, any token stride that is a multiple of 8); q_out may be
     q.  Tokens with a negative slot are skipped."""
     lib = load_library()
-    s = _on_one_device(stream, q_out, q, key, value, k_cache, v_cache, cos_sin, positions,
+    s = _on_one_device(stream, key, value, q_out, q, k_cache, v_cache, cos_sin, positions,
                        slot_mapping, status)
     dtype = key.dtype
     code = _dtype_code(key)
@@ -673,8 +685,8 @@ def kvp_rope_append(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, 
             k_cache.is_contiguous() and v_cache.is_contiguous()):
         _need(k_cache, "k_cache", dtype, pool)
         _need(v_cache, "v_cache", dtype, pool)
-    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d, cos_sin, positions, slot_mapping,
-                                      sections, interleaved)
+    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, pool[1], pool[3], cos_sin, positions,
+                                      slot_mapping, sections, interleaved)
     _check(lib.kvp_rope_append(*rows, k_cache.data_ptr(), v_cache.data_ptr(), cos_sin.data_ptr(),
                                P, positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, rope, d,
                                code, _ptr(status), s), "kvp_rope_append")
@@ -686,12 +698,12 @@ def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v
     """As kvp_rope_append into 4-bit pools (see kvp_append_int4): the rotated key,
     rounded to its dtype, and value are quantised."""
     lib = load_library()
-    s = _on_one_device(stream, q_out, q, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
+    s = _on_one_device(stream, key, value, q_out, q, k_cache, v_cache, k_scale_zero, v_scale_zero,
                        cos_sin, positions, slot_mapping, status)
     code = _dtype_code(key)
-    d = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
-    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, d, cos_sin, positions, slot_mapping,
-                                      sections, interleaved)
+    d, kv, dim = _int4_pools(k_cache, v_cache, k_scale_zero, v_scale_zero, key.dtype)
+    T, Hq, rope, P, rows = _rope_args(q_out, q, key, value, kv, dim, cos_sin, positions,
+                                      slot_mapping, sections, interleaved)
     _check(lib.kvp_rope_append_int4(*rows, k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
                                     cos_sin.data_ptr(), P, positions.data_ptr(),
