@@ -4,8 +4,10 @@ Thin marshalling over the C ABI in ``include/kvp.h``: every function here has
 the C entry point's name, turns torch tensors into pointers and sizes, passes
 torch's current CUDA stream, and raises :class:`KvpError` on a non-OK status.
 All computation happens in the library's CUDA kernels; there is no fallback.
-If ``_lib/libkvp.so`` has not been built, the first call raises
-``RuntimeError`` (build it with ``__graft_entry__.build()`` or
+The short entry points (4-bit cache, rotary append, tables) are called through
+``_lib/_kvp_calls.so``, which looks at the tensors in C++.
+If the libraries have not been built, the first call raises
+``RuntimeError`` (build them with ``__graft_entry__.build()`` or
 ``python -m pagedattention_decode_kvp_gb300._build``).
 
 Block manager: :class:`BlockManager` wraps the host allocator (``kvp_bm_*``).
@@ -14,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -434,9 +437,43 @@ def kvp_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, 
 
 
 # ------------------------------------------------------------------ 4-bit cache
-# The calls below are short on the GPU, so their checks are written to cost
-# little: one expression tells whether everything is in order, and only where it
-# is not are the arguments gone through one by one for the error.
+# The calls below are short on the GPU, and looking at a dozen tensors from here
+# takes longer: _kvp_calls.so (csrc/kvp_calls.cpp) makes a call that is in order
+# beyond doubt, on the current stream.  Everything else -- other streams, and
+# whatever turns out wrong -- takes the way in this file, where the checks and
+# their errors are.
+@functools.lru_cache(maxsize=None)
+def _calls():
+    _torch()  # its libraries first
+    load_library()
+    path = os.path.join(os.path.dirname(LIB_PATH), "_kvp_calls.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"_kvp_calls.so is not built ({path}); run __graft_entry__.build() or "
+                           "python -m pagedattention_decode_kvp_gb300._build")
+    spec = importlib.util.spec_from_file_location("_kvp_calls", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def _made(status: Optional[int], where: str) -> bool:
+    """Whether _kvp_calls made the call (None: it did not)."""
+    if status is None:
+        return False
+    if status != KVP_OK:
+        raise KvpError(status, where)
+    return True
+
+
+def _status_ptr(status) -> Optional[int]:
+    if status is None:
+        return None
+    if status.dtype is not _torch().int32 or status.numel() < 1:
+        raise TypeError(f"status must be an int32 word, got {status.dtype}, "
+                        f"shape {tuple(status.shape)}")
+    return status.data_ptr()
+
+
 def _on_one_device(stream, *ts) -> int:
     """CUDA tensors (the first one is there) of the current device, where kernels
     launch; returns the stream to use."""
@@ -544,7 +581,7 @@ def _int4_rows(name, stream, key, value, k_cache, v_cache, k_scale_zero, v_scale
     _check(getattr(lib, name)(
         key.data_ptr(), value.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), slot_mapping.data_ptr(), T, d,
-        _ptr(status), s), name)
+        _status_ptr(status), s), name)
 
 
 def kvp_append_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot_mapping, *,
@@ -552,6 +589,10 @@ def kvp_append_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, sl
     """Quantise key/value [T, Hkv, D] (fp16/bf16) to 4 bits with one (scale, zero)
     pair per 64 elements and scatter them: codes into uint8 pools
     [NB, Hkv, bs, D/2], pairs into [NB, Hkv, bs, D/64, 2] of key's dtype."""
+    if stream is None and _made(_calls().append_int4(
+            key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot_mapping, status),
+            "kvp_append_int4"):
+        return
     _int4_rows("kvp_append_int4", stream, key, value, k_cache, v_cache, k_scale_zero,
                v_scale_zero, slot_mapping, status)
 
@@ -560,6 +601,10 @@ def kvp_read_int4(key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot
                   status=None, stream=None) -> None:
     """key/value [T, Hkv, D] = the values held in 4 bits at slot_mapping [T]
     (rows of negative slots are left as they are)."""
+    if stream is None and _made(_calls().read_int4(
+            key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, slot_mapping, status),
+            "kvp_read_int4"):
+        return
     _int4_rows("kvp_read_int4", stream, key, value, k_cache, v_cache, k_scale_zero,
                v_scale_zero, slot_mapping, status)
 
@@ -574,7 +619,7 @@ def kvp_copy_blocks_int4(k_cache, v_cache, k_scale_zero, v_scale_zero, pairs, *,
     _need(pairs, "pairs", _torch().int32, (_extents(pairs, "pairs", 2)[0], 2))
     _check(lib.kvp_copy_blocks_int4(k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
-                                    pairs.data_ptr(), pairs.shape[0], d, _ptr(status), s),
+                                    pairs.data_ptr(), pairs.shape[0], d, _status_ptr(status), s),
            "kvp_copy_blocks_int4")
 
 
@@ -584,6 +629,10 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
     """As kvp_attention_decode over 4-bit pools (see kvp_append_int4); q, out and
     the (scale, zero) pairs share one dtype.  Workspace:
     kvp_decode_workspace_bytes(..., kv_int4=True)."""
+    if stream is None and _made(_calls().attention_decode_int4(
+            out, q, k_cache, v_cache, k_scale_zero, v_scale_zero, block_tables, context_lens,
+            scale, workspace, partition_blocks, phases, status), "kvp_attention_decode_int4"):
+        return
     lib = load_library()
     s = _on_one_device(stream, out, q, k_cache, v_cache, k_scale_zero, v_scale_zero, block_tables,
                        context_lens, workspace, status)
@@ -611,7 +660,7 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
         out.data_ptr(), q.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), block_tables.data_ptr(), MB,
         context_lens.data_ptr(), B, Hq, scale, d, partition_blocks, ws, ws_bytes, phases,
-        _ptr(status), s), "kvp_attention_decode_int4")
+        _status_ptr(status), s), "kvp_attention_decode_int4")
 
 
 # ------------------------------------------------------------------ rotary append
@@ -674,6 +723,10 @@ def kvp_rope_append(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, 
     (i, i + R/2).  q, key and value may be slices of one projection's output
     (contiguous heads, any token stride that is a multiple of 8); q_out may be
     q.  Tokens with a negative slot are skipped."""
+    if stream is None and _made(_calls().rope_append(
+            q_out, q, key, value, k_cache, v_cache, cos_sin, positions, slot_mapping, sections,
+            interleaved, status), "kvp_rope_append"):
+        return
     lib = load_library()
     s = _on_one_device(stream, key, value, q_out, q, k_cache, v_cache, cos_sin, positions,
                        slot_mapping, status)
@@ -689,7 +742,7 @@ def kvp_rope_append(q_out, q, key, value, k_cache, v_cache, cos_sin, positions, 
                                       slot_mapping, sections, interleaved)
     _check(lib.kvp_rope_append(*rows, k_cache.data_ptr(), v_cache.data_ptr(), cos_sin.data_ptr(),
                                P, positions.data_ptr(), slot_mapping.data_ptr(), T, Hq, rope, d,
-                               code, _ptr(status), s), "kvp_rope_append")
+                               code, _status_ptr(status), s), "kvp_rope_append")
 
 
 def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero,
@@ -697,6 +750,10 @@ def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v
                          status=None, stream=None) -> None:
     """As kvp_rope_append into 4-bit pools (see kvp_append_int4): the rotated key,
     rounded to its dtype, and value are quantised."""
+    if stream is None and _made(_calls().rope_append_int4(
+            q_out, q, key, value, k_cache, v_cache, k_scale_zero, v_scale_zero, cos_sin,
+            positions, slot_mapping, sections, interleaved, status), "kvp_rope_append_int4"):
+        return
     lib = load_library()
     s = _on_one_device(stream, key, value, q_out, q, k_cache, v_cache, k_scale_zero, v_scale_zero,
                        cos_sin, positions, slot_mapping, status)
@@ -707,7 +764,7 @@ def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v
     _check(lib.kvp_rope_append_int4(*rows, k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
                                     cos_sin.data_ptr(), P, positions.data_ptr(),
-                                    slot_mapping.data_ptr(), T, Hq, rope, d, code, _ptr(status),
+                                    slot_mapping.data_ptr(), T, Hq, rope, d, code, _status_ptr(status),
                                     s), "kvp_rope_append_int4")
 
 
@@ -728,6 +785,10 @@ def kvp_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_co
     (-1 behind the new tokens) and positions [T] are written.  All int32.
     context_lens_out / free_count_out may be context_lens / free_count.  All or
     nothing: see kvp.h for the device errors."""
+    if stream is None and _made(_calls().extend_tables(
+            block_tables, context_lens, new_lens, free_blocks, free_count, context_lens_out,
+            free_count_out, slot_mapping, query_start, positions, status), "kvp_extend_tables"):
+        return
     lib = load_library()
     s = _on_one_device(stream, block_tables, context_lens, new_lens, free_blocks, free_count,
                        context_lens_out, free_count_out, slot_mapping, query_start, positions,
@@ -759,7 +820,7 @@ def kvp_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_co
                                  new_lens.data_ptr(), B, free_blocks.data_ptr(),
                                  free_count.data_ptr(), NB, context_lens_out.data_ptr(),
                                  free_count_out.data_ptr(), slot_mapping.data_ptr(), T,
-                                 query_start.data_ptr(), _ptr(positions), _ptr(status), s),
+                                 query_start.data_ptr(), _ptr(positions), _status_ptr(status), s),
            "kvp_extend_tables")
 
 
@@ -767,6 +828,10 @@ def kvp_release_tables(block_tables, context_lens, finished, free_blocks, free_c
                        context_lens_out, free_count_out, *, status=None, stream=None) -> None:
     """Push the blocks of every request with finished[b] != 0 on the free stack
     and set its length to 0 (all int32; outputs as kvp_extend_tables)."""
+    if stream is None and _made(_calls().release_tables(
+            block_tables, context_lens, finished, free_blocks, free_count, context_lens_out,
+            free_count_out, status), "kvp_release_tables"):
+        return
     lib = load_library()
     s = _on_one_device(stream, block_tables, context_lens, finished, free_blocks, free_count,
                        context_lens_out, free_count_out, status)
@@ -789,7 +854,7 @@ def kvp_release_tables(block_tables, context_lens, finished, free_blocks, free_c
     _check(lib.kvp_release_tables(block_tables.data_ptr(), MB, context_lens.data_ptr(),
                                   finished.data_ptr(), B, free_blocks.data_ptr(),
                                   free_count.data_ptr(), NB, context_lens_out.data_ptr(),
-                                  free_count_out.data_ptr(), _ptr(status), s),
+                                  free_count_out.data_ptr(), _status_ptr(status), s),
            "kvp_release_tables")
 
 
@@ -797,14 +862,14 @@ def kvp_selftest_wait_timeout(status, limit_ns, stream=None):
     """Run the library's bounded mbarrier wait on a barrier nothing arrives
     on, giving up after limit_ns: it records KVP_ERR_TIMEOUT in `status`."""
     _need_cuda(status)
-    _check(load_library().kvp_selftest_wait_timeout(_ptr(status), int(limit_ns),
+    _check(load_library().kvp_selftest_wait_timeout(_status_ptr(status), int(limit_ns),
                                                      _stream_ptr(stream)),
            "kvp_selftest_wait_timeout")
 
 
 def kvp_read_status(status, stream=None) -> int:
     """Synchronise the stream and return the device status word's kvp_status."""
-    return int(load_library().kvp_read_status(_ptr(status), _stream_ptr(stream)))
+    return int(load_library().kvp_read_status(_status_ptr(status), _stream_ptr(stream)))
 
 
 # ------------------------------------------------------------------ block manager

@@ -1,15 +1,18 @@
-"""In-tree build of libkvp.so (nvcc, sm_103a only).
+"""In-tree build of libkvp.so (nvcc, sm_103a only) and of _kvp_calls.so, the
+binding of its short calls (g++, against the installed torch).
 
 Each translation unit is compiled in parallel to an object under ``_build/``
-and linked with ``nvcc -shared`` into ``_lib/libkvp.so``; an object is rebuilt
-when it is older than its source or any header.  No cmake, no ninja.
+and linked into ``_lib/``; an object is rebuilt when it is older than its source
+or any header.  No cmake, no ninja.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libkvp.so")
+CALLS_PATH = os.path.join(LIB_DIR, "_kvp_calls.so")
+CALLS_SOURCE = "kvp_calls.cpp"
 
 SOURCES = [
     "kvp_api.cu",
@@ -41,9 +46,17 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3",
               f"-I{INCLUDE}", f"-I{CSRC}"]
 
 
+def _cuda_home() -> str:
+    return os.environ.get("CUDA_HOME", "/usr/local/cuda")
+
+
 def _nvcc() -> str:
-    cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
+    cand = os.path.join(_cuda_home(), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
+
+
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
 
 
 def _headers_mtime() -> float:
@@ -56,22 +69,38 @@ def _compile(src: str, ptxas_verbose: bool) -> tuple[str, str]:
     s = os.path.join(CSRC, src)
     o = os.path.join(BUILD_DIR, src + ".o")
     cmd = [_nvcc(), *ARCH, *NVCC_FLAGS, "-c", s, "-o", o]
+    if src == CALLS_SOURCE:
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-I{INCLUDE}",
+               f"-I{_torch_dir()}/include", f"-I{_cuda_home()}/include",
+               f"-I{sysconfig.get_paths()['include']}", "-c", s, "-o", o]
     if ptxas_verbose and src.endswith(".cu"):
         cmd += ["-Xptxas", "-v"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
     return o, r.stderr
 
 
+def _link(path: str, objs: list[str], cmd: list[str], anew: bool) -> None:
+    if not anew and os.path.exists(path) and \
+            os.path.getmtime(path) >= max(os.path.getmtime(o) for o in objs):
+        return
+    tmp = path + f".tmp{os.getpid()}"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile (incrementally) and link libkvp.so; returns its path."""
+    """Compile (incrementally) and link libkvp.so and _kvp_calls.so; returns the
+    former's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     hdr = _headers_mtime()
     todo = []
     objs = []
-    for src in SOURCES:
+    for src in [*SOURCES, CALLS_SOURCE]:
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD_DIR, src + ".o")
         objs.append(o)
@@ -83,14 +112,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         with cf.ThreadPoolExecutor(max_workers=min(len(todo), os.cpu_count() or 4)) as ex:
             for _, log in ex.map(lambda f: _compile(f, ptxas_verbose), todo):
                 logs.append(log)
-    if todo or force or not os.path.exists(LIB_PATH) or \
-            os.path.getmtime(LIB_PATH) < max(os.path.getmtime(o) for o in objs):
-        tmp = LIB_PATH + f".tmp{os.getpid()}"
-        cmd = [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp, "-ldl"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB_PATH)
+    calls = objs.pop()
+    _link(LIB_PATH, objs, [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-ldl"],
+          force or any(s != CALLS_SOURCE for s in todo))
+    lib = os.path.join(_torch_dir(), "lib")
+    _link(CALLS_PATH, [calls], ["g++", "-shared", calls, f"-L{LIB_DIR}", "-lkvp", f"-L{lib}",
+                                "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                                "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
+          force or CALLS_SOURCE in todo)
     if verbose or ptxas_verbose:
         for log in logs:
             if log.strip():

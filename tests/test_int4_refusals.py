@@ -280,3 +280,18 @@ def test_plain_tables_by_hand():
     assert slots == [95, 0, 112, -1] and starts == [0, 2, 3] and pos == [15, 16, 0, 0]
     n, free, top = plain64.release(t, n, [1, 0], free, top)
     assert n == [0, 1] and top == 5 and free == [4, 9, 2, 5, 0]
+
+
+def test_compiled_calls_leave_cpu_tensors_to_the_checks(lib):
+    x, z = torch.zeros(2, 2, 64, dtype=torch.float16), torch.zeros(2, dtype=torch.int32)
+    kc, ks = torch.zeros(4, 2, 16, 32, dtype=torch.uint8), \
+        torch.zeros(4, 2, 16, 1, 2, dtype=torch.float16)
+    c = kvp._calls()
+    assert c.append_int4(x, x, kc, kc, ks, ks, z, None) is None
+    assert c.read_int4() is None and c.extend_tables(z, z) is None and c.release_tables() is None
+    assert c.attention_decode_int4(x) is None and c.rope_append(x, x, x, x) is None
+    assert c.rope_append_int4(None) is None
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        kvp.kvp_append_int4(x, x, kc, kc, ks, ks, z)
+    with pytest.raises(TypeError, match="status"):
+        kvp._status_ptr(z.long())
