@@ -731,13 +731,23 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
     if (threadIdx.x == 0) p.notes[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (!find_piece(p, index, pieces, walk)) return;
   } else {
-    const int b = blockIdx.z, n = p.context_lens[b], nblk = blocks_of(p, n);
-    const int blk0 = blockIdx.x * p.part_blocks;
+    // The table's slice comes beside the length, entries behind the context
+    // included (nothing looks at those): one trip to memory less, 0.5 us of 5.
+    const int b = blockIdx.z, blk0 = blockIdx.x * p.part_blocks;
+    const int32_t* row = p.block_tables + static_cast<size_t>(b) * p.max_blocks + blk0;
+    const int most = min(min(p.part_blocks, kTable), p.max_blocks - blk0);
+    for (int i = threadIdx.x; i < most; i += blockDim.x)
+      cp_async4(dev::smem_addr(tables) + i * 4, row + i);
+    cp_async_commit();
+    const int n = p.context_lens[b], nblk = blocks_of(p, n);
     if (nblk == 0 && blk0 == 0) {
       zero_rows<D>(p, b, head0, nheads);
       if (n != 0 && threadIdx.x == 0) dev::set_status(p.status, kErrBadBlock);
     }
-    if (blk0 >= nblk) return;
+    if (blk0 >= nblk) {
+      cp_async_wait<0>();
+      return;
+    }
     if (threadIdx.x == 0) {
       walk.pos = 0;
       walk.end = min(p.part_blocks, nblk - blk0);
@@ -790,8 +800,10 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
     return bad;
   };
 
-  fetch_table(0);
-  cp_async_commit();
+  if (balanced) {
+    fetch_table(0);
+    cp_async_commit();
+  }
   cp_async_wait<0>();
   bool bad = __syncthreads_or(table_bad(0)) != 0;  // of this segment's table
   bool run_bad = false;                            // of the run

@@ -147,8 +147,6 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablePara
   }
   longlong2 sum;
   longlong2 at = block_scan(mine, &sum);
-  if (sum.x > p.num_tokens || count < 0 || count > p.num_blocks) err = kErrBadBlock;
-  else if (sum.y > count && err == 0) err = KVP_ERR_OOM;
   for (int b = b0; b < b1; ++b) {  // (wrong lengths give wrong offsets, which nothing uses)
     const int n = p.context_lens[b], k = p.new_lens[b];
     tok0[b] = static_cast<int32_t>(at.x);
@@ -157,8 +155,10 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const TablePara
     at.x += k;
     at.y += blocks_for(n + k) - blocks_for(n);
   }
-  err = __syncthreads_or(err == kErrBadBlock) ? kErrBadBlock
-                                              : (__syncthreads_or(err) ? KVP_ERR_OOM : 0);
+  if (__syncthreads_or(err) || sum.x > p.num_tokens || count < 0 || count > p.num_blocks)
+    err = kErrBadBlock;
+  else if (sum.y > count)
+    err = KVP_ERR_OOM;
   const int tokens = static_cast<int>(sum.x), blocks = static_cast<int>(sum.y);
 
   // ---- the ids this step will use: blocks off the stack, and the partly
@@ -299,23 +299,23 @@ __global__ void __launch_bounds__(kThreads) release_tables_kernel(const TablePar
   }
   longlong2 sum;
   longlong2 at = block_scan(mine, &sum);
-  if (count < 0 || count > p.num_blocks) err = kErrBadBlock;
-  else if (count + sum.y > p.num_blocks && err == 0) err = KVP_ERR_REFCOUNT;
   for (int b = b0; b < b1; ++b) {
     blk0[b] = static_cast<int32_t>(at.y);
     if (p.finished[b] != 0) at.y += blocks_for(p.context_lens[b]);
   }
-  err = __syncthreads_or(err == kErrBadBlock) ? kErrBadBlock
-                                              : (__syncthreads_or(err) ? KVP_ERR_REFCOUNT : 0);
+  if (__syncthreads_or(err) || count < 0 || count > p.num_blocks) err = kErrBadBlock;
+  else if (count + sum.y > p.num_blocks) err = KVP_ERR_REFCOUNT;
   const int blocks = static_cast<int>(sum.y);
   auto id_of = [&](int j) {
     const int b = find_request(blk0, p.batch, j);
     return p.block_tables[static_cast<size_t>(b) * p.max_blocks + (j - blk0[b])];
   };
+  int mine0 = 0;  // this thread's first id, mostly its only one
   if (err == 0) {
     for (int j = first; j < blocks; j += stride) {
       const int id = id_of(j);
       if (id < 0 || id >= p.num_blocks) err = kErrBadBlock;
+      if (j == first) mine0 = id;
     }
   }
   err = cluster_error(err);
@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(kThreads) release_tables_kernel(const TablePar
     return;
   }
   if (first == 0) *p.free_count_out = count + blocks;
-  for (int j = first; j < blocks; j += stride) p.free_blocks[count + j] = id_of(j);
+  for (int j = first; j < blocks; j += stride)
+    p.free_blocks[count + j] = j == first ? mine0 : id_of(j);
   for (int b = first; b < p.batch; b += stride)
     p.context_lens_out[b] = p.finished[b] != 0 ? 0 : p.context_lens[b];
 }
