@@ -25,12 +25,13 @@
 // split-half pair are its own, and uses its 8 (cos, sin) pairs for every head
 // of the token it works on.  Measured, prompts of 33098 tokens, 32 kv heads of
 // 128 (shares of the measured copy bandwidth): rotation with a 16-bit append 242
-// us (0.96 to 1.0), 4-bit append 140 us (0.71), read-back 110 us (0.90);
+// us (0.96 to 1.0), 4-bit append 138 us (0.72), read-back 110 us (0.90);
 // rotation with a 4-bit append, 8191 tokens of 64 + 8 heads, 56 us (0.79).  The
-// quantiser is what holds the 4-bit appends: 419 instructions for four K and four
-// V rows fill 67% of the issue slots, and neither more CTAs per SM (139 us with
-// 9, 142 with 10, spilling) nor the next rows' loads ahead of the arithmetic
-// (138 us at 6 CTAs, 150 at 8) change that.  A step of 64 tokens takes 2.9 us.
+// quantiser is what holds the 4-bit appends: 403 instructions for four K and four
+// V rows fill 67% of the issue slots, and neither more CTAs per SM (with the 8 at
+// 140 us: 139 with 9, 142 with 10, spilling) nor the next rows' loads ahead of the
+// arithmetic (138 at 6 CTAs, 150 at 8) change that, nor one check over all of a
+// lane's elements (157: exact ties are common).  A step of 64 tokens takes 2.9 us.
 #include "kvp_device.cuh"
 #include "kvp_serve.h"
 
@@ -178,10 +179,23 @@ __device__ __forceinline__ uint32_t pack_nibbles(const uint32_t (&k)[8]) {
   return odd * 16u + even;
 }
 
+// Both 16-bit halves of w less z, each rounded once to float32.
+template <bool kBf16>
+__device__ __forceinline__ float2 sub2(uint32_t w, float z) {
+  float2 d;
+  if constexpr (kBf16)
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; sub.rn.f32.bf16 %0, l, %3; sub.rn.f32.bf16 %1, h, %3;}"
+        : "=f"(d.x), "=f"(d.y) : "r"(w), "f"(z));
+  else
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; sub.rn.f32.f16 %0, l, %3; sub.rn.f32.f16 %1, h, %3;}"
+        : "=f"(d.x), "=f"(d.y) : "r"(w), "f"(z));
+  return d;
+}
+
 template <bool kBf16>
 __device__ __forceinline__ uint32_t quantise8_u4(const uint4& raw, float s, float z, Bracket b) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  const uint64_t nz2 = dev::f2pack(-z, -z), magic2 = dev::f2pack(kMagic, kMagic);
+  const uint64_t magic2 = dev::f2pack(kMagic, kMagic);
   const uint64_t lo2 = dev::f2pack(b.lo, b.lo), hi2 = dev::f2pack(b.hi, b.hi);
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   const uint64_t minus2 = dev::f2pack(-1.f, -1.f);
@@ -190,9 +204,8 @@ __device__ __forceinline__ uint32_t quantise8_u4(const uint4& raw, float s, floa
   float d[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = dev::unpack2<kBf16>(w[i]);
-    const uint64_t d2 = dev::fadd2(dev::f2pack(x.x, x.y), nz2);
-    const float2 du = dev::f2unpack(d2);
+    const float2 du = sub2<kBf16>(w[i], z);
+    const uint64_t d2 = dev::f2pack(du.x, du.y);
     const float2 mu = dev::f2unpack(dev::ffma2(d2, lo2, magic2));
     more2[i] = dev::ffma2(dev::f2pack(mu.x, mu.y), minus2, dev::ffma2(d2, hi2, magic2));
     sum2 = dev::fadd2(sum2, more2[i]);
