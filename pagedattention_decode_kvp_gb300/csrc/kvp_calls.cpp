@@ -124,10 +124,18 @@ PyObject* guarded(F&& call) {
   Py_RETURN_NONE;
 }
 
-#define KVP_WITHOUT_GIL(...)  \
-  Py_BEGIN_ALLOW_THREADS;     \
-  __VA_ARGS__;                \
-  Py_END_ALLOW_THREADS
+// Other threads may run Python while a launch is made (given back on the way of an
+// exception as well).
+class WithoutGil {
+ public:
+  WithoutGil() : state_(PyEval_SaveThread()) {}
+  ~WithoutGil() { PyEval_RestoreThread(state_); }
+  WithoutGil(const WithoutGil&) = delete;
+  WithoutGil& operator=(const WithoutGil&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
 
 // key, value, pools, slot_mapping, status
 template <bool kRead>
@@ -147,16 +155,17 @@ PyObject* rows_int4(PyObject*, PyObject* const* args, Py_ssize_t n) {
         value->sizes() != key->sizes())
       return false;
     const kvp_stream_t st = a.stream();
-    KVP_WITHOUT_GIL(*s = kRead ? kvp_read_int4(ptr<void>(key), ptr<void>(value), dt,
-                                               ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
-                                               ptr<void>(p.ks), ptr<void>(p.vs),
-                                               ptr<int32_t>(slots), static_cast<int32_t>(T), p.d,
-                                               status, st)
-                               : kvp_append_int4(ptr<void>(key), ptr<void>(value), dt,
-                                                 ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
-                                                 ptr<void>(p.ks), ptr<void>(p.vs),
-                                                 ptr<int32_t>(slots), static_cast<int32_t>(T),
-                                                 p.d, status, st));
+    const WithoutGil guard;
+    *s = kRead ? kvp_read_int4(ptr<void>(key), ptr<void>(value), dt,
+                               ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
+                               ptr<void>(p.ks), ptr<void>(p.vs),
+                               ptr<int32_t>(slots), static_cast<int32_t>(T), p.d,
+                               status, st)
+               : kvp_append_int4(ptr<void>(key), ptr<void>(value), dt,
+                                 ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
+                                 ptr<void>(p.ks), ptr<void>(p.vs),
+                                 ptr<int32_t>(slots), static_cast<int32_t>(T),
+                                 p.d, status, st);
     return true;
   });
 }
@@ -184,13 +193,14 @@ PyObject* attention_decode_int4(PyObject*, PyObject* const* args, Py_ssize_t n) 
         out->sizes() != q->sizes() || tables->size(0) != B || !shape(lens, {B}))
       return false;
     const kvp_stream_t st = a.stream();
-    KVP_WITHOUT_GIL(*s = kvp_attention_decode_int4(
-                        ptr<void>(out), ptr<void>(q), dt, ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
-                        ptr<void>(p.ks), ptr<void>(p.vs), ptr<int32_t>(tables),
-                        static_cast<int32_t>(MB), ptr<int32_t>(lens), static_cast<int32_t>(B),
-                        static_cast<int32_t>(Hq), scale, p.d, part,
-                        ws != nullptr ? ws->data_ptr() : nullptr, ws != nullptr ? ws->nbytes() : 0,
-                        phases, status, st));
+    const WithoutGil guard;
+    *s = kvp_attention_decode_int4(
+        ptr<void>(out), ptr<void>(q), dt, ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
+        ptr<void>(p.ks), ptr<void>(p.vs), ptr<int32_t>(tables),
+        static_cast<int32_t>(MB), ptr<int32_t>(lens), static_cast<int32_t>(B),
+        static_cast<int32_t>(Hq), scale, p.d, part,
+        ws != nullptr ? ws->data_ptr() : nullptr, ws != nullptr ? ws->nbytes() : 0,
+        phases, status, st);
     return true;
   });
 }
@@ -270,20 +280,22 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
       return false;
     const kvp_stream_t st = a.stream();
     if constexpr (kInt4) {
-      KVP_WITHOUT_GIL(*s = kvp_rope_append_int4(
-                          ptr<void>(qo), qos, ptr<void>(q), qs, ptr<void>(key), ks,
-                          ptr<void>(value), vs, ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
-                          ptr<void>(p.ks), ptr<void>(p.vs), ptr<float>(cs),
-                          static_cast<int32_t>(P), ptr<int32_t>(pos), ptr<int32_t>(slots),
-                          static_cast<int32_t>(T), static_cast<int32_t>(Hq), rope, d, dt, status,
-                          st));
+      const WithoutGil guard;
+      *s = kvp_rope_append_int4(
+          ptr<void>(qo), qos, ptr<void>(q), qs, ptr<void>(key), ks,
+          ptr<void>(value), vs, ptr<uint8_t>(p.kc), ptr<uint8_t>(p.vc),
+          ptr<void>(p.ks), ptr<void>(p.vs), ptr<float>(cs),
+          static_cast<int32_t>(P), ptr<int32_t>(pos), ptr<int32_t>(slots),
+          static_cast<int32_t>(T), static_cast<int32_t>(Hq), rope, d, dt, status,
+          st);
     } else {
-      KVP_WITHOUT_GIL(*s = kvp_rope_append(
-                          ptr<void>(qo), qos, ptr<void>(q), qs, ptr<void>(key), ks,
-                          ptr<void>(value), vs, ptr<void>(kc), ptr<void>(vc), ptr<float>(cs),
-                          static_cast<int32_t>(P), ptr<int32_t>(pos), ptr<int32_t>(slots),
-                          static_cast<int32_t>(T), static_cast<int32_t>(Hq), rope, d, dt, status,
-                          st));
+      const WithoutGil guard;
+      *s = kvp_rope_append(
+          ptr<void>(qo), qos, ptr<void>(q), qs, ptr<void>(key), ks,
+          ptr<void>(value), vs, ptr<void>(kc), ptr<void>(vc), ptr<float>(cs),
+          static_cast<int32_t>(P), ptr<int32_t>(pos), ptr<int32_t>(slots),
+          static_cast<int32_t>(T), static_cast<int32_t>(Hq), rope, d, dt, status,
+          st);
     }
     return true;
   });
@@ -308,13 +320,14 @@ PyObject* extend_tables(PyObject*, PyObject* const* args, Py_ssize_t n) {
         !shape(t[8], {B + 1}) || (pos != nullptr && !shape(pos, {T})))
       return false;
     const kvp_stream_t st = a.stream();
-    KVP_WITHOUT_GIL(*s = kvp_extend_tables(
-                        ptr<int32_t>(t[0]), static_cast<int32_t>(MB), ptr<int32_t>(t[1]),
-                        ptr<int32_t>(t[2]), static_cast<int32_t>(B), ptr<int32_t>(t[3]),
-                        ptr<int32_t>(t[4]), static_cast<int32_t>(NB), ptr<int32_t>(t[5]),
-                        ptr<int32_t>(t[6]), ptr<int32_t>(t[7]), static_cast<int32_t>(T),
-                        ptr<int32_t>(t[8]), pos != nullptr ? ptr<int32_t>(pos) : nullptr, status,
-                        st));
+    const WithoutGil guard;
+    *s = kvp_extend_tables(
+        ptr<int32_t>(t[0]), static_cast<int32_t>(MB), ptr<int32_t>(t[1]),
+        ptr<int32_t>(t[2]), static_cast<int32_t>(B), ptr<int32_t>(t[3]),
+        ptr<int32_t>(t[4]), static_cast<int32_t>(NB), ptr<int32_t>(t[5]),
+        ptr<int32_t>(t[6]), ptr<int32_t>(t[7]), static_cast<int32_t>(T),
+        ptr<int32_t>(t[8]), pos != nullptr ? ptr<int32_t>(pos) : nullptr, status,
+        st);
     return true;
   });
 }
@@ -335,11 +348,12 @@ PyObject* release_tables(PyObject*, PyObject* const* args, Py_ssize_t n) {
         !shape(t[4], {1}) || !shape(t[5], {B}) || !shape(t[6], {1}))
       return false;
     const kvp_stream_t st = a.stream();
-    KVP_WITHOUT_GIL(*s = kvp_release_tables(
-                        ptr<int32_t>(t[0]), static_cast<int32_t>(MB), ptr<int32_t>(t[1]),
-                        ptr<int32_t>(t[2]), static_cast<int32_t>(B), ptr<int32_t>(t[3]),
-                        ptr<int32_t>(t[4]), static_cast<int32_t>(NB), ptr<int32_t>(t[5]),
-                        ptr<int32_t>(t[6]), status, st));
+    const WithoutGil guard;
+    *s = kvp_release_tables(
+        ptr<int32_t>(t[0]), static_cast<int32_t>(MB), ptr<int32_t>(t[1]),
+        ptr<int32_t>(t[2]), static_cast<int32_t>(B), ptr<int32_t>(t[3]),
+        ptr<int32_t>(t[4]), static_cast<int32_t>(NB), ptr<int32_t>(t[5]),
+        ptr<int32_t>(t[6]), status, st);
     return true;
   });
 }

@@ -138,3 +138,53 @@ def test_empty_calls():
     q = torch.zeros((0, 4, 64), dtype=torch.float16, device="cuda")
     assert kvp._calls().attention_decode_int4(q, q, *pools, torch.zeros((0, 3), **z), e, 1.0, None,
                                               0, 3, None) == kvp.KVP_OK
+
+
+def test_a_tensor_without_data_is_an_error():
+    """An exception on the way to the library leaves the interpreter as it was."""
+    fake = pytest.importorskip("torch._subclasses.fake_tensor")
+    with fake.FakeTensorMode():
+        x = torch.empty((2, 2, 64), dtype=torch.float16, device="cuda")
+        kc = torch.empty((4, 2, 16, 32), dtype=torch.uint8, device="cuda")
+        ks = torch.empty((4, 2, 16, 1, 2), dtype=torch.float16, device="cuda")
+        slots = torch.empty(2, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        with pytest.raises(Exception):
+            kvp.kvp_append_int4(x, x, kc, kc, ks, ks, slots)
+    assert sum(range(10)) == 45
+
+
+def test_two_threads_on_two_streams():
+    from threading import Thread
+    calls = [arguments(torch.float16) for _ in range(2)]
+    want = [arguments(torch.float16) for _ in range(2)]
+    for a in want:
+        kvp._calls().rope_append_int4(*a["rope_append_int4"])
+        kvp._calls().append_int4(*a["append_int4"])
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(a):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    r = a["rope_append_int4"]
+                    kvp.kvp_rope_append_int4(*r[:11], sections=r[11], interleaved=r[12],
+                                             status=r[13])
+                    k = a["append_int4"]
+                    kvp.kvp_append_int4(*k[:7], status=k[7])
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [Thread(target=work, args=(a,)) for a in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for a, b in zip(calls, want):
+        for name in ("rope_append_int4", "append_int4"):
+            for x, y in zip(a[name], b[name]):
+                if isinstance(x, torch.Tensor):
+                    assert torch.equal(bits(x), bits(y))
