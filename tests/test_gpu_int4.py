@@ -570,3 +570,15 @@ def test_append_int4_infinities_stay_in_their_rows(dtype):
                            plain64.pack4(c)[fine])
         assert torch.equal(bits(pairs[slots.long() // 16, :, slots.long() % 16])[fine],
                            bits(s)[fine])
+
+
+def test_decode_int4_balanced_runs_longer_than_the_staged_table():
+    """So many query heads that one piece is left: its runs span several slices of
+    their block tables."""
+    c = Case([8300, 0, 9000], 8 * 229, 1, 128, torch.float16, seed=51, max_blocks=600)
+    c.check(c.run())
+    c.tables[2, 540] = 10 ** 6  # in the second slice
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = c.run(0, status)
+    assert kvp.kvp_read_status(status) == kvp.KVP_ERR_BAD_BLOCK
+    assert torch.count_nonzero(out[2]) == 0 and torch.count_nonzero(out[0]) > 0
