@@ -216,10 +216,11 @@ kvp_status shape_decode(int batch, int num_q_heads, const kvp_cache_desc& c, int
     // request; two partial states of up to 8 heads per CTA and a note
     const int per_request = c.num_kv_heads * s.qgroups;
     const int pieces = std::max(1, kSms * int4_ctas_per_sm(c.head_dim) / per_request);
-    const long long even = (static_cast<long long>(batch) * max_blocks + pieces - 1) / pieces;
+    const long long size =
+        cut_contexts(static_cast<long long>(batch) * max_blocks, batch, pieces).size;
     s.part_blocks = 0;
     // (below the table's width: a context can always be cut)
-    s.run_blocks = static_cast<int>(std::min<long long>(std::max(even, 8ll), max_blocks - 1));
+    s.run_blocks = static_cast<int>(std::min<long long>(size, max_blocks - 1));
     s.max_parts = pieces * per_request;
     s.ws_bytes = static_cast<size_t>(s.max_parts) *
                  (2 * kHeadsPerCta * (static_cast<size_t>(c.head_dim) + 2) * sizeof(float) +

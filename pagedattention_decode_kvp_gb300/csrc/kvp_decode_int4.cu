@@ -70,7 +70,6 @@ namespace {
 constexpr int kBuf = 2;       // steps per warp: one in use, one on the way
 constexpr int kCentre = 8;    // steps between two centrings of the sums
 constexpr int kTable = 512;                 // table entries of a segment
-constexpr int kMinRun = 2 * kWarps;          // blocks of a piece at least
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -594,35 +593,64 @@ __device__ __forceinline__ int blocks_of(const Int4DecodeParams& p, int n) {
   return n <= 0 || (n - 1) / kBlockSize >= p.max_blocks ? 0 : (n - 1) / kBlockSize + 1;
 }
 
-__device__ __forceinline__ long long piece_size(long long total, int pieces) {
-  const long long even = (total + pieces - 1) / pieces;
-  return even > kMinRun ? even : kMinRun;
-}
-
-// Sets the walk of piece `index` of `pieces`; false when it has no blocks.
-__device__ __forceinline__ bool find_piece(const Int4DecodeParams& p, int index, int pieces,
-                                           Walk& walk) {
+// Exclusive prefix sum over the CTA's threads; the whole in *total.
+__device__ __forceinline__ long long prefix_sum(long long mine, long long* total) {
   __shared__ long long part[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
-  const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += blocks_of(p, p.context_lens[b]);
   long long sum = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += x;
   }
+  __syncthreads();  // an earlier call's parts are read
   if (lane == 31) part[warp] = sum;
   __syncthreads();
-  long long total = 0, at = sum - mine;
+  long long at = sum - mine;
+  *total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) at += part[w];
-    total += part[w];
+    *total += part[w];
   }
-  const long long size = piece_size(total, pieces), pos = index * size;
+  return at;
+}
+
+// Sets the walk of piece `index` of `pieces`; false when it has no blocks.
+__device__ __forceinline__ bool find_piece(const Int4DecodeParams& p, int index, int pieces,
+                                           Walk& walk) {
+  const int per = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
+  const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += blocks_of(p, p.context_lens[b]);
+  long long total;
+  long long at = prefix_sum(mine, &total);
+  const Cut cut = cut_contexts(total, p.batch, pieces);
+  if (cut.aligned) {
+    const int size = static_cast<int>(cut.size);
+    int runs = 0;
+    for (int b = b0; b < b1; ++b) runs += (blocks_of(p, p.context_lens[b]) + size - 1) / size;
+    long long first = prefix_sum(runs, &total);
+    if (index >= total) return false;
+    if (first <= index && index < first + runs) {
+      int b = b0, n;
+      while (index >= first + (n = (blocks_of(p, p.context_lens[b]) + size - 1) / size)) {
+        first += n;
+        ++b;
+      }
+      walk.b = b;
+      walk.n = p.context_lens[b];
+      walk.nblk = blocks_of(p, walk.n);
+      walk.blk0 = static_cast<int>(index - first) * size;
+      walk.pos = 0;  // (so that the context's pieces are counted from this one)
+      walk.end = min(size, walk.nblk - walk.blk0);
+      walk.size = size;
+      walk.index = walk.left = walk.flags = walk.runs = 0;
+    }
+    __syncthreads();
+    return true;
+  }
+  const long long size = cut.size, pos = index * size;
   if (pos >= total) return false;
   if (at <= pos && pos < at + mine) {  // one thread's requests hold the piece's start
     int b = b0, nblk;
@@ -1018,17 +1046,27 @@ __global__ void __launch_bounds__(512) merge_long_kernel(const Int4DecodeParams 
     start += __shfl_xor_sync(0xffffffffu, start, o);
   }
   const int nblk = blocks_of(p, p.context_lens[b]);
-  const long long size = piece_size(total, pieces);
-  const int first = static_cast<int>(start / size);
-  const int runs = static_cast<int>((start + nblk - 1) / size) - first + 1;
+  const Cut cut = cut_contexts(total, p.batch, pieces);
+  int first = static_cast<int>(start / cut.size);
+  int runs = static_cast<int>((start + nblk - 1) / cut.size) - first + 1;
+  bool later = start % cut.size != 0;  // the first run is its CTA's second
+  if (cut.aligned) {
+    first = 0;
+    for (int i = lane; i < b; i += 32)
+      first += static_cast<int>((blocks_of(p, p.context_lens[i]) + cut.size - 1) / cut.size);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+    runs = static_cast<int>((nblk + cut.size - 1) / cut.size);
+    later = false;
+  }
   if (nblk == 0 || runs <= 1) return;  // its rows are final
   Merge<E> m;
   m.clear();
 #pragma unroll 4
   for (int i = warp; i < runs; i += W)
     m.add(p,
-          (static_cast<size_t>((first + i) * units + unit) * 2 +
-           (i == 0 && start % size != 0 ? 1 : 0)) * 8 + hh,
+          (static_cast<size_t>((first + i) * units + unit) * 2 + (i == 0 && later ? 1 : 0)) * 8 +
+              hh,
           lane);
   if (lane == 0) s_ml[warp] = make_float2(m.M, m.bad ? -1.f : m.L);
 #pragma unroll

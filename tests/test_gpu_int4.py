@@ -582,3 +582,22 @@ def test_decode_int4_balanced_runs_longer_than_the_staged_table():
     out = c.run(0, status)
     assert kvp.kvp_read_status(status) == kvp.KVP_ERR_BAD_BLOCK
     assert torch.count_nonzero(out[2]) == 0 and torch.count_nonzero(out[0]) > 0
+
+
+@pytest.mark.parametrize("Hq,kv,lens", [(8, 1, [9011, 3000, 1, 0, 6345]), (8, 8, [2500, 17, 2499]),
+                                        (32, 16, [1100, 1099, 1088, 1])])
+def test_decode_int4_contexts_cut_by_themselves(Hq, kv, lens):
+    """Few blocks for the GPU: every context is cut alone, into runs of one size."""
+    c = Case(lens, Hq, kv, 64, torch.bfloat16, seed=61, max_blocks=600)
+    out = c.run()
+    c.check(out)
+    for i in range(len(lens)):  # a failed context leaves the others' bits
+        if lens[i] < 1000:
+            continue
+        keep = c.tables[i, lens[i] // 16 - 1].clone()
+        c.tables[i, lens[i] // 16 - 1] = -5
+        bad = c.run()
+        c.tables[i, lens[i] // 16 - 1] = keep
+        assert torch.count_nonzero(bad[i]) == 0
+        others = [j for j in range(len(lens)) if j != i]
+        assert torch.equal(bad[others], out[others])
