@@ -7,10 +7,11 @@
 //         Q_g = sum_{d in g} q_d,
 //   out_d = sum_t p_t (s_tg c_td + z_tg) / sum_t p_t,   p_t = 2^(u_t - m).
 // A CTA walks blocks of one kv head for up to 8 of its query heads: each of its
-// 4 warps streams its own 16-token blocks, a few at a time, through a ring of
-// stages, and the warps' states are merged at the end of a context.  Which blocks
-// a CTA walks: a whole context where tables are short, else an equal piece of all
-// contexts together (see Walk), or a partition of the size the caller asks for.
+// 4 warps (its only one where there are many short runs) streams its own 16-token
+// blocks, a few at a time, through a ring of stages, and the warps' states are
+// merged at the end of a context.  Which blocks a CTA walks: a whole context
+// where tables are short, else a piece of all contexts together (see Walk), or a
+// partition of the size the caller asks for.
 //
 // A block is 2 (8 D + 32 D / 64) bytes = 2304 at D = 128, little over half of
 // an INT8 block, while a warp has the same 32 D codes to widen: unlike the 8-bit
@@ -69,7 +70,8 @@ namespace {
 
 constexpr int kBuf = 2;       // steps per warp: one in use, one on the way
 constexpr int kCentre = 8;    // steps between two centrings of the sums
-constexpr int kTable = 512;                 // table entries of a segment
+constexpr int kTable = 512;   // table entries of a segment
+constexpr int kSms = 152;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -115,7 +117,6 @@ struct Int4Path {
   static constexpr int kCodeBytes = 16 * D / 2;        // K or V codes of a block
   static constexpr int kPairBytes = 16 * kGroups * 4;  // their (s, z) pairs
   static constexpr int kStageBytes = 2 * (kCodeBytes + kPairBytes);
-  static constexpr int kS = kWarps * kStages;
   static_assert(kStageBytes % 128 == 0, "stages stay aligned for 16-byte copies");
 
   static constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // code pairs of a word
@@ -526,6 +527,7 @@ struct Int4Path {
   // Thread `tid` of the first 32 kParts merges 8 outputs of one head, d ... d + 3
   // and d + 32 ... d + 35: their unnormalised sum, the reference M and the weight
   // L (0 without tokens).
+  template <int W>
   __device__ __forceinline__ static void merge8(const uint8_t* rings, int tid, float (&o)[8],
                                                 float& M, float& L, int& head, int& d) {
     const int part = tid >> 5, lane = tid & 31;
@@ -533,16 +535,16 @@ struct Int4Path {
     d = 64 * (part >> 1) + 4 * (lane >> 2);
     M = -INFINITY;
     L = 0.f;
-    const float* of[kWarps];  // a warp's state
+    const float* of[W];  // a warp's state
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       of[w] = reinterpret_cast<const float*>(rings + w * kRingBytes + kMergeAt);
       if (of[w][kParts * 256 + 8 + head] > 0.f) M = fmaxf(M, of[w][kParts * 256 + head]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float l = of[w][kParts * 256 + 8 + head];
       const float f = l > 0.f ? exp2f(of[w][kParts * 256 + head] - M) : 0.f;
       L = fmaf(f, l, L);
@@ -717,28 +719,30 @@ __device__ __forceinline__ void next_segment(const Int4DecodeParams& p, Walk& wa
   walk.flags = walk.left == 0 ? kLater : flags;
 }
 
-template <class Path>
+template <class Path, int W>
 constexpr size_t int4_smem() {
-  return static_cast<size_t>(Path::kS) * Path::kStageBytes + kWarps * Path::kQueryBytes +
+  return static_cast<size_t>(W) * (Path::kRingBytes + Path::kQueryBytes) +
          2 * kTable * sizeof(int32_t);
 }
 
 // part_blocks > 0: grid (partitions, units, requests), one run per CTA.
 // part_blocks == 0: balanced, grid units * pieces.
-template <class Path>
-__global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(const Int4DecodeParams p) {
+// W: warps, 4 or (short runs, see launch_int4) 1.
+template <class Path, int W>
+__global__ void __launch_bounds__(W * 32, Path::kCtas * (kWarps / W))
+    decode_int4_kernel(const Int4DecodeParams p) {
   constexpr int D = Path::kD, H = Path::kHeads;
   constexpr int kCB = Path::kCodeBytes, kPB = Path::kPairBytes, kSB = Path::kStageBytes;
   constexpr int kPieces = kCB / 16;  // 16-byte pieces of a block's K (or V) codes
   extern __shared__ __align__(128) uint8_t smem[];
-  uint4* qs = reinterpret_cast<uint4*>(smem + Path::kS * kSB);
-  int32_t* tables = reinterpret_cast<int32_t*>(qs + kWarps * (Path::kQueryBytes / 16));
+  uint4* qs = reinterpret_cast<uint4*>(smem + W * Path::kRingBytes);
+  int32_t* tables = reinterpret_cast<int32_t*>(qs + W * (Path::kQueryBytes / 16));
   qs += threadIdx.x / 32 * (Path::kQueryBytes / 16);
   __shared__ Walk walk;
   __shared__ Segment segs[4];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const bool balanced = p.part_blocks == 0;
+  const bool balanced = W == kWarps && p.part_blocks == 0;
   const int units = p.num_kv_heads * p.qgroups;
   const int unit = balanced ? blockIdx.x % units : blockIdx.y;
   const int kvh = unit / p.qgroups;
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
   const uint8_t* vc = static_cast<const uint8_t*>(p.v_pool) + lane * 16;
   const uint8_t* pairs = static_cast<const uint8_t*>(is_v ? p.v_sz : p.k_sz) +
                          (lane - (is_v ? kPairPieces : 0)) * 16;
-  constexpr int kStep = Path::kStep, kStride = kStep * kWarps, kStepBytes = kStep * kSB;
+  constexpr int kStep = Path::kStep, kStride = kStep * W, kStepBytes = kStep * kSB;
 
   // A segment's slice of the block table comes on chip during the segment
   // before ("踩坑一"), entry by entry; each thread checks those it fetched.
@@ -841,11 +845,11 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
     const Segment& seg = segs[s & 3];
     const int nb = seg.nb;
     const int32_t* tbl = tables + (s & 1) * kTable;
-    auto issue_step = [&](int i, int at) {  // table entries i, i + 4 to byte `at` of the ring
+    auto issue_step = [&](int i, int at) {  // table entries i, i + W ... to byte `at` of the ring
 #pragma unroll
       for (int b = 0; b < kStep; ++b) {
-        if (i + b * kWarps < nb) {
-          const uint32_t tile = static_cast<uint32_t>(tbl[i + b * kWarps]) * p.num_kv_heads + kvh;
+        if (i + b * W < nb) {
+          const uint32_t tile = static_cast<uint32_t>(tbl[i + b * W]) * p.num_kv_heads + kvh;
           const uint8_t* ks = kc + static_cast<uint64_t>(tile) * kCB;
           const uint8_t* vs = vc + static_cast<uint64_t>(tile) * kCB;
 #pragma unroll
@@ -874,10 +878,10 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
     // ---- ... while the run before is merged over the warps
     if (done_flags & kMerge) {
       const size_t row0 = static_cast<size_t>(done_b) * p.num_q_heads + head0;
-      if (threadIdx.x < 32 * Path::kParts) {
+      for (int t = threadIdx.x; t < 32 * Path::kParts; t += 32 * W) {
         float o[8], M, L;
         int hh, d;
-        Path::merge8(smem, threadIdx.x, o, M, L, hh, d);
+        Path::template merge8<W>(smem, t, o, M, L, hh, d);
         if (run_bad) L = -1.f;  // marks a failed run
         if (hh >= nheads) {
           // (a column without a query head)
@@ -923,9 +927,9 @@ __global__ void __launch_bounds__(kWarps * 32, Path::kCtas) decode_int4_kernel(c
         cp_async_wait<kBuf - 2>();
         __syncwarp();  // the step has landed; its predecessor's stages are read
         issue_step(i + (kBuf - 1) * kStride, next);
-        const int have = min(kStep, (nb - i + kWarps - 1) / kWarps);
+        const int have = min(kStep, (nb - i + W - 1) / W);
         int valid = kBlockSize * have;
-        if (i + (have - 1) * kWarps == nb - 1) valid += tail - kBlockSize;
+        if (i + (have - 1) * W == nb - 1) valid += tail - kBlockSize;
         const bool first = init && i == warp;
         if (valid == kBlockSize * kStep)
           Path::template consume<false>(st, qs, ring + at, valid, first, lane);
@@ -1090,15 +1094,30 @@ __global__ void __launch_bounds__(512) merge_long_kernel(const Int4DecodeParams 
       p, static_cast<size_t>(b) * p.num_q_heads + unit / p.qgroups * p.group + head + hh, lane);
 }
 
+template <class Path, int W>
+cudaError_t launch_warps(const Int4DecodeParams& p, dim3 grid, cudaStream_t s) {
+  constexpr size_t smem = int4_smem<Path, W>();
+  const cudaError_t e =
+      ensure_smem_attr(reinterpret_cast<const void*>(&decode_int4_kernel<Path, W>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_int4_kernel<Path, W>, grid, dim3(W * 32), smem, s, p);
+}
+
 template <class Path>
 cudaError_t launch_int4(const Int4DecodeParams& p, int grid_x, cudaStream_t s) {
-  constexpr size_t smem = int4_smem<Path>();
-  const cudaError_t e =
-      ensure_smem_attr(reinterpret_cast<const void*>(&decode_int4_kernel<Path>), smem);
-  if (e != cudaSuccess) return e;
-  const dim3 grid = p.part_blocks == 0 ? dim3(grid_x)
-                                       : dim3(grid_x, p.num_kv_heads * p.qgroups, p.batch);
-  return launch_pdl(decode_int4_kernel<Path>, grid, dim3(kWarps * 32), smem, s, p);
+  if (p.part_blocks == 0) return launch_warps<Path, kWarps>(p, dim3(grid_x), s);
+  // More runs than CTAs of four warps fit the GPU, all of them short: a warp for
+  // each, which keeps as many warps resident but four times the runs, and no warp
+  // waits for another.  One warp and four, head_dim 128, 1024 runs: of 1 block 6.3
+  // and 13.2 us, of 16 14.0 and 19.9, of 32 21.6 and 26.2; 2048 runs of 32 43.4
+  // and 43.6, of 64 73.7 and 66.5; 512 runs of 16 10.3 and 11.6, of 32 18.1 and
+  // 17.4; 256 runs (one wave) of 1 5.3 and 5.2, of 16 9.8 and 6.7.
+  constexpr int kOneWarpBlocks = 32;
+  const dim3 grid(grid_x, p.num_kv_heads * p.qgroups, p.batch);
+  const long long runs = static_cast<long long>(grid.x) * grid.y * grid.z;
+  return runs > kSms * Path::kCtas && p.part_blocks <= kOneWarpBlocks
+             ? launch_warps<Path, 1>(p, grid, s)
+             : launch_warps<Path, kWarps>(p, grid, s);
 }
 
 }  // namespace

@@ -601,3 +601,27 @@ def test_decode_int4_contexts_cut_by_themselves(Hq, kv, lens):
         assert torch.count_nonzero(bad[i]) == 0
         others = [j for j in range(len(lens)) if j != i]
         assert torch.equal(bad[others], out[others])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,kv,B,most,pb", [(64, 32, 20, 500, 0), (8, 1, 650, 40, 0),
+                                             (33, 11, 60, 200, 5), (40, 1, 130, 17, 1)])
+def test_decode_int4_many_short_runs(dtype, D, Hq, kv, B, most, pb):
+    """More runs than CTAs of four warps fit the GPU: a warp for each."""
+    lens = [1 + (i * i * 7 + 3 * i) % most for i in range(B)]
+    lens[1], lens[B // 2], lens[-1] = 0, most, 16
+    c = Case(lens, Hq, kv, D, dtype, seed=71)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = c.run(pb, status)
+    assert kvp.kvp_read_status(status) == kvp.KVP_OK
+    c.check(out)
+    assert torch.count_nonzero(out[1]) == 0
+    assert torch.equal(out, c.run(pb))
+    c.tables[B // 2, 0] = c.kc.shape[0]
+    c.lens[5] = 16 * c.tables.shape[1] + 1
+    bad = c.run(pb, status)
+    assert kvp.kvp_read_status(status) == kvp.KVP_ERR_BAD_BLOCK
+    assert torch.count_nonzero(bad[B // 2]) == 0 and torch.count_nonzero(bad[5]) == 0
+    rest = [i for i in range(B) if i not in (5, B // 2)]
+    assert torch.equal(bad[rest], out[rest])
