@@ -32,6 +32,8 @@
 // 140 us: 139 with 9, 142 with 10, spilling) nor the next rows' loads ahead of the
 // arithmetic (138 at 6 CTAs, 150 at 8) change that, nor one check over all of a
 // lane's elements (157: exact ties are common).  A step of 64 tokens takes 2.9 us.
+#include <algorithm>
+
 #include "kvp_device.cuh"
 #include "kvp_serve.h"
 
@@ -344,41 +346,70 @@ __device__ __forceinline__ void load_angles(const RowParams& p, const int (&pos)
   }
 }
 
-// One CTA: kRowThreads / L row slots (L = D / 16 lanes each), row_lanes of them
-// on one token.  A slot takes the token's units r, r + step, ...: query rows
-// first, then (K, V) row pairs of the kv heads; gridDim.y CTAs share a token's
-// units.
+// One CTA: kRowThreads / L row slots (L = D / 16 lanes each), row_lanes = 2^row_shift
+// of them on one token.  A slot takes the token's units r, r + step, ...:
+// query rows first, then (K, V) row pairs of the kv heads; gridDim.y CTAs share a
+// token's units.
 template <bool kBf16, int D, bool kRope, bool kInt4>
 __global__ void __launch_bounds__(kRowThreads, kRope ? 6 : 8) row_kernel(const RowParams p) {
   constexpr int L = D / 16;
   constexpr int kSlots = kRowThreads / L;
-  constexpr int kWarpRows = 32 / L;  // row slots of a warp, all on one token (row_lanes >= 8)
+  constexpr int kWarpRows = 32 / L;  // row slots of a warp
   dev::grid_dependency_wait();
   dev::launch_dependents();
   const int c = threadIdx.x % L;
   const int rs = threadIdx.x / L;
+  const int row_lanes = 1 << p.row_shift;
   const long long t =
-      static_cast<long long>(blockIdx.x) * (kSlots / p.row_lanes) + rs / p.row_lanes;
-  if (t >= p.num_tokens) return;
-  const int slot = p.slots[t];
-  if (slot < 0) return;  // padding token
-  const int unit0 = blockIdx.y * p.row_lanes + rs % p.row_lanes;
-  const int step = gridDim.y * p.row_lanes;
+      static_cast<long long>(blockIdx.x) * (kSlots >> p.row_shift) + (rs >> p.row_shift);
+  const bool there = t < p.num_tokens;
+  const long long tt = there ? t : 0;
+  const int unit0 = blockIdx.y * row_lanes + (rs & (row_lanes - 1));
+  const int step = gridDim.y * row_lanes;
   const int nq = kRope ? p.num_q_heads : 0;
-
   const LaneChunks k = lane_chunks<D, kRope>(p, c);
+
+  // The slot, the positions and the first rows set out together (the rows of a
+  // padding token for nothing): 8191 tokens of 64 + 8 heads 54.6 -> 53.4 us, a step
+  // of 64 tokens 3.0 -> 2.7.  Not where the quantiser follows: there the rows it
+  // holds back spill (140 -> 154 us).
+  constexpr bool kAhead = !kInt4;
+  constexpr int U = kRope ? 4 : 2;  // rows in flight per lane
+  const uint16_t* q = p.q + tt * p.q_stride;
+  const uint16_t* kr = p.key + tt * p.k_stride;
+  const uint16_t* vr = p.value + tt * p.v_stride;
+  RowPair x[U];  // query rows, or a K and a V row
+  auto load_queries = [&](int r) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r + u * step < nq) x[u] = load_pair(q + (r + u * step) * D, k.a, k.b);
+  };
+  if (kAhead && unit0 < nq) {
+    load_queries(unit0);
+  } else if (kAhead) {
+    const int h = min(unit0 - nq, p.num_kv_heads - 1);
+    x[0] = load_pair(kr + h * D, k.a, k.b);
+    x[1] = load_pair(vr + h * D, k.a, k.b);
+  }
+  int pos[4] = {0, 0, 0, 0};
+  if constexpr (kRope) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      if (a < p.num_axes) pos[a] = p.positions[static_cast<size_t>(a) * p.num_tokens + tt];
+  }
+  // (a warp can hold several tokens and shares its lanes' sums: it goes on while
+  // one of them is live)
+  const int slot = there ? p.slots[tt] : -1;
+  bool live = slot >= 0;  // not a padding token
+  if (!__any_sync(0xffffffffu, live)) return;
+
   bool bad = slot >= p.num_slots;
   float cs[8], sn[8];
   if constexpr (kRope) {
-    int pos[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      if (a < p.num_axes) {
-        pos[a] = p.positions[static_cast<size_t>(a) * p.num_tokens + t];
-        bad |= pos[a] < 0 || pos[a] >= p.max_position;
-      }
-    }
-    if (!bad) {
+    for (int a = 0; a < 4; ++a)
+      if (live && a < p.num_axes) bad |= pos[a] < 0 || pos[a] >= p.max_position;
+    if (live && !bad) {
       if (k.rot_a) load_angles(p, pos, p.interleaved ? 4 * k.a : 8 * c, cs, sn);
       if (k.rot_b) load_angles(p, pos, p.interleaved ? 4 * k.b : 8 * c + 4, cs + 4, sn + 4);
     }
@@ -391,19 +422,16 @@ __global__ void __launch_bounds__(kRowThreads, kRope ? 6 : 8) row_kernel(const R
       for (int r = unit0; r < nq; r += step)
         store_pair(p.q_out + t * p.q_out_stride + r * D, k.a, k.b, zero);
     }
-    return;
+    live = false;
   }
 
   int r = unit0;
+  // this lane's slot among those of its token in the warp
+  const int lead = rs & (min(row_lanes, kWarpRows) - 1);
   if constexpr (kRope) {
-    constexpr int U = 4;  // rows in flight per lane
-    const uint16_t* q = p.q + t * p.q_stride;
-    uint16_t* qo = p.q_out + t * p.q_out_stride;
-    for (; r < nq; r += U * step) {
-      RowPair x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (r + u * step < nq) x[u] = load_pair(q + (r + u * step) * D, k.a, k.b);
+    uint16_t* qo = p.q_out + tt * p.q_out_stride;
+    while (live && r < nq) {
+      if (!kAhead) load_queries(r);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (r + u * step < nq) {
@@ -411,31 +439,35 @@ __global__ void __launch_bounds__(kRowThreads, kRope ? 6 : 8) row_kernel(const R
           store_pair(qo + (r + u * step) * D, k.a, k.b, x[u]);
         }
       }
+      r += U * step;
+      if (kAhead) load_queries(r);
     }
-    // back to the first unit at which one of the warp's slots is past the query rows
-    const int last = unit0 + kWarpRows - 1 - (threadIdx.x & 31) / L;
+    // back to the first unit at which one of the token's slots in this warp is past
+    // the query rows
+    const int last = unit0 - lead + min(row_lanes, kWarpRows) - 1;
     r = last >= nq ? unit0 : unit0 + (nq - last + step - 1) / step * step;
   }
-  // K and V rows.  A warp's row slots lie on one token, so all its lanes come
-  // here together; the loop runs until the warp's first slot is done.
-  const uint16_t* kr = p.key + t * p.k_stride;
-  const uint16_t* vr = p.value + t * p.v_stride;
-  const int lead = (threadIdx.x & 31) / L;  // this lane's slot in the warp
+  // K and V rows.  All lanes of the warp come here together; the loop runs until
+  // the first slots are done.  (Lanes without a row redo one.)
   for (; r - lead < nq + p.num_kv_heads; r += step) {
     const int h = r - nq;
-    const bool live = h >= 0 && h < p.num_kv_heads;
-    const int hc = min(max(h, 0), p.num_kv_heads - 1);  // (lanes without a row redo one)
-    RowPair x = load_pair(kr + hc * D, k.a, k.b);
-    const RowPair y = load_pair(vr + hc * D, k.a, k.b);
-    if constexpr (kRope) rotate<kBf16>(x, k, p.interleaved != 0, cs, sn);
+    const bool store = live && h >= 0 && h < p.num_kv_heads;
+    RowPair kx, vx;
+    if (kAhead) kx = x[0], vx = x[1];
+    if (!kAhead || r != unit0) {
+      const int hc = min(max(h, 0), p.num_kv_heads - 1);
+      kx = load_pair(kr + hc * D, k.a, k.b);
+      vx = load_pair(vr + hc * D, k.a, k.b);
+    }
+    if constexpr (kRope) rotate<kBf16>(kx, k, p.interleaved != 0, cs, sn);
     const size_t srow =
         (static_cast<size_t>(slot / kBlockSize) * p.num_kv_heads + h) * kBlockSize +
         slot % kBlockSize;
     if constexpr (kInt4) {
-      store_rows_int4<kBf16, D>(x, y, k, c, live, p, srow);
-    } else if (live) {
-      store_pair(static_cast<uint16_t*>(p.k_cache) + srow * D, k.a, k.b, x);
-      store_pair(static_cast<uint16_t*>(p.v_cache) + srow * D, k.a, k.b, y);
+      store_rows_int4<kBf16, D>(kx, vx, k, c, store, p, srow);
+    } else if (store) {
+      store_pair(static_cast<uint16_t*>(p.k_cache) + srow * D, k.a, k.b, kx);
+      store_pair(static_cast<uint16_t*>(p.v_cache) + srow * D, k.a, k.b, vx);
     }
   }
 }
@@ -460,31 +492,36 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sz) {
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// A warp per token and 512 / D heads: lane (head, c) of L = D / 16 lanes per head
-// writes the 16-byte chunks c and c + L of K and of V, so that a store covers
-// whole sectors (32 bytes a lane in a row instead: 128 us where this takes 110).
+// A warp per 512 / D rows: of one token and as many heads, or, with fewer heads,
+// `heads` (a power of two) of each of several tokens.  L = D / 16 lanes share a
+// row; lane c writes the 16-byte chunks c and c + L of K and of V, so that a store
+// covers whole sectors (32 bytes a lane in a row instead: 128 us where this takes
+// 110).
 template <bool kBf16, int D>
 __global__ void __launch_bounds__(128) read_int4_kernel(
     uint4* __restrict__ key, uint4* __restrict__ value, const uint8_t* __restrict__ kc,
     const uint8_t* __restrict__ vc, const uint32_t* __restrict__ ksz,
     const uint32_t* __restrict__ vsz, const int32_t* __restrict__ slots, int num_tokens,
-    int num_kv_heads, int num_slots, int32_t* status) {
-  constexpr int L = D / 16, kHeads = 32 / L;
+    int num_kv_heads, int heads, int num_slots, int32_t* status) {
+  constexpr int L = D / 16, kRows = 32 / L;
   dev::grid_dependency_wait();
   dev::launch_dependents();
   const int lane = threadIdx.x & 31, c = lane % L;
-  const long long t = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int row = lane / L, h = blockIdx.y * heads + (row & (heads - 1));
+  const int shift = 31 - __clz(heads);
+  const long long t = (static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5)) *
+                          (kRows >> shift) +
+                      (row >> shift);
   if (t >= num_tokens) return;
   const int slot = slots[t];
   if (slot < 0) return;  // padding token: the rows are left as they are
   const bool bad = slot >= num_slots;
-  if (bad && blockIdx.y == 0 && lane == 0) dev::set_status(status, kErrBadBlock);
+  if (bad && h == 0 && c == 0) dev::set_status(status, kErrBadBlock);
   const size_t row0 =
       bad ? 0
           : static_cast<size_t>(slot / kBlockSize) * num_kv_heads * kBlockSize + slot % kBlockSize;
   uint4* ko = key + t * num_kv_heads * (D / 8) + c;
   uint4* vo = value + t * num_kv_heads * (D / 8) + c;
-  const int h = blockIdx.y * kHeads + lane / L;
   if (h < num_kv_heads) {
     uint4 k2[2], v2[2];
     if (bad) {
@@ -523,11 +560,15 @@ cudaError_t launch_rows(RowParams p, cudaStream_t s) {
   // step lies where four CTAs per SM have work: rotation of 64 + 8 heads of 128
   // into 4 bits, 128 tokens 6.5 and 5.0 us, 256 tokens 6.5 and 6.8, 4096 tokens 31
   // and 59; 16 + 8 heads of 64, 512 tokens 5.2 and 4.7, 1024 tokens 5.3 and 6.9.
+  // Never more slots than the token has units (@ROW).
   const bool many = p.num_tokens * units >= 152 * 4 * kSlots;
-  p.row_lanes = many ? 8 : kSlots;
-  const long long per_cta = kSlots / p.row_lanes;
+  p.row_shift = 0;
+  const long long most = many ? std::min<long long>(8, kRope ? (units + 3) / 4 : units) : kSlots;
+  while (1 << p.row_shift < std::min(units, most)) ++p.row_shift;
+  const int row_lanes = 1 << p.row_shift;
+  const long long per_cta = kSlots / row_lanes;
   const dim3 grid(static_cast<unsigned>((p.num_tokens + per_cta - 1) / per_cta),
-                  many ? 1u : static_cast<unsigned>((units + kSlots - 1) / kSlots));
+                  many ? 1u : static_cast<unsigned>((units + row_lanes - 1) / row_lanes));
   return launch_pdl(row_kernel<kBf16, D, kRope, kInt4>, grid, dim3(kRowThreads), 0, s, p);
 }
 
@@ -558,15 +599,19 @@ cudaError_t launch_read_int4(void* key, void* value, bool bf16, const uint8_t* k
                              const int32_t* slots, int num_tokens, const kvp_cache_desc& c,
                              int32_t* status, cudaStream_t s) {
   if (num_tokens == 0) return cudaSuccess;
-  const int groups = (c.num_kv_heads * (c.head_dim / 16) + 31) / 32;  // of heads, a warp each
-  const dim3 grid(static_cast<unsigned>((num_tokens - 1) / 4 + 1), static_cast<unsigned>(groups));
+  const int rows = 512 / c.head_dim;  // of a warp
+  int heads = 1;
+  while (heads < c.num_kv_heads && heads < rows) heads *= 2;
+  const int tokens = 4 * (rows / heads);  // of a CTA
+  const dim3 grid(static_cast<unsigned>((num_tokens - 1) / tokens + 1),
+                  static_cast<unsigned>((c.num_kv_heads + heads - 1) / heads));
   const int nslots = c.num_blocks * kBlockSize;
 #define KVP_READ_CASE(BF, DD)                                                                   \
   if (bf16 == BF && c.head_dim == DD)                                                           \
     return launch_pdl(read_int4_kernel<BF, DD>, grid, dim3(128), 0, s, static_cast<uint4*>(key), \
                       static_cast<uint4*>(value), kc, vc, static_cast<const uint32_t*>(ksz),    \
                       static_cast<const uint32_t*>(vsz), slots, num_tokens, c.num_kv_heads,     \
-                      nslots, status);
+                      heads, nslots, status);
   KVP_READ_CASE(false, 64)
   KVP_READ_CASE(false, 128)
   KVP_READ_CASE(true, 64)

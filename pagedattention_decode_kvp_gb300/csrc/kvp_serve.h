@@ -69,7 +69,8 @@ struct RowParams {
   int32_t axis_end[3];          // first pair past axis 0, 1, 2
   int32_t interleaved;          // pairs (2i, 2i + 1), else (i, i + R / 2)
   int32_t sections_by_4;        // every section is a multiple of 4 pairs
-  int32_t row_lanes;            // rows of one token a CTA works on at a time (set at launch)
+  int32_t row_shift;            // log2 of the rows of one token a CTA works on at a time (set
+                                // at launch)
 };
 
 // Requests one table call handles (its offsets live in shared memory), and slots
