@@ -555,16 +555,24 @@ template <bool kBf16, int D, bool kRope, bool kInt4>
 cudaError_t launch_rows(RowParams p, cudaStream_t s) {
   constexpr int kSlots = kRowThreads / (D / 16);
   const long long units = (kRope ? p.num_q_heads : 0) + p.num_kv_heads;
-  // Many tokens: 8 slots per token, so a lane uses its angles for several
-  // heads.  Few: all of a CTA's slots on one token, and CTAs side by side.  The
-  // step lies where four CTAs per SM have work: rotation of 64 + 8 heads of 128
-  // into 4 bits, 128 tokens 6.5 and 5.0 us, 256 tokens 6.5 and 6.8, 4096 tokens 31
-  // and 59; 16 + 8 heads of 64, 512 tokens 5.2 and 4.7, 1024 tokens 5.3 and 6.9.
-  // Never more slots than the token has units (@ROW).
+  // Few tokens: all of a CTA's slots on one token, and CTAs side by side.  The step
+  // lies where four CTAs per SM have work: rotation of 64 + 8 heads of 128 into 4
+  // bits, 128 tokens 6.5 and 5.0 us (many, few), 256 tokens 6.5 and 6.8, 4096
+  // tokens 31 and 59; 16 + 8 heads of 64, 512 tokens 5.2 and 4.7, 1024 tokens 5.3
+  // and 6.9.
+  // Many: up to 8 slots per token.  A rotating slot takes 9 of the token's units,
+  // for it reads the token's angles, as many bytes as a row, and has 4 rows in
+  // flight: 29843 tokens of 7 + 1 heads with 1 slot 27 us, with 2 30, with 8 65;
+  // but with less than a CTA per SM slots go before (1024 tokens of 16 + 8 heads, 4
+  // slots 7.0 us, 8 slots 5.2).
   const bool many = p.num_tokens * units >= 152 * 4 * kSlots;
+  const long long most = std::min<long long>(units, many ? 8 : kSlots);
+  const long long want = many && kRope ? std::min((units + 8) / 9, most) : most;
   p.row_shift = 0;
-  const long long most = many ? std::min<long long>(8, kRope ? (units + 3) / 4 : units) : kSlots;
-  while (1 << p.row_shift < std::min(units, most)) ++p.row_shift;
+  const long long tokens = p.num_tokens;
+  while (1 << p.row_shift < want ||
+         (1 << p.row_shift < most && tokens << p.row_shift < 152 * kSlots))
+    ++p.row_shift;
   const int row_lanes = 1 << p.row_shift;
   const long long per_cta = kSlots / row_lanes;
   const dim3 grid(static_cast<unsigned>((p.num_tokens + per_cta - 1) / per_cta),

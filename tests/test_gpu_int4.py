@@ -72,7 +72,8 @@ def special_rows(T, kv, D, dtype, seed):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("T,kv", [(1, 1), (5, 3), (37, 2), (300, 8), (1111, 5)])
+@pytest.mark.parametrize("T,kv", [(1, 1), (5, 3), (37, 2), (300, 8), (1111, 5), (11003, 1),
+                                  (7001, 2), (4003, 3)])
 def test_append_and_read_int4_bit_exact(dtype, D, T, kv):
     NB = -(-T // 16) + 3
     key, value = special_rows(T, kv, D, dtype, 11), special_rows(T, kv, D, dtype, 12).flip(0)

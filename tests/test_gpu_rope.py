@@ -53,6 +53,13 @@ SHAPES = [  # T, Hq, kv, D, R, sections, gap
     (9, 0, 4, 128, 112, (56,), 0),
     (1500, 8, 2, 128, 128, (10, 18, 18, 18), 0),
     (2100, 16, 4, 64, 64, (8, 12, 12), 24),
+    # several tokens to a warp, and units that no power of two divides
+    (9001, 1, 1, 128, 128, (16, 24, 24), 0),
+    (7001, 1, 1, 64, 48, (8, 16), 8),
+    (5003, 7, 1, 128, 64, (7, 0, 25), 16),
+    (4001, 8, 2, 64, 32, (16,), 8),
+    (2502, 5, 5, 128, 112, (56,), 0),
+    (12007, 0, 1, 64, 64, (32,), 0),
 ]
 
 
