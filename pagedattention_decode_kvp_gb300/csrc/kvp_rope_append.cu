@@ -24,14 +24,14 @@
 // row; a lane holds two 16-byte chunks, chosen so that both elements of every
 // split-half pair are its own, and uses its 8 (cos, sin) pairs for every head
 // of the token it works on.  Measured, prompts of 33098 tokens, 32 kv heads of
-// 128 (shares of the measured copy bandwidth): rotation with a 16-bit append 242
-// us (0.96 to 1.0), 4-bit append 138 us (0.72), read-back 110 us (0.90);
+// 128 (shares of the measured copy bandwidth): rotation with a 16-bit append 237
+// us (0.98 to 1.02), 4-bit append 137 us (0.72), read-back 110 us (0.90);
 // rotation with a 4-bit append, 8191 tokens of 64 + 8 heads, 56 us (0.79).  The
 // quantiser is what holds the 4-bit appends: 403 instructions for four K and four
 // V rows fill 67% of the issue slots, and neither more CTAs per SM (with the 8 at
 // 140 us: 139 with 9, 142 with 10, spilling) nor the next rows' loads ahead of the
 // arithmetic (138 at 6 CTAs, 150 at 8) change that, nor one check over all of a
-// lane's elements (157: exact ties are common).  A step of 64 tokens takes 2.9 us.
+// lane's elements (157: exact ties are common).  A step of 64 tokens takes 2.8 us.
 #include <algorithm>
 
 #include "kvp_device.cuh"
@@ -563,15 +563,15 @@ cudaError_t launch_rows(RowParams p, cudaStream_t s) {
   // Many: up to 8 slots per token.  A rotating slot takes 9 of the token's units,
   // for it reads the token's angles, as many bytes as a row, and has 4 rows in
   // flight: 29843 tokens of 7 + 1 heads with 1 slot 27 us, with 2 30, with 8 65;
-  // but with less than a CTA per SM slots go before (1024 tokens of 16 + 8 heads, 4
-  // slots 7.0 us, 8 slots 5.2).
+  // but with less than 1.5 CTAs per SM slots go before (1024 tokens of 16 + 8
+  // heads, 4 slots 7.0 us, 8 slots 5.2).
   const bool many = p.num_tokens * units >= 152 * 4 * kSlots;
   const long long most = std::min<long long>(units, many ? 8 : kSlots);
   const long long want = many && kRope ? std::min((units + 8) / 9, most) : most;
   p.row_shift = 0;
   const long long tokens = p.num_tokens;
   while (1 << p.row_shift < want ||
-         (1 << p.row_shift < most && tokens << p.row_shift < 152 * kSlots))
+         (1 << p.row_shift < most && tokens << p.row_shift < 152 * 3 / 2 * kSlots))
     ++p.row_shift;
   const int row_lanes = 1 << p.row_shift;
   const long long per_cta = kSlots / row_lanes;
