@@ -596,19 +596,19 @@ __device__ __forceinline__ int blocks_of(const Int4DecodeParams& p, int n) {
 }
 
 // Exclusive prefix sum over the CTA's threads; the whole in *total.
-__device__ __forceinline__ long long prefix_sum(long long mine, long long* total) {
-  __shared__ long long part[kWarps];
+template <class T>
+__device__ __forceinline__ T prefix_sum(T mine, T* total) {
+  __shared__ T part[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long sum = mine;
+  T sum = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+    const T x = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += x;
   }
-  __syncthreads();  // an earlier call's parts are read
   if (lane == 31) part[warp] = sum;
   __syncthreads();
-  long long at = sum - mine;
+  T at = sum - mine;
   *total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -632,8 +632,9 @@ __device__ __forceinline__ bool find_piece(const Int4DecodeParams& p, int index,
     const int size = static_cast<int>(cut.size);
     int runs = 0;
     for (int b = b0; b < b1; ++b) runs += (blocks_of(p, p.context_lens[b]) + size - 1) / size;
-    long long first = prefix_sum(runs, &total);
-    if (index >= total) return false;
+    int all;
+    int first = prefix_sum(runs, &all);
+    if (index >= all) return false;
     if (first <= index && index < first + runs) {
       int b = b0, n;
       while (index >= first + (n = (blocks_of(p, p.context_lens[b]) + size - 1) / size)) {
@@ -643,7 +644,7 @@ __device__ __forceinline__ bool find_piece(const Int4DecodeParams& p, int index,
       walk.b = b;
       walk.n = p.context_lens[b];
       walk.nblk = blocks_of(p, walk.n);
-      walk.blk0 = static_cast<int>(index - first) * size;
+      walk.blk0 = (index - first) * size;
       walk.pos = 0;  // (so that the context's pieces are counted from this one)
       walk.end = min(size, walk.nblk - walk.blk0);
       walk.size = size;
