@@ -764,8 +764,8 @@ def kvp_rope_append_int4(q_out, q, key, value, k_cache, v_cache, k_scale_zero, v
     _check(lib.kvp_rope_append_int4(*rows, k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale_zero.data_ptr(), v_scale_zero.data_ptr(),
                                     cos_sin.data_ptr(), P, positions.data_ptr(),
-                                    slot_mapping.data_ptr(), T, Hq, rope, d, code, _status_ptr(status),
-                                    s), "kvp_rope_append_int4")
+                                    slot_mapping.data_ptr(), T, Hq, rope, d, code,
+                                    _status_ptr(status), s), "kvp_rope_append_int4")
 
 
 # ------------------------------------------------------------------ device-side tables

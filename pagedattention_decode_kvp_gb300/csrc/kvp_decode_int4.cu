@@ -276,7 +276,8 @@ struct Int4Path {
     float acc[kStep][kGroups][4];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      uint32_t wa[kStep][2], wb[kStep][2];  // of tokens g8 and g8 + 8: elements 64 g + 32 w + 8 t4 ...
+      // of tokens g8 and g8 + 8: elements 64 g + 32 w + 8 t4 ...
+      uint32_t wa[kStep][2], wb[kStep][2];
 #pragma unroll
       for (int b = 0; b < kStep; ++b) {
         dev::ldsm_x4(dev::smem_addr(tile + b * kStageBytes) + matrix_at(g, lane), wa[b][0], wb[b][0],
@@ -1112,8 +1113,9 @@ cudaError_t launch_int4(const Int4DecodeParams& p, int grid_x, cudaStream_t s) {
   // waits for another.  One warp and four, head_dim 128, 1024 runs: of 1 block 6.3
   // and 13.2 us, of 16 14.0 and 19.9, of 32 21.6 and 26.2; 2048 runs of 32 43.4
   // and 43.6, of 64 73.7 and 66.5; 512 runs of 16 10.3 and 11.6, of 32 18.1 and
-  // 17.4; 256 runs (one wave) of 1 5.3 and 5.2, of 16 9.8 and 6.7.
-  constexpr int kOneWarpBlocks = 32;
+  // 17.4; 256 runs (one wave) of 1 5.3 and 5.2, of 16 9.8 and 6.7.  head_dim 64,
+  // runs of 64 blocks: 1024 25.2 and 24.6, 2048 38.6 and 44.2, 4096 64.7 and 81.1.
+  constexpr int kOneWarpBlocks = Path::kD == 64 ? 64 : 32;
   const dim3 grid(grid_x, p.num_kv_heads * p.qgroups, p.batch);
   const long long runs = static_cast<long long>(grid.x) * grid.y * grid.z;
   return runs > kSms * Path::kCtas && p.part_blocks <= kOneWarpBlocks
