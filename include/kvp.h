@@ -350,7 +350,8 @@ kvp_status kvp_copy_blocks_int4(uint8_t* k_cache, uint8_t* v_cache, void* k_scal
  * float32 accumulation; q, out and the pairs are of `dtype`, scales not negative
  * (as the appends write them), elements of q below 2^115 in size.  out must not
  * overlap q.  A weight softmax_i * scale is rounded to fp16 before its product
- * with the codes.  Workspace from kvp_decode_workspace_bytes with kv_8bit = 4;
+ * with the codes; V may be of any size, but bf16 values below 2^-112 lose
+ * precision.  Workspace from kvp_decode_workspace_bytes with kv_8bit = 4;
  * pools need 16-byte alignment only.  Table entries behind a context may be read,
  * but nothing depends on them.  KVP_DECODE_MERGE_RUNS is accepted and changes
  * nothing (blocks are fetched one by one).  Arguments otherwise as

@@ -38,6 +38,11 @@
 //     lies in [8, 16) and moved only when an a passes 4096, so a block costs
 //     neither a maximum over its tokens nor a rescale.  Weights 2^-28 of the
 //     largest are the smallest that count, as for any fp16 weight.
+//   * That ties r to the size of V, which the sums of P and P z bear only so far:
+//     fp16 scales (of the weights that count) from 2^-21 to 2^28, bf16 from 2^-23 to
+//     2^18.  A run that meets other values goes on in a loop of its own (any_size),
+//     whose r follows the scores alone and whose a has a factor for each group: V of
+//     any size, 57 contexts of 9200 tokens 115 us instead of 103.
 //   * A product with ones gives sum_t a_t of the rounded weights; subtracting
 //     7.5 times it centres the codes, so that the rounding of a is weighted by
 //     c - 7.5 and not by c.  (The ones are 1.0: with the subnormal 2^-24 in
@@ -160,10 +165,24 @@ struct Int4Path {
     }
   }
 
+  // A lane's sum of P stays below this, so that no sum of P z over lanes, warps and
+  // pieces passes the largest value: bf16 zeros have float32's range, for fp16 ones
+  // there is room.
+  static constexpr float kMostWeight = kBf16 ? 0x1p-14f : 0x1p60f;
+  // P is that small with bf16 pairs because s comes 2^48 times larger.
+  static constexpr int kLiftBy = 48;
+  static constexpr float kLift = kBf16 ? static_cast<float>(1ll << kLiftBy) : 1.f;
+
   // The query operand of the K product lives in shared memory, a copy per warp:
   // for each group and pair of k-steps 4 words per lane.  (In registers it took
   // the step loop over the 168 that three CTAs leave.)
   static constexpr int kQueryBytes = kGroups * 2 * 32 * 16;
+  // ... and behind it the factors E of the warp's sums (see any_size), one for each
+  // group and head.
+  static constexpr int kWarpBytes = kQueryBytes + kGroups * 8 * 4;
+  __device__ __forceinline__ static float* factors(uint4* qs, int g, int i, int lane) {
+    return reinterpret_cast<float*>(qs + kQueryBytes / 16) + 8 * g + 2 * (lane & 3) + i;
+  }
 
   __device__ __forceinline__ static void init(State& st, const Query& x, float scale_log2,
                                               uint4* qs, int lane) {
@@ -235,7 +254,10 @@ struct Int4Path {
     }
   }
 
-  // (s, z) pairs of one token, one per group.
+  // (s, z) pairs of one token, one per group.  kLifted: s kLift, by an addition to the
+  // exponent in the instruction that widens a bf16 (0 becomes 2^(48 - 127), and s from
+  // 2^(128 - 48) on an infinity, a NaN or negative: too_large and reference see those).
+  template <bool kLifted>
   __device__ __forceinline__ static void load_pairs(const uint8_t* base, int tok,
                                                     float (&s)[kGroups], float (&z)[kGroups]) {
     uint32_t w[kGroups];
@@ -249,7 +271,7 @@ struct Int4Path {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float2 x = dev::unpack2<kBf16>(w[g]);
-      s[g] = x.x;
+      s[g] = kLifted && kBf16 ? __uint_as_float(w[g] * 65536u + (uint32_t{kLiftBy} << 23)) : x.x;
       z[g] = x.y;
     }
   }
@@ -265,7 +287,7 @@ struct Int4Path {
   // this lane's rows g8, g8 + 8 and heads 2 t4, 2 t4 + 1, and V's pairs of those
   // tokens.  kTail: only the first `valid` tokens count (other slots may hold
   // anything).
-  template <bool kTail>
+  template <bool kTail, bool kLifted>
   __device__ __forceinline__ static void scores(const State& st, const uint4* qs,
                                                 const uint8_t* tile, int valid, int lane,
                                                 float (&v)[kStep][4], float (&s0)[kStep][kGroups],
@@ -299,8 +321,8 @@ struct Int4Path {
     for (int b = 0; b < kStep; ++b) {
       const uint8_t* pairs = tile + b * kStageBytes + 2 * kCodeBytes;
       float ks0[kGroups], kz0[kGroups], ks1[kGroups], kz1[kGroups];
-      load_pairs(pairs, tok0, ks0, kz0);
-      load_pairs(pairs, tok1, ks1, kz1);
+      load_pairs<false>(pairs, tok0, ks0, kz0);
+      load_pairs<false>(pairs, tok1, ks1, kz1);
       float us[4] = {0.f, 0.f, 0.f, 0.f};
       v[b][0] = v[b][2] = -st.r[0];
       v[b][1] = v[b][3] = -st.r[1];
@@ -315,12 +337,21 @@ struct Int4Path {
         v[b][2] = fmaf(kz1[g], st.qz[g][0], v[b][2]);
         v[b][3] = fmaf(kz1[g], st.qz[g][1], v[b][3]);
       }
-      v[b][0] = fmaf(us[0], st.f[0], v[b][0]);
-      v[b][1] = fmaf(us[1], st.f[1], v[b][1]);
-      v[b][2] = fmaf(us[2], st.f[0], v[b][2]);
-      v[b][3] = fmaf(us[3], st.f[1], v[b][3]);
-      load_pairs(pairs + kPairBytes, tok0, s0[b], z0[b]);
-      load_pairs(pairs + kPairBytes, tok1, s1[b], z1[b]);
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        if constexpr (D == 64) {  // (as add_weights)
+          const float2 x = dev::f2unpack(dev::ffma2(dev::f2pack(us[i], us[i + 1]),
+                                                    dev::f2pack(st.f[0], st.f[1]),
+                                                    dev::f2pack(v[b][i], v[b][i + 1])));
+          v[b][i] = x.x;
+          v[b][i + 1] = x.y;
+        } else {
+          v[b][i] = fmaf(us[i], st.f[0], v[b][i]);
+          v[b][i + 1] = fmaf(us[i + 1], st.f[1], v[b][i + 1]);
+        }
+      }
+      load_pairs<kLifted>(pairs + kPairBytes, tok0, s0[b], z0[b]);
+      load_pairs<kLifted>(pairs + kPairBytes, tok1, s1[b], z1[b]);
       if constexpr (kTail) {
         const bool in0 = tok0 < valid - 16 * b, in1 = tok1 < valid - 16 * b;
         v[b][0] = in0 ? v[b][0] : -INFINITY;
@@ -338,14 +369,65 @@ struct Int4Path {
     }
   }
 
+  // Sums of P, a block further.  D = 64 adds two heads at a time, and takes the last
+  // product of their scores so: 32 x 32 heads of 4096 72.3 -> 70.3 us (D = 128 gains
+  // nothing, 112.4 and 112.3).
+  __device__ __forceinline__ static void add_weights(float& l0, float& l1, const float (&pr)[4]) {
+    if constexpr (D == 64) {
+      const float2 l = dev::f2unpack(dev::fadd2(
+          dev::f2pack(l0, l1), dev::fadd2(dev::f2pack(pr[0], pr[1]), dev::f2pack(pr[2], pr[3]))));
+      l0 = l.x;
+      l1 = l.y;
+    } else {
+      l0 += pr[0] + pr[2];
+      l1 += pr[1] + pr[3];
+    }
+  }
+
+  // A step's sums with z (mid: 7.5, for the s that were loaded).
+  __device__ __forceinline__ static void add_zeros(State& st, const float (&pr)[kStep][4],
+                                                   const float (&s0)[kStep][kGroups],
+                                                   const float (&z0)[kStep][kGroups],
+                                                   const float (&s1)[kStep][kGroups],
+                                                   const float (&z1)[kStep][kGroups], float mid) {
+#pragma unroll
+    for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float c0 = fmaf(mid, s0[b][g], z0[b][g]), c1 = fmaf(mid, s1[b][g], z1[b][g]);
+        st.zo[g][0] = fmaf(pr[b][0], c0, fmaf(pr[b][2], c1, st.zo[g][0]));
+        st.zo[g][1] = fmaf(pr[b][1], c0, fmaf(pr[b][3], c1, st.zo[g][1]));
+      }
+    }
+  }
+
+  // Whether an a is above 4096 (0x6c00) or an infinity; in bf16 or negative or NaN
+  // (see load_pairs), by a comparison of integers.
+  __device__ __forceinline__ static bool too_large(const uint32_t (&ap)[kStep][kGroups][2]) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if constexpr (kBf16)
+          top = __vimax3_u16x2(top, ap[b][g][0], ap[b][g][1]);
+        else
+          top = max_half2(top, max_half2(ap[b][g][0], ap[b][g][1]));
+      }
+    }
+    const uint32_t above = (top & 0x7fff7fffu) + 0x13ff13ffu;
+    return ((kBf16 ? above | top : above) & 0x80008000u) != 0u;
+  }
+
   // A step's blocks, kStageBytes apart (each: K codes, V codes, K pairs, V pairs).
   // kTail: only the first `valid` of their tokens count.  first: the warp's first
-  // step, which sets the reference.
+  // step, which sets the reference.  False (for the whole warp) where the sizes of the
+  // values are not for this path: then the step has not been taken.
   template <bool kTail>
-  __device__ __forceinline__ static void consume(State& st, const uint4* qs, const uint8_t* tile,
+  __device__ __forceinline__ static bool consume(State& st, const uint4* qs, const uint8_t* tile,
                                                  int valid, bool first, int lane) {
     float v[kStep][4], s0[kStep][kGroups], z0[kStep][kGroups], s1[kStep][kGroups], z1[kStep][kGroups];
-    scores<kTail>(st, qs, tile, valid, lane, v, s0, z0, s1, z1);
+    scores<kTail, true>(st, qs, tile, valid, lane, v, s0, z0, s1, z1);
 
     // ---- weights
     float pr[kStep][4], l0, l1;
@@ -357,8 +439,7 @@ struct Int4Path {
       for (int b = 0; b < kStep; ++b) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) pr[b][i] = dev::ex2_approx(v[b][i]);
-        l0 += pr[b][0] + pr[b][2];
-        l1 += pr[b][1] + pr[b][3];
+        add_weights(l0, l1, pr[b]);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           ap[b][g][0] = dev::pack2<false>(pr[b][0] * s0[b][g], pr[b][1] * s0[b][g]);
@@ -367,33 +448,22 @@ struct Int4Path {
       }
     };
     weights();
-    uint32_t top = 0u;
-#pragma unroll
-    for (int b = 0; b < kStep; ++b) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) top = max_half2(top, max_half2(ap[b][g][0], ap[b][g][1]));
-    }
-    // an a above 4096 (0x6c00 in either half; a is never negative), or a sum of
-    // weights that nears the float range (2^110: weights of rows without scale)
-    const bool move =
-        ((top + 0x13ff13ffu) & 0x80008000u) != 0u || fmaxf(l0, l1) > 1.2980742e33f;
+    const bool move = too_large(ap) || !(fmaxf(l0, l1) <= kMostWeight);
     if (__any_sync(0xffffffffu, move || first)) {
-      reference(st, v, s0, s1, first);
+      if (!reference(st, v, s0, s1, first)) return false;
       weights();
     }
     st.l[0] = l0;
     st.l[1] = l1;
-#pragma unroll
-    for (int b = 0; b < kStep; ++b) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float c0 = fmaf(7.5f, s0[b][g], z0[b][g]), c1 = fmaf(7.5f, s1[b][g], z1[b][g]);
-        st.zo[g][0] = fmaf(pr[b][0], c0, fmaf(pr[b][2], c1, st.zo[g][0]));
-        st.zo[g][1] = fmaf(pr[b][1], c0, fmaf(pr[b][3], c1, st.zo[g][1]));
-      }
-    }
+    add_zeros(st, pr, s0, z0, s1, z1, 7.5f / kLift);
+    add_values(st, ap, tile, lane);
+    return true;
+  }
 
-    // ---- values: the blocks' products, straight into the sums
+  // The blocks' products of a and V's codes, straight into the sums.
+  __device__ __forceinline__ static void add_values(State& st,
+                                                    const uint32_t (&ap)[kStep][kGroups][2],
+                                                    const uint8_t* tile, int lane) {
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
@@ -435,41 +505,78 @@ struct Int4Path {
     }
   }
 
-  // Rare: move the reference so that the step's largest a lies in [8, 16),
-  // never down.  v is relative to the old one on entry, to the new one on exit.
-  __device__ __forceinline__ static void reference(State& st, float (&v)[kStep][4],
+  // Exponent of x >= 0 (-127 for 0 and below the normal range).
+  __device__ __forceinline__ static int exponent(float x) {
+    return static_cast<int>(__float_as_uint(x) >> 23) - 127;
+  }
+  // 2^x, 0 below the normal range.
+  __device__ __forceinline__ static float pow2(int x) {
+    return x < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(x + 127) << 23);
+  }
+  // Largest x over the warp's rows, for this lane's head.
+  __device__ __forceinline__ static float over_rows(float x) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  }
+  // Largest score, rounded up, and largest P s of each group for that reference; v
+  // becomes the scores themselves.
+  __device__ __forceinline__ static float sizes(const State& st, float (&v)[kStep][4],
+                                                const float (&s0)[kStep][kGroups],
+                                                const float (&s1)[kStep][kGroups], int i,
+                                                float (&big)[kGroups]) {
+    float mx = -1e30f;
+#pragma unroll
+    for (int b = 0; b < kStep; ++b) {
+      v[b][i] += st.r[i];
+      v[b][i + 2] += st.r[i];
+      mx = fmaxf(mx, fmaxf(v[b][i], v[b][i + 2]));
+    }
+    mx = ceilf(over_rows(mx));
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      big[g] = 0.f;
+#pragma unroll
+      for (int b = 0; b < kStep; ++b)
+        big[g] = fmaxf(big[g], fmaxf(dev::ex2_approx(v[b][i] - mx) * s0[b][g],
+                                     dev::ex2_approx(v[b][i + 2] - mx) * s1[b][g]));
+      big[g] = over_rows(big[g]);
+    }
+    return mx;
+  }
+
+  // Rare: move the reference so that the step's largest a lies in [8, 16), never
+  // down.  v is relative to the old one on entry, to the new one on exit.  False, and
+  // nothing has changed, where the values are outside the sizes above.
+  __device__ __forceinline__ static bool reference(State& st, float (&v)[kStep][4],
                                                    const float (&s0)[kStep][kGroups],
                                                    const float (&s1)[kStep][kGroups], bool first) {
+    float now[2];
+    bool fits = true;
+#pragma unroll
+    for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) fits = fits && s0[b][g] >= 0.f && s1[b][g] >= 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float mx = -INFINITY, big = 0.f;
+      float big[kGroups];
+      const float mx = sizes(st, v, s0, s1, i, big);
+      const float top = kGroups == 2 ? fmaxf(big[0], big[1]) : big[0];
+      fits = fits && top >= (kBf16 ? 0x1p25f : 0x1p-21f) && top < (kBf16 ? 0x1p66f : 0x1p28f) &&
+             st.l[i] <= 0.25f * kMostWeight;
+      now[i] = mx + static_cast<float>(exponent(top) - 3);
+      if (!first) now[i] = fmaxf(st.r[i], now[i]);
+    }
+    if (!__all_sync(0xffffffffu, fits)) return false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float al = first ? 0.f : dev::ex2_approx(st.r[i] - now[i]);
+      st.r[i] = now[i];
 #pragma unroll
       for (int b = 0; b < kStep; ++b) {
-        v[b][i] += st.r[i];
-        v[b][i + 2] += st.r[i];
-        mx = fmaxf(mx, fmaxf(v[b][i], v[b][i + 2]));
-      }
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-#pragma unroll
-      for (int b = 0; b < kStep; ++b) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-          big = fmaxf(big, fmaxf(dev::ex2_approx(v[b][i] - mx) * s0[b][g],
-                                 dev::ex2_approx(v[b][i + 2] - mx) * s1[b][g]));
-      }
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      // no weight yet (rows of one value): 2^60, until one exceeds it
-      const int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-      const float shift = big > 0.f ? static_cast<float>(max(e, -80) - 3) : -60.f;
-      const float now = first ? mx + shift : fmaxf(st.r[i], mx + shift);
-      const float al = first ? 0.f : dev::ex2_approx(st.r[i] - now);
-      st.r[i] = now;
-#pragma unroll
-      for (int b = 0; b < kStep; ++b) {
-        v[b][i] -= now;
-        v[b][i + 2] -= now;
+        v[b][i] -= now[i];
+        v[b][i + 2] -= now[i];
       }
       st.l[i] *= al;
 #pragma unroll
@@ -484,6 +591,92 @@ struct Int4Path {
         }
       }
     }
+    return true;
+  }
+
+  // A step of values of any size.  The reference follows the scores alone: P is 2^-20
+  // at most where it is set, and moves on when a lane's sum passes 2^-14.  a = P s E
+  // has a power of two E for each head and group that takes the step's largest a of
+  // that group into [8, 16).  Neither r nor 2^r / E, what an a of 1 stands for, ever
+  // goes down.  So sums of P lose only what float32 does, sums of P (z + 7.5 s) never
+  // pass the largest value, and what an a loses is small beside its own group.
+  // enter: the steps before were `consume`'s.
+  __device__ __forceinline__ static void any_size(State& st, uint4* qs, const uint8_t* tile,
+                                                  int valid, bool first, bool enter, int lane) {
+    float v[kStep][4], s0[kStep][kGroups], z0[kStep][kGroups], s1[kStep][kGroups], z1[kStep][kGroups];
+    scores<true, false>(st, qs, tile, valid, lane, v, s0, z0, s1, z1);
+    float pr[kStep][4], l0, l1;
+    uint32_t ap[kStep][kGroups][2];
+    auto weights = [&] {
+      l0 = st.l[0];
+      l1 = st.l[1];
+#pragma unroll
+      for (int b = 0; b < kStep; ++b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pr[b][i] = dev::ex2_approx(v[b][i]);
+        add_weights(l0, l1, pr[b]);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          const float e0 = *factors(qs, g, 0, lane), e1 = *factors(qs, g, 1, lane);
+          ap[b][g][0] = dev::pack2<false>(pr[b][0] * e0 * s0[b][g], pr[b][1] * e1 * s0[b][g]);
+          ap[b][g][1] = dev::pack2<false>(pr[b][2] * e0 * s1[b][g], pr[b][3] * e1 * s1[b][g]);
+        }
+      }
+    };
+    if (enter) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) *factors(qs, g, i, lane) = kLift;
+      }
+      __syncwarp();
+    }
+    weights();
+    const bool move = first || enter || too_large(ap) || fmaxf(l0, l1) > 0x1p-14f;
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float big[kGroups];
+        const float mx = sizes(st, v, s0, s1, i, big), sum = over_rows(st.l[i]);
+        float now = mx + 20.f;
+        if (!first) now = fmaxf(now, st.r[i] + static_cast<float>(max(exponent(sum) + 20, 0)));
+        const int up = first ? 0 : static_cast<int>(fminf(now - st.r[i], 400.f));
+        const int past = static_cast<int>(fminf(now - mx, 400.f));
+        const float al = pow2(-up);
+        st.r[i] = now;
+        st.l[i] *= al;
+#pragma unroll
+        for (int b = 0; b < kStep; ++b) {
+          v[b][i] -= now;
+          v[b][i + 2] -= now;
+        }
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          float* e = factors(qs, g, i, lane);
+          const int was = exponent(*e);
+          // (without a row with a scale: as large as it gets)
+          const int want = big[g] > 0.f ? min(126, 3 + past - exponent(big[g])) : 126;
+          const int to = max(-126, first ? want : min(want, was + up));
+          const float keep = first ? 0.f : pow2(to - was - up);
+          __syncwarp();  // the old factor is read
+          *e = pow2(to);
+          st.zo[g][i] *= al;
+          st.as[g][i] *= keep;
+          st.as[g][i + 2] *= keep;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            st.o[g][j][i] *= keep;
+            st.o[g][j][i + 2] *= keep;
+          }
+        }
+      }
+      __syncwarp();
+      weights();
+    }
+    st.l[0] = l0;
+    st.l[1] = l1;
+    add_zeros(st, pr, s0, z0, s1, z1, 7.5f);
+    add_values(st, ap, tile, lane);
   }
 
   // The warp's state for the merge: per (group, head parity i) and lane, outputs
@@ -495,7 +688,9 @@ struct Int4Path {
   static constexpr int kRingBytes = kStages * kStageBytes;
   static_assert((kParts * 256 + 16) * 4 <= kStep * kStageBytes, "the state fits a step's place");
 
-  __device__ __forceinline__ static void finalize(State& st, uint8_t* ring, int lane) {
+  // kFactors: the sums have them (see any_size).
+  template <bool kFactors>
+  __device__ __forceinline__ static void finalize(State& st, uint4* qs, uint8_t* ring, int lane) {
     const int g8 = lane >> 2, t4 = lane & 3;
     float* mine = reinterpret_cast<float*>(ring + kMergeAt);
     float* ml = mine + kParts * 256;
@@ -509,14 +704,20 @@ struct Int4Path {
         float z = st.zo[g][i];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        const float mid = 7.5f * st.as[g][i];
+        constexpr float kUnit = kFactors ? 1.f : 1.f / kLift;
+        const float mid = 7.5f * kUnit * st.as[g][i];
+        const float per = kFactors ? pow2(-exponent(*factors(qs, g, i, lane))) : 1.f;
+        auto value = [&](float o, float step) {  // o steps of a code
+          const float x = fmaf(o, step * kUnit, -mid);
+          return kFactors ? fmaf(x, per, z) : x + z;
+        };
         float4* at = reinterpret_cast<float4*>(mine + (2 * g + i) * 256) + lane;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          at[32 * h] = make_float4(fmaf(st.o[g][2 * h][i], 16777216.f, -mid) + z,
-                                   fmaf(st.o[g][2 * h][i + 2], 1048576.f, -mid) + z,
-                                   fmaf(st.o[g][2 * h + 1][i], 16777216.f, -mid) + z,
-                                   fmaf(st.o[g][2 * h + 1][i + 2], 1048576.f, -mid) + z);
+          at[32 * h] = make_float4(value(st.o[g][2 * h][i], 16777216.f),
+                                   value(st.o[g][2 * h][i + 2], 1048576.f),
+                                   value(st.o[g][2 * h + 1][i], 16777216.f),
+                                   value(st.o[g][2 * h + 1][i + 2], 1048576.f));
       }
       if (g8 == 0) {
         ml[2 * t4 + i] = st.r[i];
@@ -723,7 +924,7 @@ __device__ __forceinline__ void next_segment(const Int4DecodeParams& p, Walk& wa
 
 template <class Path, int W>
 constexpr size_t int4_smem() {
-  return static_cast<size_t>(W) * (Path::kRingBytes + Path::kQueryBytes) +
+  return static_cast<size_t>(W) * (Path::kRingBytes + Path::kWarpBytes) +
          2 * kTable * sizeof(int32_t);
 }
 
@@ -738,8 +939,8 @@ __global__ void __launch_bounds__(W * 32, Path::kCtas * (kWarps / W))
   constexpr int kPieces = kCB / 16;  // 16-byte pieces of a block's K (or V) codes
   extern __shared__ __align__(128) uint8_t smem[];
   uint4* qs = reinterpret_cast<uint4*>(smem + W * Path::kRingBytes);
-  int32_t* tables = reinterpret_cast<int32_t*>(qs + W * (Path::kQueryBytes / 16));
-  qs += threadIdx.x / 32 * (Path::kQueryBytes / 16);
+  int32_t* tables = reinterpret_cast<int32_t*>(qs + W * (Path::kWarpBytes / 16));
+  qs += threadIdx.x / 32 * (Path::kWarpBytes / 16);
   __shared__ Walk walk;
   __shared__ Segment segs[4];
   const int warp = threadIdx.x >> 5;
@@ -842,6 +1043,7 @@ __global__ void __launch_bounds__(W * 32, Path::kCtas * (kWarps / W))
   bool bad = __syncthreads_or(table_bad(0)) != 0;  // of this segment's table
   bool run_bad = false;                            // of the run
   typename Path::State st;
+  bool plain = true;                               // no any_size in this run (of this warp)
   int done_flags = 0, done_b = 0, done_runs = 0;   // of the segment before
   for (int s = 0;; ++s) {
     const Segment& seg = segs[s & 3];
@@ -917,29 +1119,54 @@ __global__ void __launch_bounds__(W * 32, Path::kCtas * (kWarps / W))
     }
     if (nb == 0) break;
     if (threadIdx.x == 0) next_segment(p, walk, segs[(s + 2) & 3], ahead);
-    if (seg.flags & kInit) Path::init(st, query, p.scale_log2, qs, lane);
+    if (seg.flags & kInit) {
+      Path::init(st, query, p.scale_log2, qs, lane);
+      plain = true;
+    }
 
     // ---- the segment's blocks
     run_bad |= bad;
     if (!bad) {
       const int tail = seg.tail;
       const bool init = (seg.flags & kInit) != 0;
-      int at = 0, next = (kBuf - 1) * kStepBytes;
-      for (int i = warp; i < nb; i += kStride) {
+      int i = warp, at = 0, next = (kBuf - 1) * kStepBytes;
+      auto fetch = [&] {
         cp_async_wait<kBuf - 2>();
         __syncwarp();  // the step has landed; its predecessor's stages are read
         issue_step(i + (kBuf - 1) * kStride, next);
+      };
+      auto tokens = [&] {
         const int have = min(kStep, (nb - i + W - 1) / W);
-        int valid = kBlockSize * have;
-        if (i + (have - 1) * W == nb - 1) valid += tail - kBlockSize;
-        const bool first = init && i == warp;
-        if (valid == kBlockSize * kStep)
-          Path::template consume<false>(st, qs, ring + at, valid, first, lane);
-        else
-          Path::template consume<true>(st, qs, ring + at, valid, first, lane);
+        return kBlockSize * have + (i + (have - 1) * W == nb - 1 ? tail - kBlockSize : 0);
+      };
+      auto advance = [&](bool first) {
         if (i / kStride % kCentre == 0) Path::centre(st, first ? kCentre / 2 : 1);
         at = at == (kBuf - 1) * kStepBytes ? 0 : at + kStepBytes;
         next = next == (kBuf - 1) * kStepBytes ? 0 : next + kStepBytes;
+        i += kStride;
+      };
+      bool leave = false;
+      if (plain) {
+        while (i < nb) {
+          fetch();
+          const int valid = tokens();
+          const bool first = init && i == warp;
+          leave = !(valid == kBlockSize * kStep
+                        ? Path::template consume<false>(st, qs, ring + at, valid, first, lane)
+                        : Path::template consume<true>(st, qs, ring + at, valid, first, lane));
+          if (leave) break;
+          advance(first);
+        }
+        plain = !leave;
+      }
+      if (!plain) {
+        while (i < nb) {
+          if (!leave) fetch();
+          const bool first = init && i == warp;
+          Path::any_size(st, qs, ring + at, tokens(), first, leave, lane);
+          leave = false;
+          advance(first);
+        }
       }
     } else if (threadIdx.x == 0) {
       dev::set_status(p.status, kErrBadBlock);
@@ -950,7 +1177,10 @@ __global__ void __launch_bounds__(W * 32, Path::kCtas * (kWarps / W))
     cp_async_wait<0>();
     if (done_flags & kMerge) {
       __syncwarp();  // the ring is read
-      Path::finalize(st, ring, lane);
+      if (plain)
+        Path::template finalize<false>(st, qs, ring, lane);
+      else
+        Path::template finalize<true>(st, qs, ring, lane);
     }
     bad = __syncthreads_or(table_bad(s + 1)) != 0;
   }

@@ -1,0 +1,84 @@
+"""4-bit decode over values of any size: rows of very different scales, and rows
+without a scale beside them."""
+import math
+
+import pytest
+import torch
+
+import plain64
+from test_gpu_int4 import DTYPES, Case, gen, randn
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = DTYPES
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from pagedattention_decode_kvp_gb300 import _build
+    import pagedattention_decode_kvp_gb300 as kvp
+    _build.build()
+    kvp.load_library()
+
+
+def widened(c, max_blocks):
+    """The same case with wider tables (the automatic split)."""
+    more = torch.full((c.tables.shape[0], max_blocks - c.tables.shape[1]), -1, dtype=torch.int32)
+    c.tables = torch.cat([c.tables, more], 1)
+    return c
+
+
+def check_all(c):
+    """One pass, given partitions, balanced pieces."""
+    ref, tol = plain64.decode4(c.q, c.kc, c.vc, c.ks, c.vs, c.tables, c.lens, c.scale)
+    for way, pb in (("one pass", 0), ("one block a partition", 1), ("partitions", 3),
+                    ("balanced", -1)):
+        if pb < 0:
+            widened(c, 70)
+        out = c.run(max(pb, 0))
+        assert torch.isfinite(out).all(), way
+        err = (out.cpu().double() - ref).abs()
+        worst = float((err / tol.clamp(min=1e-300)).max())
+        assert (err <= tol).all(), f"{way}: worst error is {worst:.3g} of the bound"
+
+
+def test_zero_rows_beside_one_large_row():
+    """Equal scores, 16 rows of zeros and one of +-1e30: a 17th of it."""
+    k, v = torch.zeros(17, 1, 64), torch.zeros(17, 1, 64)
+    v[16] = torch.linspace(-1e30, 1e30, 64)
+    c = Case([17], 2, 1, 64, BF16, k=[k], v=[v])
+    check_all(c)
+
+
+@pytest.mark.parametrize("dtype,size", [(F16, 13), (F16, -12)] +
+                         [(BF16, s) for s in (40, -40, 80, -80, 110, -110, 125)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [5, 16, 150])
+def test_rows_without_a_scale_beside_rows_of_any_size(dtype, size, D, at):
+    """Rows of one value (0, ordinary, or as large as the others) before and after
+    rows of size 2^size, in a block (at 5), across warps and across runs; scores
+    equal and not."""
+    n = 200
+    rows = (torch.randn(n, 1, D, generator=gen(1)).clamp(-2.9, 2.9) * 2.0 ** size).to(dtype)
+    flat = torch.randn(n, 1, 1, generator=gen(2)).expand(-1, -1, D)
+    early = (torch.arange(n) < at)[:, None, None]
+    v, k = [], []
+    for const in (torch.zeros_like(flat), flat, flat.clamp(-2.9, 2.9) * 2.0 ** size):
+        for first in (True, False):
+            v.append(torch.where(early == first, const.to(dtype), rows))
+            k.append(torch.zeros(n, 1, D) if first else randn((n, 1, D), dtype, 7))
+    c = Case([n] * 6, 3, 1, D, dtype, seed=5, k=k, v=v)
+    check_all(c)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [0, 100, 126])
+def test_large_rows_without_a_scale_under_rising_scores(D, size):
+    """Scores that climb by over 100 powers of two, values that only the zeros
+    carry."""
+    n = 300
+    direction = torch.sign(torch.randn(D, generator=gen(1)))
+    k = [(direction * torch.arange(n)[:, None, None] * f).to(BF16) for f in (0.5 / D, 2.0 / D)]
+    v = [(torch.randn(n, 1, 1, generator=gen(2)).clamp(-1.9, 1.9) * 2.0 ** size)
+         .expand(-1, -1, D).to(BF16)] * 2
+    q = (direction * math.sqrt(D)).expand(2, 2, D).to(BF16).contiguous()
+    check_all(Case([n] * 2, 2, 1, D, BF16, k=k, v=v, q=q))
