@@ -1,11 +1,12 @@
-"""4-bit decode over values of any size: rows of very different scales, and rows
-without a scale beside them."""
+"""4-bit decode over values of any size: rows and groups of very different scales,
+rows without a scale beside them."""
 import math
 
 import pytest
 import torch
 
 import plain64
+import rms64
 from test_gpu_int4 import DTYPES, Case, gen, randn
 
 pytestmark = pytest.mark.gpu
@@ -27,7 +28,7 @@ def widened(c, max_blocks):
     return c
 
 
-def check_all(c):
+def check_all(c, dtype, rms=False):
     """One pass, given partitions, balanced pieces."""
     ref, tol = plain64.decode4(c.q, c.kc, c.vc, c.ks, c.vs, c.tables, c.lens, c.scale)
     for way, pb in (("one pass", 0), ("one block a partition", 1), ("partitions", 3),
@@ -39,6 +40,9 @@ def check_all(c):
         err = (out.cpu().double() - ref).abs()
         worst = float((err / tol.clamp(min=1e-300)).max())
         assert (err <= tol).all(), f"{way}: worst error is {worst:.3g} of the bound"
+        for b in range(len(ref)) if rms else ():
+            e = rms64.relative(out[b], ref[b])
+            assert (e < rms64.limit(dtype, ref[b])).all(), (way, b, e)
 
 
 def test_zero_rows_beside_one_large_row():
@@ -46,7 +50,7 @@ def test_zero_rows_beside_one_large_row():
     k, v = torch.zeros(17, 1, 64), torch.zeros(17, 1, 64)
     v[16] = torch.linspace(-1e30, 1e30, 64)
     c = Case([17], 2, 1, 64, BF16, k=[k], v=[v])
-    check_all(c)
+    check_all(c, BF16)
 
 
 @pytest.mark.parametrize("dtype,size", [(F16, 13), (F16, -12)] +
@@ -67,7 +71,7 @@ def test_rows_without_a_scale_beside_rows_of_any_size(dtype, size, D, at):
             v.append(torch.where(early == first, const.to(dtype), rows))
             k.append(torch.zeros(n, 1, D) if first else randn((n, 1, D), dtype, 7))
     c = Case([n] * 6, 3, 1, D, dtype, seed=5, k=k, v=v)
-    check_all(c)
+    check_all(c, dtype)
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -81,4 +85,26 @@ def test_large_rows_without_a_scale_under_rising_scores(D, size):
     v = [(torch.randn(n, 1, 1, generator=gen(2)).clamp(-1.9, 1.9) * 2.0 ** size)
          .expand(-1, -1, D).to(BF16)] * 2
     q = (direction * math.sqrt(D)).expand(2, 2, D).to(BF16).contiguous()
-    check_all(Case([n] * 2, 2, 1, D, BF16, k=k, v=v, q=q))
+    check_all(Case([n] * 2, 2, 1, D, BF16, k=k, v=v, q=q), BF16)
+
+
+GROUPS = [(F16, 9, -9), (F16, 12, -12), (F16, -10, 12)] + \
+    [(BF16, a, b) for a, b in ((0, -18), (-20, 0), (12, -12), (-15, 15), (30, -30), (-50, 50),
+                               (110, -100))]
+
+
+@pytest.mark.parametrize("dtype,a,b", GROUPS)
+def test_two_groups_of_different_scale(dtype, a, b):
+    """head_dim 128: each group of 64 is as exact as if the other were not there,
+    at one ratio throughout or one that changes from token to token."""
+    n = 320
+    v = []
+    for grade in (lambda t: 1.0, lambda t: t / n, lambda t: 1 - t / n, lambda t: float(t % 2)):
+        f = torch.tensor([grade(t) for t in range(n)])[:, None, None, None]
+        x = torch.randn(n, 2, 2, 64, generator=gen(3)).clamp(-2.9, 2.9)
+        v.append((x * torch.exp2(f * torch.tensor([float(a), float(b)])[:, None]))
+                 .flatten(2).to(dtype))
+    c = Case([n] * 4, 8, 2, 128, dtype, seed=9, v=v)
+    check_all(c, dtype)
+    steady = Case([n], 8, 2, 128, dtype, seed=9, v=v[:1])
+    check_all(steady, dtype, rms=True)
