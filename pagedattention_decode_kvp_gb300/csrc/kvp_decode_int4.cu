@@ -138,10 +138,10 @@ struct Int4Path {
     float r[2], l[2];            // reference and sum of P (this lane's tokens)
   };
 
-  // Power of two that takes x > 0 into [2^k, 2^(k+1)), its exponent within +-100.
+  // Power of two that takes x > 0 into [2^k, 2^(k+1)), 2^126 at most.
   __device__ __forceinline__ static float pow2_to(float x, int k) {
     const int e = static_cast<int>(__float_as_uint(x) >> 23) - 127;
-    const int up = min(100, max(-100, k - e));
+    const int up = min(126, max(-126, k - e));
     return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
   }
 

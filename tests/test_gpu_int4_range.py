@@ -1,5 +1,5 @@
 """4-bit decode over values of any size: rows and groups of very different scales,
-rows without a scale beside them."""
+rows without a scale beside them, and queries up to the stated limits."""
 import math
 
 import pytest
@@ -108,3 +108,16 @@ def test_two_groups_of_different_scale(dtype, a, b):
     check_all(c, dtype)
     steady = Case([n], 8, 2, 128, dtype, seed=9, v=v[:1])
     check_all(steady, dtype, rms=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [118.99, 115.0, 111.5, 80.0, -115.0, -124.0])
+def test_queries_at_the_stated_limits(D, size):
+    """bf16 queries of almost 2^119 (times the scale of 2^-3 and 2^-3.5 below 2^116)
+    and down to 2^-126, with keys that keep the scores ordinary."""
+    n = 90
+    q = torch.rand(1, 6, D, generator=gen(4)) * 2.0 ** size
+    q[0, 3, 5] = 2.0 ** size
+    k = [(torch.randn(n, 2, D, generator=gen(5)).clamp(-2.9, 2.9) * 2.0 ** -size).to(BF16)]
+    c = Case([n], 6, 2, D, BF16, seed=14, k=k, q=q.to(BF16))
+    check_all(c, BF16)
