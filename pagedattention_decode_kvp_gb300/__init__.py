@@ -862,14 +862,14 @@ def kvp_selftest_wait_timeout(status, limit_ns, stream=None):
     """Run the library's bounded mbarrier wait on a barrier nothing arrives
     on, giving up after limit_ns: it records KVP_ERR_TIMEOUT in `status`."""
     _need_cuda(status)
-    _check(load_library().kvp_selftest_wait_timeout(_status_ptr(status), int(limit_ns),
+    _check(load_library().kvp_selftest_wait_timeout(_ptr(status), int(limit_ns),
                                                      _stream_ptr(stream)),
            "kvp_selftest_wait_timeout")
 
 
 def kvp_read_status(status, stream=None) -> int:
     """Synchronise the stream and return the device status word's kvp_status."""
-    return int(load_library().kvp_read_status(_status_ptr(status), _stream_ptr(stream)))
+    return int(load_library().kvp_read_status(_ptr(status), _stream_ptr(stream)))
 
 
 # ------------------------------------------------------------------ block manager
