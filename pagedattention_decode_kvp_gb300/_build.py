@@ -1,5 +1,5 @@
 """In-tree build of libkvp.so (nvcc, sm_103a only) and of _kvp_calls.so, the
-binding of its short calls (g++, against the installed torch).
+binding of its short calls (g++, against the installed torch, if there is one).
 
 Each translation unit is compiled in parallel to an object under ``_build/``
 and linked into ``_lib/``; an object is rebuilt when it is older than its source
@@ -55,8 +55,9 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _torch_dir() -> str:
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None else None
 
 
 def _headers_mtime() -> float:
@@ -93,33 +94,36 @@ def _link(path: str, objs: list[str], cmd: list[str], anew: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile (incrementally) and link libkvp.so and _kvp_calls.so; returns the
-    former's path."""
+    """Compile (incrementally) and link libkvp.so, which needs nvcc alone, and
+    _kvp_calls.so, where torch is installed; returns the former's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     hdr = _headers_mtime()
-    todo = []
-    objs = []
-    for src in [*SOURCES, CALLS_SOURCE]:
-        s = os.path.join(CSRC, src)
-        o = os.path.join(BUILD_DIR, src + ".o")
-        objs.append(o)
-        if force or ptxas_verbose or not os.path.exists(o) or \
-                os.path.getmtime(o) < max(os.path.getmtime(s), hdr):
-            todo.append(src)
-    logs = []
-    if todo:
-        with cf.ThreadPoolExecutor(max_workers=min(len(todo), os.cpu_count() or 4)) as ex:
-            for _, log in ex.map(lambda f: _compile(f, ptxas_verbose), todo):
-                logs.append(log)
-    calls = objs.pop()
+    torch_dir = _torch_dir()
+
+    def obj(src):
+        return os.path.join(BUILD_DIR, src + ".o")
+
+    def stale(src):
+        return force or ptxas_verbose or not os.path.exists(obj(src)) or \
+            os.path.getmtime(obj(src)) < max(os.path.getmtime(os.path.join(CSRC, src)), hdr)
+
+    todo = [src for src in ([CALLS_SOURCE] if torch_dir else []) + SOURCES if stale(src)]
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 4))) as ex:
+        jobs = {src: ex.submit(_compile, src, ptxas_verbose) for src in todo}
+    calls = jobs.pop(CALLS_SOURCE, None)
+    logs = [job.result()[1] for job in jobs.values()]
+    objs = [obj(src) for src in SOURCES]
     _link(LIB_PATH, objs, [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-ldl"],
-          force or any(s != CALLS_SOURCE for s in todo))
-    lib = os.path.join(_torch_dir(), "lib")
-    _link(CALLS_PATH, [calls], ["g++", "-shared", calls, f"-L{LIB_DIR}", "-lkvp", f"-L{lib}",
-                                "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-                                "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"],
-          force or CALLS_SOURCE in todo)
+          force or bool(jobs))
+    if calls is not None:
+        logs.append(calls.result()[1])
+    if torch_dir:
+        lib = os.path.join(torch_dir, "lib")
+        _link(CALLS_PATH, [obj(CALLS_SOURCE)],
+              ["g++", "-shared", obj(CALLS_SOURCE), f"-L{LIB_DIR}", "-lkvp", f"-L{lib}",
+               "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+               f"-Wl,-rpath,{lib}"], force or calls is not None)
     if verbose or ptxas_verbose:
         for log in logs:
             if log.strip():

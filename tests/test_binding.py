@@ -1,7 +1,11 @@
 """The Python binding and its build, without a GPU."""
+import os
+
+import pytest
 import torch
 
 import pagedattention_decode_kvp_gb300 as kvp
+from pagedattention_decode_kvp_gb300 import _build
 
 
 class Recorder:
@@ -36,3 +40,50 @@ def test_read_status_takes_any_tensor(monkeypatch):
     status = torch.zeros(1, dtype=torch.int64)
     kvp.kvp_selftest_wait_timeout(status, 100, Stream)
     assert lib.calls[-1] == ("kvp_selftest_wait_timeout", (status.data_ptr(), 100, 7))
+
+
+class Toolchain:
+    """The build in an empty directory, with compilers that only leave a file."""
+
+    def __init__(self, monkeypatch, tmp_path):
+        self.compiled, self.linked, self.broken = [], [], ()
+        for name, path in (("BUILD_DIR", "build"), ("LIB_DIR", "lib"), ("LIB_PATH", "lib/libkvp.so"),
+                           ("CALLS_PATH", "lib/_kvp_calls.so")):
+            monkeypatch.setattr(_build, name, str(tmp_path / path))
+        monkeypatch.setattr(_build.subprocess, "run", self.run)
+
+    def run(self, cmd, **kw):
+        out = cmd[cmd.index("-o") + 1]
+        (self.compiled if "-c" in cmd else self.linked).append(os.path.basename(out).split(".tmp")[0])
+        failed = any(os.path.basename(out).startswith(b) for b in self.broken)
+        if not failed:
+            open(out, "w").close()
+        return _build.subprocess.CompletedProcess(cmd, int(failed), "", "broken" * failed)
+
+
+@pytest.fixture
+def toolchain(monkeypatch, tmp_path):
+    return Toolchain(monkeypatch, tmp_path)
+
+
+def test_the_library_builds_without_torch(toolchain, monkeypatch):
+    """A C caller needs nvcc and nothing else."""
+    find = _build.importlib.util.find_spec
+    monkeypatch.setattr(_build.importlib.util, "find_spec",
+                        lambda name, *a: None if name == "torch" else find(name, *a))
+    assert _build.build() == _build.LIB_PATH and os.path.exists(_build.LIB_PATH)
+    assert toolchain.linked == ["libkvp.so"] and "kvp_calls.cpp.o" not in toolchain.compiled
+    assert len(toolchain.compiled) == len(_build.SOURCES)
+
+
+def test_the_library_builds_where_the_binding_does_not(toolchain):
+    toolchain.broken = ("kvp_calls",)
+    with pytest.raises(RuntimeError, match="kvp_calls.cpp"):
+        _build.build()
+    assert os.path.exists(_build.LIB_PATH) and not os.path.exists(_build.CALLS_PATH)
+    toolchain.broken = ()
+    assert _build.build() == _build.LIB_PATH and os.path.exists(_build.CALLS_PATH)
+    assert toolchain.linked == ["libkvp.so", "_kvp_calls.so"]
+    n = len(toolchain.compiled)
+    _build.build()  # and nothing is done twice
+    assert len(toolchain.compiled) == n and len(toolchain.linked) == 2
