@@ -450,6 +450,10 @@ def _calls():
     if not os.path.exists(path):
         raise RuntimeError(f"_kvp_calls.so is not built ({path}); run __graft_entry__.build() or "
                            "python -m pagedattention_decode_kvp_gb300._build")
+    from . import _build
+    if _build.calls_key_built() != _build.calls_key():
+        raise RuntimeError(f"{path} was built for another torch or Python; run "
+                           "__graft_entry__.build() or python -m pagedattention_decode_kvp_gb300._build")
     spec = importlib.util.spec_from_file_location("_kvp_calls", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

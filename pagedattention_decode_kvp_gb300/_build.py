@@ -3,7 +3,8 @@ binding of its short calls (g++, against the installed torch, if there is one).
 
 Each translation unit is compiled in parallel to an object under ``_build/``
 and linked into ``_lib/``; an object is rebuilt when it is older than its source
-or any header.  No cmake, no ninja.
+or any header, that of _kvp_calls.so also when torch or Python is another.  No
+cmake, no ninja.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libkvp.so")
 CALLS_PATH = os.path.join(LIB_DIR, "_kvp_calls.so")
+CALLS_KEY_PATH = os.path.join(LIB_DIR, "_kvp_calls.key")
 CALLS_SOURCE = "kvp_calls.cpp"
 
 SOURCES = [
@@ -58,6 +60,24 @@ def _nvcc() -> str:
 def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
     return os.path.dirname(spec.origin) if spec is not None else None
+
+
+def calls_key() -> str:
+    """What _kvp_calls.so is built for: it holds the layouts of one torch's C++ types
+    and one Python's."""
+    torch_dir, torch = _torch_dir(), ""
+    if torch_dir is not None:
+        with open(os.path.join(torch_dir, "version.py")) as f:
+            torch = f.read()
+    return f"{sysconfig.get_config_var('SOABI')}\n{torch_dir}\n{torch}"
+
+
+def calls_key_built() -> str | None:
+    """calls_key() of the _kvp_calls.so that is there."""
+    if not os.path.exists(CALLS_KEY_PATH):
+        return None
+    with open(CALLS_KEY_PATH) as f:
+        return f.read()
 
 
 def _headers_mtime() -> float:
@@ -108,7 +128,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return force or ptxas_verbose or not os.path.exists(obj(src)) or \
             os.path.getmtime(obj(src)) < max(os.path.getmtime(os.path.join(CSRC, src)), hdr)
 
-    todo = [src for src in ([CALLS_SOURCE] if torch_dir else []) + SOURCES if stale(src)]
+    key = calls_key()
+    todo = [src for src in SOURCES if stale(src)]
+    if torch_dir and (stale(CALLS_SOURCE) or calls_key_built() != key):
+        todo.insert(0, CALLS_SOURCE)
+        if os.path.exists(CALLS_KEY_PATH):
+            os.remove(CALLS_KEY_PATH)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(todo), os.cpu_count() or 4))) as ex:
         jobs = {src: ex.submit(_compile, src, ptxas_verbose) for src in todo}
     calls = jobs.pop(CALLS_SOURCE, None)
@@ -124,6 +149,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
               ["g++", "-shared", obj(CALLS_SOURCE), f"-L{LIB_DIR}", "-lkvp", f"-L{lib}",
                "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
                f"-Wl,-rpath,{lib}"], force or calls is not None)
+        if calls_key_built() != key:
+            tmp = CALLS_KEY_PATH + f".tmp{os.getpid()}"
+            with open(tmp, "w") as f:
+                f.write(key)
+            os.replace(tmp, CALLS_KEY_PATH)
     if verbose or ptxas_verbose:
         for log in logs:
             if log.strip():

@@ -48,7 +48,8 @@ class Toolchain:
     def __init__(self, monkeypatch, tmp_path):
         self.compiled, self.linked, self.broken = [], [], ()
         for name, path in (("BUILD_DIR", "build"), ("LIB_DIR", "lib"), ("LIB_PATH", "lib/libkvp.so"),
-                           ("CALLS_PATH", "lib/_kvp_calls.so")):
+                           ("CALLS_PATH", "lib/_kvp_calls.so"),
+                           ("CALLS_KEY_PATH", "lib/_kvp_calls.key")):
             monkeypatch.setattr(_build, name, str(tmp_path / path))
         monkeypatch.setattr(_build.subprocess, "run", self.run)
 
@@ -87,3 +88,36 @@ def test_the_library_builds_where_the_binding_does_not(toolchain):
     n = len(toolchain.compiled)
     _build.build()  # and nothing is done twice
     assert len(toolchain.compiled) == n and len(toolchain.linked) == 2
+
+
+def test_the_binding_is_built_anew_for_another_torch_or_python(toolchain, monkeypatch):
+    _build.build()
+    toolchain.compiled.clear(), toolchain.linked.clear()
+    for change in (lambda: monkeypatch.setattr(_build.sysconfig, "get_config_var", lambda n: "other"),
+                   lambda: monkeypatch.setattr(_build, "_torch_dir", lambda: str(other))):
+        other = os.path.join(_build.BUILD_DIR, "torch")
+        os.makedirs(other, exist_ok=True)
+        open(os.path.join(other, "version.py"), "w").write("__version__ = '9'")
+        change()
+        assert _build.calls_key_built() != _build.calls_key()
+        _build.build()
+        assert _build.calls_key_built() == _build.calls_key()
+        _build.build()
+    assert toolchain.compiled == ["kvp_calls.cpp.o"] * 2
+    assert toolchain.linked == ["_kvp_calls.so"] * 2
+    # one that could not be built is not taken for the present one
+    open(os.path.join(other, "version.py"), "w").write("__version__ = '10'")
+    toolchain.broken = ("kvp_calls",)
+    with pytest.raises(RuntimeError):
+        _build.build()
+    assert _build.calls_key_built() is None
+
+
+def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
+    _build.build()
+    kvp._calls.cache_clear()
+    with monkeypatch.context() as m:
+        m.setattr(_build, "calls_key", lambda: "another")
+        with pytest.raises(RuntimeError, match="another torch or Python"):
+            kvp._calls()
+    assert kvp._calls() is not None
