@@ -510,11 +510,20 @@ def _need(t, name, dtype, shape):
         raise ValueError("tensors passed to the GPU entry points must be contiguous")
 
 
+def _int32(x, name):
+    """A count as the library takes it (ctypes would pass its low word on)."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise KvpError(KVP_ERR_UNSUPPORTED, f"{name} of {x}")
+    return x
+
+
 def _extents(t, name, dims):
     """Shape of a tensor of that many dimensions."""
     shape = t.shape
     if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(shape)}")
+    for n in shape:
+        _int32(n, name)
     return shape
 
 
@@ -527,6 +536,8 @@ def _desc(nb, hkv, bs, d) -> kvp_cache_desc:
 def _rope_desc(rotary_dim, sections, interleaved) -> kvp_rope_desc:
     if not 1 <= len(sections) <= 4:
         raise ValueError(f"1 to 4 axes are allowed, sections has {len(sections)}")
+    for n in sections:
+        _int32(n, "section")
     return kvp_rope_desc(rotary_dim, len(sections), (ctypes.c_int32 * 4)(*sections), interleaved)
 
 
@@ -537,6 +548,8 @@ def _int4_sizes(codes):
     if len(codes) != 4:
         raise ValueError("4-bit pools are [num_blocks, num_kv_heads, block_size, head_dim / 2]")
     nb, hkv, bs, half = codes
+    for n in (nb, hkv, bs, 2 * half):
+        _int32(n, "pool extent")
     return kvp_cache_desc(nb, hkv, bs, 2 * half), (nb, hkv, bs, half // 32, 2), hkv, 2 * half
 
 
@@ -663,8 +676,8 @@ def kvp_attention_decode_int4(out, q, k_cache, v_cache, k_scale_zero, v_scale_ze
     _check(lib.kvp_attention_decode_int4(
         out.data_ptr(), q.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale_zero.data_ptr(), v_scale_zero.data_ptr(), block_tables.data_ptr(), MB,
-        context_lens.data_ptr(), B, Hq, scale, d, partition_blocks, ws, ws_bytes, phases,
-        _status_ptr(status), s), "kvp_attention_decode_int4")
+        context_lens.data_ptr(), B, Hq, scale, d, _int32(partition_blocks, "partition_blocks"), ws,
+        ws_bytes, _int32(phases, "phases"), _status_ptr(status), s), "kvp_attention_decode_int4")
 
 
 # ------------------------------------------------------------------ rotary append

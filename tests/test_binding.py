@@ -14,6 +14,9 @@ class Recorder:
     def __init__(self):
         self.calls = []
 
+    def kvp_status_string(self, status):
+        return b"status"
+
     def __getattr__(self, name):
         def call(*args):
             self.calls.append((name, args))
@@ -121,3 +124,49 @@ def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
         with pytest.raises(RuntimeError, match="another torch or Python"):
             kvp._calls()
     assert kvp._calls() is not None
+
+
+def test_counts_past_32_bits_are_refused(monkeypatch):
+    """A count that the C interface's int32 cannot hold must not arrive there as its
+    low word: 2^32 + 5 slots would be listed as 5."""
+    lib = Recorder()
+    monkeypatch.setattr(kvp, "load_library", lambda: lib)
+    monkeypatch.setattr(kvp, "_on_one_device", lambda stream, *ts: 0)
+
+    def i32(*shape):
+        return torch.empty(shape, dtype=torch.int32, device="meta")
+
+    many, one, two = 2 ** 32 + 5, i32(1), i32(2)
+    tables = i32(2, 3)
+
+    def refused(f, *args, **kw):
+        with pytest.raises(kvp.KvpError) as e:
+            f(*args, stream=Stream, **kw)
+        assert e.value.status == kvp.KVP_ERR_UNSUPPORTED and lib.calls == []
+
+    refused(kvp.kvp_extend_tables, tables, two, two, i32(9), one, two, one, i32(many), i32(3))
+    refused(kvp.kvp_extend_tables, tables, two, two, i32(many), one, two, one, i32(4), i32(3))
+    refused(kvp.kvp_extend_tables, i32(2, many), two, two, i32(9), one, two, one, i32(4), i32(3))
+    refused(kvp.kvp_release_tables, i32(many, 1), i32(many), i32(many), i32(9), one, i32(many), one)
+    refused(kvp.kvp_release_tables, tables, two, two, i32(many), one, two, one)
+    f16 = dict(dtype=torch.float16, device="meta")
+    codes = torch.empty((many, 1, 16, 32), dtype=torch.uint8, device="meta")
+    pairs = torch.empty((many, 1, 16, 1, 2), **f16)
+    row = torch.empty((1, 1, 64), **f16)
+    refused(kvp.kvp_append_int4, row, row, codes, codes, pairs, pairs, one)
+    refused(kvp.kvp_attention_decode_int4, row, row, codes, codes, pairs, pairs, i32(1, 4), one, 1.0)
+    small, few = codes[:4], pairs[:4]
+    refused(kvp.kvp_copy_blocks_int4, small, small, few, few, i32(many, 2))
+    for parts in (2 ** 32, -2 ** 31 - 1):
+        refused(kvp.kvp_attention_decode_int4, row, row, small, small, few, few, i32(1, 4), one, 1.0,
+                partition_blocks=parts)
+    refused(kvp.kvp_attention_decode_int4, row, row, small, small, few, few, i32(1, 4), one, 1.0,
+            phases=2 ** 32 + 3)
+    pool = torch.empty((4, 1, 16, 64), **f16)
+    angles = torch.empty((many, 64), dtype=torch.float32, device="meta")
+    refused(kvp.kvp_rope_append, row, row, row, row, pool, pool, angles, one, one)
+    angles = torch.empty((9, 64), dtype=torch.float32, device="meta")
+    refused(kvp.kvp_rope_append, row, row, row, row, pool, pool, angles, i32(2, 1), one,
+            sections=(2 ** 32 + 16, 16))
+    refused(kvp.kvp_rope_append, row, row, row, row, torch.empty((many, 1, 16, 64), **f16), pool,
+            angles, one, one)
