@@ -349,9 +349,11 @@ kvp_status kvp_copy_blocks_int4(uint8_t* k_cache, uint8_t* v_cache, void* k_scal
  * K_i = code * scale + zero (V likewise), products with the codes in fp16 with
  * float32 accumulation; q, out and the pairs are of `dtype`, scales not negative
  * (as the appends write them), elements of q below 2^120 in size, and below 2^116
- * times `scale`.  out must not overlap q.  A weight softmax_i * scale is rounded to
+ * times `scale`; those more than 2^24 below the largest of their head are rounded to
+ * 2^-34 of it.  out must not overlap q.  A weight softmax_i * scale is rounded to
  * fp16 before its product with the codes; V may be of any size, but bf16 values
- * below 2^-112 lose precision.  Workspace from kvp_decode_workspace_bytes with
+ * below 2^-112 lose precision.  Where a softmax sum is no number (a NaN in q or in a
+ * context's K) the row is written as zeros, as by the other decodes.  Workspace from kvp_decode_workspace_bytes with
  * kv_8bit = 4; pools need 16-byte alignment only.  Table entries behind a context
  * may be read, but nothing depends on them.  KVP_DECODE_MERGE_RUNS is accepted and
  * changes nothing (blocks are fetched one by one).  Arguments otherwise as

@@ -1259,7 +1259,7 @@ __global__ void __launch_bounds__(256) merge_noted_kernel(const Int4DecodeParams
 
 // The same for few contexts with many runs each: a block per (query head of a
 // unit, unit, request) and 16 warps over the runs.  The request's place among
-// the pieces is found from the lengths again (pieces / 8 of them at most).
+// the pieces is found from the lengths again (pieces / 12 of them at most).
 template <int D, bool kBf16Out>
 __global__ void __launch_bounds__(512) merge_long_kernel(const Int4DecodeParams p, int pieces) {
   constexpr int E = D / 32, W = 16;
