@@ -16,11 +16,11 @@
 // A block is 2 (8 D + 32 D / 64) bytes = 2304 at D = 128, little over half of
 // an INT8 block, while a warp has the same 32 D codes to widen: unlike the 8-bit
 // decodes the kernel fills over half of the issue slots at HBM's pace, so
-// everything here saves instructions (257 a block).  Measured, D = 128: 57
-// contexts of 9200 tokens, 8 kv heads, 103 us (0.87 of the measured copy
-// bandwidth), 32 of 4096 with 32 kv heads 110 us (0.81), 64 of 512 to 8192 66 us
-// (0.67: a start of about 6 us, a refill of the ring at every run, the merge's
-// 3 us); its ring alone, without the arithmetic, takes 91 us of the 103.
+// everything here saves instructions (263 a block, a run's start and end among
+// them).  Measured, D = 128: 57 contexts of 9200 tokens, 8 kv heads, 103 us (0.87 of
+// the measured copy bandwidth), 32 of 4096 with 32 kv heads 111 us (0.80), 64 of 512
+// to 8192 67 us (0.65: a start of about 6 us, a refill of the ring at every run, the
+// merge's 3 us); its ring alone, without the arithmetic, takes 91 us of the 103.
 //   * A code left where it lies is already a number: the fp16 bit pattern
 //     0x000c is the subnormal c 2^-24 and 0x00c0 is 16 c 2^-24, both exact
 //     tensor-core operands.  So one AND turns two codes into an operand pair,
@@ -1347,6 +1347,7 @@ cudaError_t launch_int4(const Int4DecodeParams& p, int grid_x, cudaStream_t s) {
   // and 43.6, of 64 73.7 and 66.5; 512 runs of 16 10.3 and 11.6, of 32 18.1 and
   // 17.4; 256 runs (one wave) of 1 5.3 and 5.2, of 16 9.8 and 6.7.  head_dim 64,
   // runs of 64 blocks: 1024 25.2 and 24.6, 2048 38.6 and 44.2, 4096 64.7 and 81.1.
+  // (At its edge the rule costs up to 4%: 512 runs of 32, 1024 of 64.)
   constexpr int kOneWarpBlocks = Path::kD == 64 ? 64 : 32;
   const dim3 grid(grid_x, p.num_kv_heads * p.qgroups, p.batch);
   const long long runs = static_cast<long long>(grid.x) * grid.y * grid.z;

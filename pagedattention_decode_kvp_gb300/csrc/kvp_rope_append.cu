@@ -27,11 +27,13 @@
 // 128 (shares of the measured copy bandwidth): rotation with a 16-bit append 237
 // us (0.98 to 1.02), 4-bit append 137 us (0.72), read-back 110 us (0.90);
 // rotation with a 4-bit append, 8191 tokens of 64 + 8 heads, 56 us (0.79).  The
-// quantiser is what holds the 4-bit appends: 403 instructions for four K and four
-// V rows fill 67% of the issue slots, and neither more CTAs per SM (with the 8 at
-// 140 us: 139 with 9, 142 with 10, spilling) nor the next rows' loads ahead of the
-// arithmetic (138 at 6 CTAs, 150 at 8) change that, nor one check over all of a
-// lane's elements (157: exact ties are common).  A step of 64 tokens takes 2.8 us.
+// 4-bit appends are held by the quantiser, 395 instructions for four K and four V
+// rows, and by the wait for rows, of which none is on its way meanwhile: 44% of the
+// warps are resident, the issue slots 66% full, and global memory is the first
+// stall.  More CTAs per SM (with the 8 at 140 us: 139 with 9, 142 with 10, spilling)
+// or the next rows' loads in registers (138 at 6 CTAs, 150 at 8, spilling) do not
+// change that, nor does one check over all of a lane's elements (157: exact ties are
+// common).  A step of 64 tokens takes 2.8 to 3.1 us.
 #include <algorithm>
 
 #include "kvp_device.cuh"

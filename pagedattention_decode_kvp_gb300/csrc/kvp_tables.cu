@@ -16,10 +16,10 @@
 // checks and the writes also lets lengths and counts be updated in place.  Above
 // 16384 tokens the slots are written by a second launch that fills the GPU, from
 // the first one's outputs alone (tables, lengths and query offsets).
-// Measured, a release and an extend together: 64 requests of one token each 8.3
-// us, 1000 of them 13, 1024 requests with prompts, 524291 slots, 20 (37 with the
-// slots in the cluster's launch; 64 requests with 64003 slots 13.6 against 12.9,
-// and a second launch for 1000 slots costs 5); 16384 requests 131.
+// Measured, a release and an extend together: 64 requests of one token each 8.8 to
+// 9.7 us, 1000 of them 13, 1024 requests with prompts, 524291 slots, 20 (37 with the
+// slots in the cluster's launch; 64 requests with 64003 slots 13.6 against 12.9, and
+// a second launch for 1000 slots costs 5); 16384 requests 131.
 #include <cooperative_groups.h>
 
 #include "kvp_device.cuh"
