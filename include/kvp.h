@@ -352,7 +352,8 @@ kvp_status kvp_copy_blocks_int4(uint8_t* k_cache, uint8_t* v_cache, void* k_scal
  * times `scale`; those more than 2^24 below the largest of their head are rounded to
  * 2^-34 of it.  out must not overlap q.  A weight softmax_i * scale is rounded to
  * fp16 before its product with the codes; V may be of any size, but bf16 values
- * below 2^-112 lose precision.  Where a softmax sum is no number (a NaN in q or in a
+ * below 2^-112 lose precision, and a weight below 2^-64 of the largest may count as
+ * zero.  Where a softmax sum is no number (a NaN in q or in a
  * context's K) the row is written as zeros, as by the other decodes.  Workspace from kvp_decode_workspace_bytes with
  * kv_8bit = 4; pools need 16-byte alignment only.  Table entries behind a context
  * may be read, but nothing depends on them.  KVP_DECODE_MERGE_RUNS is accepted and

@@ -121,3 +121,41 @@ def test_queries_at_the_stated_limits(D, size):
     k = [(torch.randn(n, 2, D, generator=gen(5)).clamp(-2.9, 2.9) * 2.0 ** -size).to(BF16)]
     c = Case([n], 6, 2, D, BF16, seed=14, k=k, q=q.to(BF16))
     check_all(c, BF16)
+
+
+@pytest.mark.parametrize("dtype,size", [(F16, 12), (BF16, 30), (BF16, -90), (BF16, 110)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [100, 5000, 8700])
+def test_sizes_that_change_in_the_middle_of_a_long_run(dtype, size, D, at):
+    """From one token on, in a run of two slices of its block table, or for one block
+    alone; whole, in pieces of all contexts and in partitions."""
+    n = 9011
+    x = torch.randn(n, 1, D, generator=gen(1)).clamp(-2.9, 2.9)
+    t = torch.arange(n)[:, None, None]
+    big = torch.tensor(2.0 ** size)
+    v = [(x * torch.where(t >= at, big, torch.tensor(1.0))).to(dtype),
+         (x * torch.where((t >= at) & (t < at + 16), big, torch.tensor(1.0))).to(dtype)]
+    c = Case([n, n], 2, 1, D, dtype, seed=3, v=v)
+    ref, tol = plain64.decode4(c.q, c.kc, c.vc, c.ks, c.vs, c.tables, c.lens, c.scale)
+    for pb in (0, 1024, 100):
+        out = c.run(pb)
+        err = (out.cpu().double() - ref).abs()
+        assert (err <= tol).all(), (pb, float((err / tol.clamp(min=1e-300)).max()))
+
+
+@pytest.mark.parametrize("dtype,size", [(F16, 12), (BF16, 60), (BF16, -100)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_runs_of_any_size(dtype, size, D):
+    """A warp for each of many runs: ordinary, without a scale, large, and both."""
+    B = 700
+    lens, v = [1 + (7 * b * b) % 45 for b in range(B)], []
+    for b, n in enumerate(lens):
+        x = torch.randn(n, 1, D, generator=gen(b)).clamp(-2.9, 2.9)
+        if b % 4 == 1:
+            x = x[..., :1].expand(-1, -1, D)
+        if b % 4 >= 2:
+            x = x * torch.where((torch.arange(n) >= n // 2)[:, None, None] | (b % 4 == 2),
+                                2.0 ** size, 1.0)
+        v.append(x.to(dtype))
+    c = Case(lens, 1, 1, D, dtype, seed=8, v=v)
+    c.check(c.run())
