@@ -353,14 +353,15 @@ kvp_status kvp_copy_blocks_int4(uint8_t* k_cache, uint8_t* v_cache, void* k_scal
  * 2^-34 of it.  out must not overlap q.  A weight softmax_i * scale is rounded to
  * fp16 before its product with the codes; V may be of any size, but bf16 values
  * below 2^-112 lose precision, and a weight below 2^-64 of the largest may count as
- * zero.  Where a softmax sum is no number (a NaN in q or in a
- * context's K) the row is written as zeros, as by the other decodes.  Workspace from kvp_decode_workspace_bytes with
- * kv_8bit = 4; pools need 16-byte alignment only.  Table entries behind a context
- * may be read, but nothing depends on them.  KVP_DECODE_MERGE_RUNS is accepted and
- * changes nothing (blocks are fetched one by one).  The automatic split goes by the
- * width of the tables: where they are much wider than the present contexts (a
- * captured loop), partition_blocks = max_blocks_per_seq, up to 1024, takes one pass.
- * Arguments otherwise as kvp_attention_decode.
+ * zero.  Where a softmax sum is no number (a NaN in q or in a context's K) the row
+ * is written as zeros, as by the other decodes.  Workspace from
+ * kvp_decode_workspace_bytes with kv_8bit = 4; pools need 16-byte alignment only.
+ * Table entries behind a context may be read, but nothing depends on them.
+ * KVP_DECODE_MERGE_RUNS is accepted and changes nothing (blocks are fetched one by
+ * one).  The automatic split goes by the width of the tables: where they are much
+ * wider than the present contexts (a captured loop), partition_blocks =
+ * max_blocks_per_seq, up to 1024, takes one pass.  Arguments otherwise as
+ * kvp_attention_decode.
  */
 kvp_status kvp_attention_decode_int4(void* out, const void* q, kvp_dtype dtype,
                                      const uint8_t* k_cache, const uint8_t* v_cache,
