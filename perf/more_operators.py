@@ -163,7 +163,8 @@ def _codes(x, block):
     most = g.abs().amax((1, 3), keepdim=True)
     safe = most.clamp(min=2.0 ** -100)
     scales = torch.where(most > 0, safe / LARGEST, 1.0)
-    codes = (g * (LARGEST / safe)).to(F8).view(torch.uint8).view(nr * block, nd * GROUP)
+    # (LARGEST / safe would be LARGEST times a reciprocal: two roundings)
+    codes = (g * torch.full_like(safe, LARGEST).div(safe)).to(F8).view(torch.uint8).view(nr * block, nd * GROUP)
     return codes[:R, :D].contiguous().view(F8), scales.view(nr, nd)
 
 
