@@ -75,7 +75,11 @@ typedef enum {
   KVP_ERR_SCRATCH_LIMIT = 9 /* decode_noalloc: sizes need more than its scratch */
 } kvp_status;
 
-typedef enum { KVP_F16 = 0, KVP_BF16 = 1 } kvp_dtype;
+typedef enum {
+  KVP_F16 = 0,
+  KVP_BF16 = 1,
+  KVP_F32 = 2 /* kvp_matmul_fp8's out only */
+} kvp_dtype;
 
 /* Shape of one cache pool (K and V pools share it). */
 typedef struct {
@@ -480,6 +484,82 @@ kvp_status kvp_release_tables(const int32_t* block_tables, int32_t max_blocks_pe
                               int32_t batch, int32_t* free_blocks, const int32_t* free_count,
                               int32_t num_blocks, int32_t* context_lens_out,
                               int32_t* free_count_out, int32_t* dev_status, kvp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A layer's projections in 8 bits: the norm in front of them, quantisers, and the
+ * matrix product.  Values are E4M3 codes ("e4m3fn", as kvp_append_fp8) times float32
+ * scales, one per 128 elements of a row (the last group of a row may be shorter).
+ * For a group whose largest magnitude is a, with b = max(a, 2^-100):
+ *   scale = b / 448 (1 where a = 0),  code = E4M3(y * (448 / b)),
+ * every operation rounded to float32 by itself, codes to nearest even.  A NaN gets
+ * the code NaN; the other elements of its group are scaled as if it were not there.
+ * A group with an infinity has an infinite scale and stands for NaN.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * kvp_rms_norm -- root-mean-square norm of rows, with the residual's addition:
+ *   h = x, or x + residual (in float32, rounded once to `dtype`, written to
+ *       residual_out),
+ *   out = h * r * weight,  r = 1 / sqrt(sum h^2 / dim + eps),
+ * in float32, rounded once to `dtype`.  Rows are those of num_heads heads of dim
+ * elements per token (1 head: the whole token; several: e.g. q's or key's heads in
+ * front of kvp_rope_append), the heads of a token one behind the other, the token
+ * strides in elements -- so x may be a slice of one projection's output.  weight:
+ * [dim] of `dtype`.  dim: a multiple of 8, at most 32768; fewer than 2^31 rows.
+ * residual and residual_out: both or neither (NULL), with one head only.  out may be
+ * x (same stride); residual_out may be residual or x (same stride); otherwise outputs
+ * must not overlap an input or each other.  All rows 16-byte aligned, strides
+ * multiples of 8.  Squares are summed in float32: elements of 2^63 and more (bf16)
+ * give a row of zeros.
+ */
+kvp_status kvp_rms_norm(void* out, int64_t out_stride, const void* x, int64_t x_stride,
+                        const void* residual, int64_t residual_stride, void* residual_out,
+                        int64_t residual_out_stride, const void* weight, float eps,
+                        int32_t num_tokens, int32_t num_heads, int32_t dim, kvp_dtype dtype,
+                        kvp_stream_t stream);
+
+/*
+ * kvp_rms_norm_fp8 -- the same norm (one head), its float32 results held as codes
+ * without a rounding to 16 bits between.  codes: rows of dim bytes, codes_stride
+ * apart (a multiple of 16), 16-byte aligned; scales: [num_tokens, ceil(dim / 128)].
+ * dim: a multiple of 16.  Other arguments and errors as kvp_rms_norm.
+ */
+kvp_status kvp_rms_norm_fp8(uint8_t* codes, int64_t codes_stride, float* scales, const void* x,
+                            int64_t x_stride, const void* residual, int64_t residual_stride,
+                            void* residual_out, int64_t residual_out_stride, const void* weight,
+                            float eps, int32_t num_tokens, int32_t dim, kvp_dtype dtype,
+                            kvp_stream_t stream);
+
+/*
+ * kvp_quantise_fp8 -- rows of 16-bit values as codes.  block_rows = 1: a scale per row
+ * and 128 columns (an activation, e.g. the attention's output); block_rows = 128: a
+ * scale per 128 x 128 elements (a weight).  scales: [ceil(rows / block_rows),
+ * ceil(cols / 128)]; cols: a multiple of 16; rows * ceil(cols / 128) < 2^31.  Rows,
+ * codes and strides as kvp_rms_norm_fp8.  x and codes must not overlap.
+ */
+kvp_status kvp_quantise_fp8(uint8_t* codes, int64_t codes_stride, float* scales, const void* x,
+                            int64_t x_stride, int32_t rows, int32_t cols, int32_t block_rows,
+                            kvp_dtype dtype, kvp_stream_t stream);
+
+/*
+ * kvp_matmul_fp8 -- matrix product of codes, on the tensor cores:
+ *   out[i, j] = sum_g a_scale[i, g] b_scale[j / 128, g] sum_{l in group g} a[i, l] b[j, l]
+ * with a: [m, k] (an activation), a_scale: [m, ceil(k / 128)], b: [n, k] (a weight),
+ * b_scale: [ceil(n / 128), ceil(k / 128)]; rows of a and b a_stride and b_stride bytes
+ * apart.  The sum of a group is formed by the tensor cores, scaled and added to the
+ * others in float32, and rounded once to out's type (fp16, bf16 or float32).
+ * k: a multiple of 16; m and n: any.  a, b and their strides are multiples of 16
+ * bytes; out: rows of n elements, out_stride >= n elements apart, aligned to its type.
+ * A NaN code, or a scale that is no number, gives NaN in the rows (columns) it
+ * belongs to.  A product of two scales must lie in float32's normal range.  out must
+ * not overlap an input.  The same call gives the same bits.  Device errors:
+ * KVP_ERR_TIMEOUT when a pipeline wait gave up (the tiles concerned are written as
+ * zeros).
+ */
+kvp_status kvp_matmul_fp8(void* out, int64_t out_stride, kvp_dtype out_dtype, const uint8_t* a,
+                          int64_t a_stride, const float* a_scale, const uint8_t* b,
+                          int64_t b_stride, const float* b_scale, int32_t m, int32_t n, int32_t k,
+                          int32_t* dev_status, kvp_stream_t stream);
 
 /*
  * kvp_attention_prefill -- causal multi-query paged attention over fp16/bf16

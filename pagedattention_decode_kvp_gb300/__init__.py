@@ -37,6 +37,7 @@ KVP_ERR_SCRATCH_LIMIT = 9
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 KVP_F16 = 0
 KVP_BF16 = 1
+KVP_F32 = 2  # kvp_matmul_fp8's out only
 KVP_PHASE_PARTIAL = 1
 KVP_PHASE_REDUCE = 2
 KVP_PHASE_ALL = 3
@@ -111,6 +112,12 @@ SIGNATURES = {
     "kvp_extend_tables": (_I32, [_P, _I32, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _I32, _P, _P,
                                  _P, _P]),
     "kvp_release_tables": (_I32, [_P, _I32, _P, _P, _I32, _P, _P, _I32, _P, _P, _P, _P]),
+    "kvp_rms_norm": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _F, _I32, _I32, _I32, _I32,
+                            _P]),
+    "kvp_rms_norm_fp8": (_I32, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _F, _I32, _I32, _I32,
+                                _P]),
+    "kvp_quantise_fp8": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P]),
+    "kvp_matmul_fp8": (_I32, [_P, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _I32, _I32, _I32, _P, _P]),
     "kvp_read_status": (_I32, [_P, _P]),
     "kvp_selftest_wait_timeout": (_I32, [_P, _I64, _P]),
     "kvp_bm_create": (_P, [_I32, _I32, _I64]),
@@ -873,6 +880,111 @@ def kvp_release_tables(block_tables, context_lens, finished, free_blocks, free_c
                                   free_count.data_ptr(), NB, context_lens_out.data_ptr(),
                                   free_count_out.data_ptr(), _status_ptr(status), s),
            "kvp_release_tables")
+
+
+# ------------------------------------------------------------------ projections in 8 bits
+def _matrix(t, name, dtype, shape) -> int:
+    """Element stride between the rows of t [rows, n], whose elements are contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _codes(t, name, shape) -> int:
+    """Byte stride between rows of E4M3 codes, held as uint8 or float8_e4m3fn."""
+    torch = _torch()
+    return _matrix(t, name, torch.uint8 if t.dtype is torch.uint8 else torch.float8_e4m3fn, shape)
+
+
+def _norm_args(x, weight, residual, residual_out, T, D, dtype):
+    _need(weight, "weight", dtype, (D,))
+    if residual is None or residual_out is None:
+        if residual is not residual_out:
+            raise ValueError("residual and residual_out go together")
+        return (None, 0, None, 0)
+    if x.dim() != 2:
+        raise ValueError("a residual goes with x [T, D]")
+    rs = _matrix(residual, "residual", dtype, (T, D))
+    ro = _matrix(residual_out, "residual_out", dtype, (T, D))
+    return residual.data_ptr(), rs, residual_out.data_ptr(), ro
+
+
+def kvp_rms_norm(out, x, weight, eps, *, residual=None, residual_out=None, stream=None) -> None:
+    """out = h / sqrt(mean(h^2) + eps) * weight per row of x [T, D], or per head of
+    x [T, H, D] (fp16/bf16; any token stride that is a multiple of 8, so x may be a
+    slice of one projection's output).  h is x, or with residual [T, D] x + residual,
+    rounded to the dtype and written to residual_out.  out may be x, residual_out may
+    be residual."""
+    lib = load_library()
+    s = _on_one_device(stream, x, out, weight, residual, residual_out)
+    dtype = x.dtype
+    code = _dtype_code(x)
+    if x.dim() == 3:
+        T, H, D = _extents(x, "x", 3)
+        xs, os_ = _rows(x, "x", dtype, (T, H, D)), _rows(out, "out", dtype, (T, H, D))
+    else:
+        (T, D), H = _extents(x, "x", 2), 1
+        xs, os_ = _matrix(x, "x", dtype, (T, D)), _matrix(out, "out", dtype, (T, D))
+    more = _norm_args(x, weight, residual, residual_out, T, D, dtype)
+    _check(lib.kvp_rms_norm(out.data_ptr(), os_, x.data_ptr(), xs, *more, weight.data_ptr(), eps, T,
+                            H, D, code, s), "kvp_rms_norm")
+
+
+def kvp_rms_norm_fp8(codes, scales, x, weight, eps, *, residual=None, residual_out=None,
+                     stream=None) -> None:
+    """As kvp_rms_norm of x [T, D], the results held as E4M3 codes [T, D] (uint8 or
+    float8_e4m3fn) with float32 scales [T, ceil(D / 128)]: a of kvp_matmul_fp8."""
+    lib = load_library()
+    s = _on_one_device(stream, x, codes, scales, weight, residual, residual_out)
+    dtype = x.dtype
+    code = _dtype_code(x)
+    T, D = _extents(x, "x", 2)
+    xs, cs = _matrix(x, "x", dtype, (T, D)), _codes(codes, "codes", (T, D))
+    _need(scales, "scales", _torch().float32, (T, -(-D // 128)))
+    more = _norm_args(x, weight, residual, residual_out, T, D, dtype)
+    _check(lib.kvp_rms_norm_fp8(codes.data_ptr(), cs, scales.data_ptr(), x.data_ptr(), xs, *more,
+                                weight.data_ptr(), eps, T, D, code, s), "kvp_rms_norm_fp8")
+
+
+def kvp_quantise_fp8(codes, scales, x, *, block_rows=1, stream=None) -> None:
+    """x [R, D] (fp16/bf16) as E4M3 codes [R, D] (uint8 or float8_e4m3fn) with float32
+    scales [ceil(R / block_rows), ceil(D / 128)]: block_rows = 1 for activations, 128 for
+    weights, one scale per 128 x 128 elements."""
+    lib = load_library()
+    s = _on_one_device(stream, x, codes, scales)
+    code = _dtype_code(x)
+    R, D = _extents(x, "x", 2)
+    xs, cs = _matrix(x, "x", x.dtype, (R, D)), _codes(codes, "codes", (R, D))
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows is 1 or 128, got {block_rows}")
+    _need(scales, "scales", _torch().float32, (-(-R // block_rows), -(-D // 128)))
+    _check(lib.kvp_quantise_fp8(codes.data_ptr(), cs, scales.data_ptr(), x.data_ptr(), xs, R, D,
+                                int(block_rows), code, s), "kvp_quantise_fp8")
+
+
+def kvp_matmul_fp8(out, a, a_scale, b, b_scale, *, status=None, stream=None) -> None:
+    """out [M, N] (fp16, bf16 or float32) = a b^T of E4M3 codes a [M, K] and b [N, K]
+    (uint8 or float8_e4m3fn) with float32 scales a_scale [M, ceil(K / 128)] and b_scale
+    [ceil(N / 128), ceil(K / 128)], as kvp_rms_norm_fp8 and kvp_quantise_fp8 write them.
+    Rows may be strided (codes by multiples of 16)."""
+    lib = load_library()
+    s = _on_one_device(stream, out, a, a_scale, b, b_scale, status)
+    torch = _torch()
+    code = KVP_F32 if out.dtype is torch.float32 else _dtype_code(out)
+    M, K = _extents(a, "a", 2)
+    N = _extents(b, "b", 2)[0]
+    as_, bs = _codes(a, "a", (M, K)), _codes(b, "b", (N, K))
+    os_ = _matrix(out, "out", out.dtype, (M, N))
+    G = -(-K // 128)
+    _need(a_scale, "a_scale", torch.float32, (M, G))
+    _need(b_scale, "b_scale", torch.float32, (-(-N // 128), G))
+    _check(lib.kvp_matmul_fp8(out.data_ptr(), os_, code, a.data_ptr(), as_, a_scale.data_ptr(),
+                              b.data_ptr(), bs, b_scale.data_ptr(), M, N, K, _status_ptr(status), s),
+           "kvp_matmul_fp8")
 
 
 def kvp_selftest_wait_timeout(status, limit_ns, stream=None):

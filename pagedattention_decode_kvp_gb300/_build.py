@@ -38,6 +38,8 @@ SOURCES = [
     "kvp_reduce.cu",
     "kvp_rope_append.cu",
     "kvp_tables.cu",
+    "kvp_norm.cu",
+    "kvp_matmul_fp8.cu",
     "kvp_prefill.cu",
     "kvp_block_manager.cpp",
     "kvp_noalloc.cu",

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "kvp_internal.h"
+#include "kvp_project.h"
 #include "kvp_serve.h"
 
 using namespace kvp;
@@ -485,6 +486,55 @@ kvp_status rope_append_common(void* q_out, int64_t q_out_stride, const void* q, 
   p.sections_by_4 = by4;
   return from_cuda(launch_rope_append(p, dtype == KVP_BF16, c.head_dim, int4,
                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Rows of `n` elements of 16 bits, `stride` elements apart: whole 16-byte pieces.
+bool rows16_ok(const void* p, int64_t stride, int64_t n) {
+  return p != nullptr && aligned(p, 16) && stride % 8 == 0 && stride >= n;
+}
+// Rows of `n` codes, `stride` bytes apart.
+bool codes_ok(const void* p, int64_t stride, int64_t n) {
+  return p != nullptr && aligned(p, 16) && stride % 16 == 0 && stride >= n;
+}
+
+// Both norms' checks of what they read; the residual's strides are not looked at
+// without one.
+kvp_status check_norm(const NormParams& p, kvp_dtype dtype) {
+  if (p.num_tokens < 0 || p.num_heads <= 0 || p.dim <= 0 || (dtype != KVP_F16 && dtype != KVP_BF16))
+    return KVP_ERR_INVALID_ARG;
+  if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return KVP_ERR_INVALID_ARG;
+  if (p.dim % 8 != 0 || p.dim > kMaxNormDim) return KVP_ERR_UNSUPPORTED;
+  // CTAs of at least one row each
+  if (static_cast<long long>(p.num_tokens) * p.num_heads >= (1ll << 31)) return KVP_ERR_UNSUPPORTED;
+  if (p.num_tokens == 0) return KVP_OK;
+  const int64_t n = static_cast<int64_t>(p.num_heads) * p.dim;
+  if (!rows16_ok(p.x, p.x_stride, n) || p.weight == nullptr || !aligned(p.weight, 16))
+    return KVP_ERR_INVALID_ARG;
+  if ((p.residual == nullptr) != (p.residual_out == nullptr)) return KVP_ERR_INVALID_ARG;
+  if (p.residual == nullptr) return KVP_OK;
+  if (p.num_heads != 1) return KVP_ERR_UNSUPPORTED;
+  if (!rows16_ok(p.residual, p.residual_stride, n) ||
+      !rows16_ok(p.residual_out, p.residual_out_stride, n))
+    return KVP_ERR_INVALID_ARG;
+  return KVP_OK;
+}
+
+// TMA descriptor over codes [rows][k], `stride` bytes from row to row: a box is 128
+// bytes of `box_rows` rows, written with the 128-byte swizzle (K-major operand);
+// what lies past k or rows arrives as zeros.
+kvp_status make_codes_map(CUtensorMap* map, const void* codes, int64_t stride, int rows, int k,
+                          int box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return KVP_ERR_CUDA;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? KVP_OK : KVP_ERR_CUDA;
 }
 
 }  // namespace
@@ -1057,6 +1107,127 @@ kvp_status kvp_attention_decode_shared_prefix(
   // 3. merge
   if (launch_decode_reduce(p, s) != cudaSuccess) return KVP_ERR_CUDA;
   return KVP_OK;
+}
+
+kvp_status kvp_rms_norm(void* out, int64_t out_stride, const void* x, int64_t x_stride,
+                        const void* residual, int64_t residual_stride, void* residual_out,
+                        int64_t residual_out_stride, const void* weight, float eps,
+                        int32_t num_tokens, int32_t num_heads, int32_t dim, kvp_dtype dtype,
+                        kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_rms_norm");
+  NormParams p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.residual_out = static_cast<uint16_t*>(residual_out);
+  p.weight = static_cast<const uint16_t*>(weight);
+  p.out = static_cast<uint16_t*>(out);
+  p.x_stride = x_stride;
+  p.residual_stride = residual_stride;
+  p.residual_out_stride = residual_out_stride;
+  p.out_stride = out_stride;
+  p.num_tokens = num_tokens;
+  p.num_heads = num_heads;
+  p.dim = dim;
+  p.eps = eps;
+  const kvp_status st = check_norm(p, dtype);
+  if (st != KVP_OK) return st;
+  if (num_tokens == 0) return KVP_OK;
+  if (!rows16_ok(out, out_stride, static_cast<int64_t>(num_heads) * dim))
+    return KVP_ERR_INVALID_ARG;
+  return from_cuda(launch_rms_norm(p, dtype == KVP_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_rms_norm_fp8(uint8_t* codes, int64_t codes_stride, float* scales, const void* x,
+                            int64_t x_stride, const void* residual, int64_t residual_stride,
+                            void* residual_out, int64_t residual_out_stride, const void* weight,
+                            float eps, int32_t num_tokens, int32_t dim, kvp_dtype dtype,
+                            kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_rms_norm_fp8");
+  NormParams p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.residual_out = static_cast<uint16_t*>(residual_out);
+  p.weight = static_cast<const uint16_t*>(weight);
+  p.codes = codes;
+  p.scales = scales;
+  p.x_stride = x_stride;
+  p.residual_stride = residual_stride;
+  p.residual_out_stride = residual_out_stride;
+  p.codes_stride = codes_stride;
+  p.num_tokens = num_tokens;
+  p.num_heads = 1;
+  p.dim = dim;
+  p.eps = eps;
+  const kvp_status st = check_norm(p, dtype);
+  if (st != KVP_OK) return st;
+  if (dim % 16 != 0) return KVP_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return KVP_OK;
+  if (!codes_ok(codes, codes_stride, dim) || scales == nullptr || !aligned(scales, 4))
+    return KVP_ERR_INVALID_ARG;
+  return from_cuda(launch_rms_norm(p, dtype == KVP_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_quantise_fp8(uint8_t* codes, int64_t codes_stride, float* scales, const void* x,
+                            int64_t x_stride, int32_t rows, int32_t cols, int32_t block_rows,
+                            kvp_dtype dtype, kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_quantise_fp8");
+  if (rows < 0 || cols <= 0 || (dtype != KVP_F16 && dtype != KVP_BF16)) return KVP_ERR_INVALID_ARG;
+  if (cols % 16 != 0 || (block_rows != 1 && block_rows != kScaleGroup)) return KVP_ERR_UNSUPPORTED;
+  if (static_cast<long long>(rows) * ((cols + kScaleGroup - 1) / kScaleGroup) >= (1ll << 31))
+    return KVP_ERR_UNSUPPORTED;
+  if (rows == 0) return KVP_OK;
+  if (!rows16_ok(x, x_stride, cols) || !codes_ok(codes, codes_stride, cols) || scales == nullptr ||
+      !aligned(scales, 4))
+    return KVP_ERR_INVALID_ARG;
+  QuantiseParams p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.codes = codes;
+  p.scales = scales;
+  p.x_stride = x_stride;
+  p.codes_stride = codes_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.block_rows = block_rows;
+  return from_cuda(
+      launch_quantise_fp8(p, dtype == KVP_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_matmul_fp8(void* out, int64_t out_stride, kvp_dtype out_dtype, const uint8_t* a,
+                          int64_t a_stride, const float* a_scale, const uint8_t* b,
+                          int64_t b_stride, const float* b_scale, int32_t m, int32_t n, int32_t k,
+                          int32_t* dev_status, kvp_stream_t stream) {
+  KVP_NVTX_RANGE("kvp_matmul_fp8");
+  if (m < 0 || n <= 0 || k <= 0 ||
+      (out_dtype != KVP_F16 && out_dtype != KVP_BF16 && out_dtype != KVP_F32))
+    return KVP_ERR_INVALID_ARG;
+  if (k % 16 != 0 || k > INT32_MAX - 127) return KVP_ERR_UNSUPPORTED;
+  if (n > INT32_MAX - 127 || m > INT32_MAX - 255) return KVP_ERR_UNSUPPORTED;
+  if (m == 0) return KVP_OK;
+  if (!codes_ok(a, a_stride, k) || !codes_ok(b, b_stride, k) || a_scale == nullptr ||
+      b_scale == nullptr || !aligned(a_scale, 4) || !aligned(b_scale, 4))
+    return KVP_ERR_INVALID_ARG;
+  if (out == nullptr || !aligned(out, out_dtype == KVP_F32 ? 4 : 2) || out_stride < n)
+    return KVP_ERR_INVALID_ARG;
+  if (a_stride >= (1ll << 40) || b_stride >= (1ll << 40)) return KVP_ERR_UNSUPPORTED;
+  MatmulParams p{};
+  p.out = out;
+  p.a_scale = a_scale;
+  p.b_scale = b_scale;
+  p.status = dev_status;
+  p.out_stride = out_stride;
+  p.m = m;
+  p.n = n;
+  p.groups = (k + kScaleGroup - 1) / kScaleGroup;
+  p.out_type = out_dtype;
+  const MatmulPlan plan = matmul_plan(m, n, p.groups);
+  const long long tiles = static_cast<long long>((m + plan.tokens - 1) / plan.tokens) *
+                          ((n + kScaleGroup - 1) / kScaleGroup) * plan.splits;
+  if (tiles >= (1ll << 31)) return KVP_ERR_UNSUPPORTED;
+  CUtensorMap ta, tb;
+  kvp_status st = make_codes_map(&ta, a, a_stride, m, k, plan.tokens);
+  if (st == KVP_OK) st = make_codes_map(&tb, b, b_stride, n, k, kScaleGroup);
+  if (st != KVP_OK) return st;
+  return from_cuda(launch_matmul_fp8(p, plan, ta, tb, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kvp_status kvp_selftest_wait_timeout(int32_t* dev_status, int64_t limit_ns,

@@ -1,0 +1,277 @@
+// kvp_norm.cu -- root-mean-square norms and E4M3 quantisers of 16-bit rows.
+//
+// Norm of a row x of D elements with weight w:
+//   h = x, or RN16(x + residual) (float32 sum, rounded once and given back),
+//   y_i = h_i * r * w_i,  r = 1 / sqrt(sum h^2 / D + eps),
+// in float32; y is rounded once to the 16-bit type, or held as E4M3 codes.
+//
+// Codes of a group of 128 elements y (of a row, or of 128 rows of a weight):
+//   a = max |y|,  b = max(a, 2^-100),  scale = b / 448 (1 where a = 0),
+//   code = E4M3(y * (448 / b)),  each operation rounded to float32 by itself.
+// The bound 2^-100 keeps 448 / b finite.
+//
+// A lane holds whole 16-byte chunks of 8 elements, a row's chunks lie on consecutive
+// lanes, so that 16 lanes hold a group.
+#include "kvp_device.cuh"
+#include "kvp_project.h"
+
+namespace kvp {
+
+namespace {
+
+constexpr float kLargest = 448.0f;   // of E4M3
+
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void widen(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = dev::unpack2<kBf16>(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
+  return make_uint4(dev::pack2<kBf16>(x[0], x[1]), dev::pack2<kBf16>(x[2], x[3]),
+                    dev::pack2<kBf16>(x[4], x[5]), dev::pack2<kBf16>(x[6], x[7]));
+}
+
+__device__ __forceinline__ float absmax8(const float (&x)[8]) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
+  return a;
+}
+
+// Scale of a group whose largest magnitude is `most`, and what its elements are
+// multiplied by.
+__device__ __forceinline__ float group_scale(float most, float* up) {
+  const float b = fmaxf(most, 0x1p-100f);
+  *up = __fdiv_rn(kLargest, b);
+  return most > 0.f ? __fdiv_rn(b, kLargest) : 1.0f;
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float up) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = dev::f32x2_to_e4m3x2(__fmul_rn(x[2 * i], up), __fmul_rn(x[2 * i + 1], up));
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// Largest of the values of `kLanes` neighbouring lanes.
+template <int kLanes>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// kThreads threads hold a row, kChunks chunks each; up to 32 of them: several rows to a
+// CTA of 128 threads; more: a CTA to a row.
+template <bool kBf16, bool kFp8, int kThreads, int kChunks>
+__global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kernel(NormParams p) {
+  constexpr int kRows = kThreads < 128 ? 128 / kThreads : 1;   // of a CTA
+  constexpr int kGroupLanes = kThreads < 16 ? kThreads : 16;
+  dev::grid_dependency_wait();
+  dev::launch_dependents();
+  const int lane = static_cast<int>(threadIdx.x) % kThreads;
+  const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kThreads;
+  const long long rows = static_cast<long long>(p.num_tokens) * p.num_heads;
+  const bool in = row < rows;
+  const long long t = p.num_heads == 1 ? row : row / p.num_heads;
+  const int head = p.num_heads == 1 ? 0 : static_cast<int>(row - t * p.num_heads);
+  const long long col = static_cast<long long>(head) * p.dim;   // of the row within its token
+  uint4 raw[kChunks], other[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int at = 8 * (lane + c * kThreads);
+    raw[c] = other[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (in && at < p.dim) {
+      raw[c] = load16(p.x + t * p.x_stride + col + at);
+      if (p.residual != nullptr) other[c] = load16(p.residual + t * p.residual_stride + at);
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    float x[8];
+    widen<kBf16>(raw[c], x);
+    if (p.residual != nullptr) {
+      float r[8];
+      widen<kBf16>(other[c], r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += r[i];
+      raw[c] = narrow<kBf16>(x);
+      widen<kBf16>(raw[c], x);
+      const int at = 8 * (lane + c * kThreads);
+      if (in && at < p.dim)
+        *reinterpret_cast<uint4*>(p.residual_out + t * p.residual_out_stride + at) = raw[c];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+  }
+#pragma unroll
+  for (int o = (kThreads < 32 ? kThreads : 32) / 2; o > 0; o >>= 1)
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if constexpr (kThreads > 32) {
+    __shared__ float part[kThreads / 32];
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
+  }
+  const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(p.dim)), p.eps));
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int at = 8 * (lane + c * kThreads);
+    const bool mine = in && at < p.dim;
+    float x[8], w[8];
+    widen<kBf16>(raw[c], x);
+    widen<kBf16>(mine ? load16(p.weight + at) : make_uint4(0u, 0u, 0u, 0u), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+    if constexpr (kFp8) {
+      const float most = lanes_max<kGroupLanes>(mine ? absmax8(x) : 0.f);
+      float up;
+      const float scale = group_scale(most, &up);
+      if (mine) {
+        *reinterpret_cast<uint2*>(p.codes + t * p.codes_stride + at) = codes8(x, up);
+        if (at % kScaleGroup == 0)
+          p.scales[t * ((p.dim + kScaleGroup - 1) / kScaleGroup) + at / kScaleGroup] = scale;
+      }
+    } else if (mine) {
+      *reinterpret_cast<uint4*>(p.out + t * p.out_stride + col + at) = narrow<kBf16>(x);
+    }
+  }
+}
+
+// Rows by themselves: 16 lanes take a group, kUnits groups one after the other.
+constexpr int kQuantUnits = 4;
+constexpr int kQuantSlots = 16;   // groups that a CTA of 256 threads works on at a time
+template <bool kBf16>
+__global__ void __launch_bounds__(256) quantise_rows_kernel(QuantiseParams p, int groups) {
+  dev::grid_dependency_wait();
+  dev::launch_dependents();
+  const int sub = threadIdx.x % 16;
+  const long long units = static_cast<long long>(p.rows) * groups;
+  const long long first =
+      static_cast<long long>(blockIdx.x) * (kQuantSlots * kQuantUnits) + threadIdx.x / 16;
+  uint4 raw[kQuantUnits];
+  long long row[kQuantUnits];
+  int at[kQuantUnits];
+#pragma unroll
+  for (int j = 0; j < kQuantUnits; ++j) {
+    const long long u = first + j * kQuantSlots;
+    row[j] = u / groups;
+    at[j] = static_cast<int>(u - row[j] * groups) * kScaleGroup + 8 * sub;
+    if (u >= units || at[j] >= p.cols) at[j] = -1;
+    raw[j] = at[j] >= 0 ? load16(p.x + row[j] * p.x_stride + at[j]) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int j = 0; j < kQuantUnits; ++j) {
+    float x[8], up;
+    widen<kBf16>(raw[j], x);
+    const float scale = group_scale(lanes_max<16>(absmax8(x)), &up);
+    if (at[j] < 0) continue;
+    *reinterpret_cast<uint2*>(p.codes + row[j] * p.codes_stride + at[j]) = codes8(x, up);
+    if (sub == 0) p.scales[row[j] * groups + at[j] / kScaleGroup] = scale;
+  }
+}
+
+// A CTA takes 128 rows of 128 columns: 8 chunks a thread.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) quantise_blocks_kernel(QuantiseParams p, int groups) {
+  dev::grid_dependency_wait();
+  dev::launch_dependents();
+  const long long block = blockIdx.x / groups;
+  const int group = blockIdx.x % groups;
+  const int at = group * kScaleGroup + 8 * (threadIdx.x % 16);
+  uint4 raw[8];
+  float most = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const long long row = block * kScaleGroup + threadIdx.x / 16 + 16 * j;
+    raw[j] = row < p.rows && at < p.cols ? load16(p.x + row * p.x_stride + at)
+                                         : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float x[8];
+    widen<kBf16>(raw[j], x);
+    most = fmaxf(most, absmax8(x));
+  }
+  most = dev::warp_max(most);
+  __shared__ float part[8];
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = most;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = fmaxf(most, part[i]);
+  float up;
+  const float scale = group_scale(most, &up);
+  if (threadIdx.x == 0) p.scales[block * groups + group] = scale;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const long long row = block * kScaleGroup + threadIdx.x / 16 + 16 * j;
+    if (row >= p.rows || at >= p.cols) continue;
+    float x[8];
+    widen<kBf16>(raw[j], x);
+    *reinterpret_cast<uint2*>(p.codes + row * p.codes_stride + at) = codes8(x, up);
+  }
+}
+
+template <bool kBf16, bool kFp8>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
+  const long long rows = static_cast<long long>(p.num_tokens) * p.num_heads;
+  const int chunks = p.dim / 8;
+#define KVP_NORM(T, C)                                                                  \
+  {                                                                                     \
+    constexpr int kRows = T < 128 ? 128 / T : 1;                                        \
+    return launch_pdl(rms_norm_kernel<kBf16, kFp8, T, C>,                               \
+                      dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)),          \
+                      dim3(T < 128 ? 128 : T), 0, s, p);                                \
+  }
+  if (chunks <= 8) KVP_NORM(8, 1)
+  if (chunks <= 16) KVP_NORM(16, 1)
+  if (chunks <= 32) KVP_NORM(32, 1)
+  if (chunks <= 64) KVP_NORM(32, 2)
+  if (chunks <= 128) KVP_NORM(128, 1)
+  if (chunks <= 256) KVP_NORM(128, 2)
+  if (chunks <= 512) KVP_NORM(256, 2)
+  if (chunks <= 1024) KVP_NORM(512, 2)
+  if (chunks <= 2048) KVP_NORM(1024, 2)
+  if (chunks <= 4096) KVP_NORM(1024, 4)
+#undef KVP_NORM
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s) {
+  if (p.out == nullptr) return bf16 ? launch_norm<true, true>(p, s) : launch_norm<false, true>(p, s);
+  return bf16 ? launch_norm<true, false>(p, s) : launch_norm<false, false>(p, s);
+}
+
+cudaError_t launch_quantise_fp8(const QuantiseParams& p, bool bf16, cudaStream_t s) {
+  const int groups = (p.cols + kScaleGroup - 1) / kScaleGroup;
+  if (p.block_rows == 1) {
+    const long long units = static_cast<long long>(p.rows) * groups;
+    constexpr int kPer = kQuantSlots * kQuantUnits;
+    const dim3 grid(static_cast<unsigned>((units + kPer - 1) / kPer));
+    return launch_pdl(bf16 ? quantise_rows_kernel<true> : quantise_rows_kernel<false>, grid,
+                      dim3(256), 0, s, p, groups);
+  }
+  const long long blocks = (static_cast<long long>(p.rows) + kScaleGroup - 1) / kScaleGroup;
+  const dim3 grid(static_cast<unsigned>(blocks * groups));
+  return launch_pdl(bf16 ? quantise_blocks_kernel<true> : quantise_blocks_kernel<false>, grid,
+                    dim3(256), 0, s, p, groups);
+}
+
+}  // namespace kvp
