@@ -40,6 +40,7 @@ SOURCES = [
     "kvp_tables.cu",
     "kvp_norm.cu",
     "kvp_matmul_fp8.cu",
+    "kvp_matmul_fp8_pair.cu",
     "kvp_prefill.cu",
     "kvp_block_manager.cpp",
     "kvp_noalloc.cu",

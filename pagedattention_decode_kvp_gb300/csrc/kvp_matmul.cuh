@@ -1,0 +1,71 @@
+// kvp_matmul.cuh -- what the block-scaled matrix products share: kind::f8f6f4
+// instructions, clusters, and the store of a result.
+#pragma once
+
+#include "kvp_device.cuh"
+#include "kvp_project.h"
+#include "kvp_umma.cuh"
+
+namespace kvp {
+namespace mm {
+
+// D[tmem] (+)= A[smem] * B[smem] over E4M3 codes; issued by one thread.  kGroup = 2: by
+// the first CTA of a pair, whose halves of A, B and D lie at the same addresses.
+template <int kGroup>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kGroup == 1) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+  }
+}
+
+// dev::mbar_wait_bounded without a call: a called function's registers do not go with
+// setmaxnreg.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+  if (dev::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = dev::global_timer_ns();
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 26); ++i) {
+    if (dev::mbar_try_wait_sleep(bar, parity, dev::kWaitHintNs)) return true;
+    if ((i & 15u) == 15u && dev::global_timer_ns() - t0 > dev::kWaitTimeoutNs) break;
+  }
+  return false;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Where CTA `rank` of the cluster has what lies at shared address `addr` here.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
+  return there;
+}
+__device__ __forceinline__ uint32_t load_remote(uint32_t there) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store_out(const MatmulParams& p, long long at, float v) {
+  if (p.out_type == KVP_F32) static_cast<float*>(p.out)[at] = v;
+  else if (p.out_type == KVP_BF16) static_cast<uint16_t*>(p.out)[at] = dev::from_float<true>(v);
+  else static_cast<uint16_t*>(p.out)[at] = dev::from_float<false>(v);
+}
+
+}  // namespace mm
+}  // namespace kvp

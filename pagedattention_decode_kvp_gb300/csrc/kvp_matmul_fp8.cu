@@ -12,9 +12,7 @@
 // buffers, so that a group is scaled while the next is multiplied.  Where few tiles
 // meet many SMs, the CTAs of a cluster share a tile's K and add their sums through
 // distributed shared memory, in the order of their ranks.
-#include "kvp_device.cuh"
-#include "kvp_project.h"
-#include "kvp_umma.cuh"
+#include "kvp_matmul.cuh"
 
 namespace kvp {
 
@@ -40,38 +38,6 @@ struct Shape {
   static_assert(kStages * kStage >= kTokens * kRowsB * 4, "the sums are exchanged in the ring");
 };
 
-// D[tmem] (+)= A[smem] * B[smem] over E4M3 codes; issued by one thread.
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                       uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A word of CTA `rank`'s shared memory, at the address that it has in this one's.
-__device__ __forceinline__ uint32_t load_remote(uint32_t addr, uint32_t rank) {
-  uint32_t there, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ void store_out(const MatmulParams& p, long long at, float v) {
-  if (p.out_type == KVP_F32) static_cast<float*>(p.out)[at] = v;
-  else if (p.out_type == KVP_BF16) static_cast<uint16_t*>(p.out)[at] = dev::from_float<true>(v);
-  else static_cast<uint16_t*>(p.out)[at] = dev::from_float<false>(v);
-}
-
 // grid.x = (token tile, weight tile, rank of the cluster), the last running fastest.
 template <int kTokens>
 __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
@@ -91,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ int failed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = splits > 1 ? cluster_rank() : 0;
+  const uint32_t rank = splits > 1 ? mm::cluster_rank() : 0;
   const long long tile = blockIdx.x / splits;
   const int tiles_n = (p.n + kRowsB - 1) / kRowsB;
   const int n0 = static_cast<int>(tile % tiles_n) * kRowsB;
@@ -152,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
         const uint64_t a = umma::smem_desc_sw128(at + kTileB, 16, 1024);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          mma_f8(tmem + buf * kTokens, b + 2 * s, a + 2 * s, kInstr, s > 0);
+          mm::mma_f8<1>(tmem + buf * kTokens, b + 2 * s, a + 2 * s, kInstr, s > 0);
         umma::commit(smem_addr(empty + st));
         umma::commit(smem_addr(sums + buf));
       }
@@ -217,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
     for (int j = 0; j < kTokens; ++j) {
       const float2 v = f2unpack(acc[j / 2]);
       if (m0 + j < p.m)
-        store_out(p, static_cast<long long>(m0 + j) * p.out_stride + n, bad ? 0.f : j & 1 ? v.y : v.x);
+        mm::store_out(p, static_cast<long long>(m0 + j) * p.out_stride + n, bad ? 0.f : j & 1 ? v.y : v.x);
     }
     return;
   }
@@ -230,18 +196,18 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
       mine[j * kRowsB + tid] = j & 1 ? v.y : v.x;
     }
   }
-  cluster_sync();
-  for (int r = 0; r < splits; ++r) bad = load_remote(smem_addr(&failed), r) != 0 || bad;
+  mm::cluster_sync();
+  for (int r = 0; r < splits; ++r) bad = mm::load_remote(mm::at_rank(smem_addr(&failed), r)) != 0 || bad;
   if (warp < kAddWarps && n < p.n) {
     const int end = min(static_cast<int>(kTokens * (rank + 1) / splits), p.m - m0);
     for (int j = kTokens * rank / splits; j < end; ++j) {
       float v = 0.f;
       for (int r = 0; r < splits; ++r)
-        v += __uint_as_float(load_remote(smem_addr(mine + j * kRowsB + tid), r));
-      store_out(p, static_cast<long long>(m0 + j) * p.out_stride + n, bad ? 0.f : v);
+        v += __uint_as_float(mm::load_remote(mm::at_rank(smem_addr(mine + j * kRowsB + tid), r)));
+      mm::store_out(p, static_cast<long long>(m0 + j) * p.out_stride + n, bad ? 0.f : v);
     }
   }
-  cluster_sync();
+  mm::cluster_sync();
 }
 
 template <int kTokens>
@@ -278,6 +244,11 @@ MatmulPlan matmul_plan(int m, int n, int groups) {
   const long long tiles = static_cast<long long>((n + kRowsB - 1) / kRowsB) *
                           ((m + plan.tokens - 1) / plan.tokens);
   plan.splits = 1;
+  // pairs where their tiles are enough for the SMs
+  if (m > 128 && static_cast<long long>((m + 255) / 256) * ((n + 255) / 256) >= kNumSms / 2) {
+    plan.tokens = 256;
+    return plan;
+  }
   while (plan.splits < 8 && tiles * plan.splits * 2 <= 304 && plan.splits * 4 <= groups)
     plan.splits *= 2;
   return plan;
@@ -286,6 +257,7 @@ MatmulPlan matmul_plan(int m, int n, int groups) {
 cudaError_t launch_matmul_fp8(const MatmulParams& p, const MatmulPlan& plan, const CUtensorMap& ta,
                               const CUtensorMap& tb, cudaStream_t s) {
   switch (plan.tokens) {
+    case 256: return launch_matmul_fp8_pair(p, ta, tb, s);
     case 16: return launch<16>(p, plan.splits, ta, tb, s);
     case 32: return launch<32>(p, plan.splits, ta, tb, s);
     case 64: return launch<64>(p, plan.splits, ta, tb, s);

@@ -42,17 +42,22 @@ struct MatmulParams {
   int32_t out_type;           // a kvp_dtype
 };
 
+constexpr int kNumSms = 152;
+
 // How a matrix product is cut (matmul_plan).
 struct MatmulPlan {
-  int tokens;                 // rows of a per tile
+  int tokens;                 // rows of a per tile (256: pairs of CTAs)
   int splits;                 // CTAs that share a tile's K
+  int box() const { return tokens < 128 ? tokens : 128; }   // rows of a per copy
 };
 MatmulPlan matmul_plan(int m, int n, int groups);
 
 cudaError_t launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_quantise_fp8(const QuantiseParams& p, bool bf16, cudaStream_t s);
-// ta, tb: K-major maps of a and b with boxes of 128 bytes x plan.tokens (a) and 128 (b) rows.
+// ta, tb: K-major maps of a and b with boxes of 128 bytes x plan.box() (a) and 128 (b) rows.
 cudaError_t launch_matmul_fp8(const MatmulParams& p, const MatmulPlan& plan, const CUtensorMap& ta,
                               const CUtensorMap& tb, cudaStream_t s);
+cudaError_t launch_matmul_fp8_pair(const MatmulParams& p, const CUtensorMap& ta,
+                                   const CUtensorMap& tb, cudaStream_t s);
 
 }  // namespace kvp

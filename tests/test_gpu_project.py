@@ -211,7 +211,8 @@ SHAPES = [(1, 768, 512), (1, 1, 16), (2, 100, 48), (7, 129, 128), (16, 128, 144)
           (32, 1000, 1024), (33, 64, 4096), (48, 4096, 512), (63, 130, 1040), (64, 10240, 1024),
           (65, 257, 2048), (100, 333, 656), (127, 128, 128), (128, 512, 4096), (129, 1281, 384),
           (200, 77, 8192), (256, 256, 256), (257, 640, 1152), (517, 2048, 1024), (1000, 1, 512),
-          (1024, 1024, 16), (2049, 1100, 640)]
+          (1024, 1024, 16), (2049, 1100, 640), (260, 9800, 400), (2500, 2000, 272),
+          (5000, 1030, 144), (2305, 2304, 4224), (513, 13000, 16)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
