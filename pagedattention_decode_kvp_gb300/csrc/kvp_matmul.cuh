@@ -30,7 +30,11 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
 // dev::mbar_wait_bounded without a call: a called function's registers do not go with
 // setmaxnreg.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
-  if (dev::mbar_try_wait(bar, parity)) return true;
+  // (reading the timer takes longer than most waits last)
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i) {
+    if (dev::mbar_try_wait(bar, parity)) return true;
+  }
   const uint64_t t0 = dev::global_timer_ns();
 #pragma unroll 1
   for (uint32_t i = 0; i < (1u << 26); ++i) {
@@ -38,6 +42,16 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     if ((i & 15u) == 15u && dev::global_timer_ns() - t0 > dev::kWaitTimeoutNs) break;
   }
   return false;
+}
+
+// Both barriers: one trip to shared memory where both are done (a trip takes about 130
+// cycles).
+__device__ __forceinline__ bool wait_both(uint32_t bar, uint32_t parity, uint32_t bar2,
+                                          uint32_t parity2) {
+  const bool one = dev::mbar_try_wait(bar, parity);
+  const bool two = dev::mbar_try_wait(bar2, parity2);
+  if (one && two) return true;
+  return wait(bar, parity) && wait(bar2, parity2);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -1,13 +1,17 @@
 // kvp_matmul_fp8_pair.cu -- the block-scaled product of kvp_matmul_fp8 for many rows:
 // pairs of CTAs on tiles of 256 x 256.
 //
-// A pair's tcgen05.mma (cta_group::2, M = N = 256) takes half of A's rows and half of
-// B's from each CTA's shared memory, so that a byte fetched serves 256 rows; each CTA
-// holds the sums of 128 rows in its TMEM: two buffers of 256 columns, all of it.  Eight
-// warps read a group's sums, a thread 128 columns of one row, and add them, scaled, to
-// float32 sums in registers (whose columns share one scale of B, and whose row one of
-// A) while the tensor cores form the next group's.  Persistent: a pair walks the tiles,
-// and the fetching warps run on into the next one.
+// A pair's tcgen05.mma (cta_group::2, M = 256, N = 128) takes half of A's rows and half
+// of B's from each CTA's shared memory, so that a byte fetched serves 256 rows; each CTA
+// holds the sums of 128 rows in its TMEM.  Eight warps read a group's sums, a thread 128
+// columns of one row, and add them, scaled, to float32 sums in registers (whose columns
+// share one scale of B, and whose row one of A) while the tensor cores form the next
+// group's.  Persistent: a pair walks the tiles, and the fetching warps run on into the
+// next one.
+//
+// What bounds it is the way round of a TMEM buffer: product, commit, read, arrival from
+// both CTAs, next product.  A tile's two column halves therefore go round by themselves,
+// each with two buffers of 128 columns and four adding warps per CTA.
 #include "kvp_matmul.cuh"
 
 namespace kvp {
@@ -15,21 +19,28 @@ namespace kvp {
 namespace {
 
 constexpr int kTile = 256;                    // rows and columns of a pair's tile
+constexpr int kHalfN = 128;                   // columns of a half: one instruction's
 constexpr uint32_t kHalf = 128 * 128;         // bytes of a CTA's half of A or B per stage
 constexpr uint32_t kStage = 2 * kHalf;
 constexpr int kStages = 6;
 constexpr int kAddWarps = 8;
-constexpr int kThreads = (kAddWarps + 4) * 32;   // three warpgroups; two warps are idle
-// Registers: the launch's 168 a thread are split anew, 2 * 128 * 232 + 128 * 40 = 384 * 168.
-constexpr int kAddRegs = 232;
-constexpr int kOtherRegs = 40;
+constexpr int kCols = 128;                    // a thread's, of one row
+constexpr int kThreads = (kAddWarps + 4) * 32;   // three warpgroups
+// Registers: the launch's 168 a thread are split anew, 256 * 216 + 128 * 72 = 384 * 168.
+constexpr int kAddRegs = 216;
+constexpr int kOtherRegs = 72;
 static_assert(kAddWarps * 32 * kAddRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
-constexpr uint32_t kWarpBytes = 4096;         // each adding warp's: scales, then results
-constexpr uint32_t kWarpOff = kStages * kStage;
+constexpr uint32_t kWarpBytes = 1024;         // each adding warp's, for its results
+constexpr int kSpan = 8;                      // groups whose scales are staged at a time
+constexpr int kSpans = 4;                     // spans that are there
+constexpr int kPitch = 132;                   // floats from one group's row scales to the next's
+constexpr uint32_t kSpanBytes = (kSpan * kPitch + 2 * kSpan) * 4;   // rows', then the halves' of B
+constexpr uint32_t kScaleOff = kStages * kStage;
+constexpr uint32_t kWarpOff = kScaleOff + kSpans * kSpanBytes;
 constexpr uint32_t kBarOff = kWarpOff + kAddWarps * kWarpBytes;
-constexpr uint32_t kSmem = 1024 + kBarOff + (2 * kStages + 5) * 8 + 16;
+constexpr int kNumBars = 2 * kStages + 9 + 2 * kSpans;
+constexpr uint32_t kSmem = 1024 + kBarOff + kNumBars * 8 + 16;
 constexpr uint32_t kTmem = 512;
-constexpr int kSpan = 32;                     // groups whose scales are staged at a time
 constexpr int kBand = 8;                      // row tiles that are walked together
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
@@ -49,8 +60,11 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       " [%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3))
       : "memory");
 }
+// Relaxed: what it announces is that TMEM was read, which tcgen05.wait::ld and the fence
+// order; a release at cluster scope waits for this thread's memory accesses and made a
+// group take 2200 cycles instead of 1300.
 __device__ __forceinline__ void arrive_remote(uint32_t there) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(there)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(there)
                : "memory");
 }
 __device__ __forceinline__ void alloc_pair(uint32_t dst) {
@@ -103,14 +117,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_fp8_pair_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap ta,
                            const __grid_constant__ CUtensorMap tb) {
   using namespace dev;
-  constexpr uint32_t kInstr = umma::instr_desc_f16(kTile, kTile, false, false, false);
+  constexpr uint32_t kInstr = umma::instr_desc_f16(kTile, kHalfN, false, false, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBarOff);   // (of the first CTA)
   uint64_t* empty = full + kStages;
-  uint64_t* sums = empty + kStages;   // [2] a TMEM buffer holds a group's sums
-  uint64_t* taken = sums + 2;         // [2] both CTAs have them in registers (first CTA)
-  uint64_t* done = taken + 2;         // every product of the pair complete
+  uint64_t* sums = empty + kStages;   // [half][2] a TMEM buffer holds a group's sums
+  uint64_t* taken = sums + 4;         // [half][2] both CTAs have read them (first CTA's)
+  uint64_t* scaled = taken + 4;       // [kSpans] scales are there
+  uint64_t* used = scaled + kSpans;   // [kSpans] they have been read
+  uint64_t* done = used + kSpans;     // every product of the pair complete
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ int failed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -122,13 +138,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     failed = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(full + i), 1);
-      mbar_init(smem_addr(empty + i), 1);
+      mbar_init(smem_addr(empty + i), 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_addr(sums + i), 1);
-      mbar_init(smem_addr(taken + i), 2 * kAddWarps);
+      mbar_init(smem_addr(taken + i), kAddWarps);   // half of each CTA's
     }
-    mbar_init(smem_addr(done), 1);
+    for (int i = 0; i < kSpans; ++i) {
+      mbar_init(smem_addr(scaled + i), 1);
+      mbar_init(smem_addr(used + i), kAddWarps);
+    }
+    mbar_init(smem_addr(done), 2);
     prefetch_tensormap(&ta);
     prefetch_tensormap(&tb);
     fence_barrier_init();
@@ -143,122 +163,155 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   bool ok = true;
   if (warp >= kAddWarps) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kAddWarps) {
-    // ---- fetch this CTA's halves; the first CTA expects the bytes of both
-    Ring<kStages> ring;
-    for (long long i = pair; i < tiles && ok; i += pairs) {
-      int tm, tn;
-      walk.at(i, &tm, &tn);
-      const int m0 = tm * kTile + 128 * rank, n0 = tn * kTile + 128 * rank;
-      for (int k = 0; k < p.groups && ok; ++k, ring.next()) {
-        const int st = ring.at;
-        ok = mm::wait(smem_addr(empty + st), ring.flip ^ 1);
-        if (ok && elect_one()) {
-          const uint32_t bar = mm::at_rank(smem_addr(full + st), 0);
-          const uint32_t at = smem_addr(sm + st * kStage);
-          if (rank == 0) mbar_arrive_expect_tx(smem_addr(full + st), 2 * kStage);
-          load_pair(at, &ta, k * 128, m0, bar);
-          load_pair(at + kHalf, &tb, k * 128, n0, bar);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kAddWarps) {
+      // ---- fetch this CTA's halves; the first CTA expects the bytes of both
+      Ring<kStages> ring;
+      for (long long i = pair; i < tiles && ok; i += pairs) {
+        int tm, tn;
+        walk.at(i, &tm, &tn);
+        const int m0 = tm * kTile + 128 * rank, n0 = tn * kTile + 64 * rank;
+        for (int k = 0; k < p.groups && ok; ++k, ring.next()) {
+          const int st = ring.at;
+          ok = mm::wait(smem_addr(empty + st), ring.flip ^ 1);
+          if (ok && elect_one()) {
+            const uint32_t bar = mm::at_rank(smem_addr(full + st), 0);
+            const uint32_t at = smem_addr(sm + st * kStage);
+            if (rank == 0) mbar_arrive_expect_tx(smem_addr(full + st), 2 * kStage);
+            load_pair(at, &ta, k * 128, m0, bar);
+            load_pair(at + kHalf, &tb, k * 128, n0, bar);
+            load_pair(at + kHalf + kHalf / 2, &tb, k * 128, n0 + kHalfN, bar);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
-    // no copy may land after the exit: the pair's last products have read every stage
-    ok = mm::wait(smem_addr(done), 0) && ok;
-  } else if (warp == kAddWarps + 1 && rank == 0) {
-    // ---- products of the pair
-    Ring<kStages> ring;
-    Ring<2> buffer;
-    for (long long i = pair; i < tiles && ok; i += pairs) {
-      for (int k = 0; k < p.groups && ok; ++k, ring.next(), buffer.next()) {
-        const int st = ring.at, buf = buffer.at;
-        ok = mm::wait(smem_addr(full + st), ring.flip) &&
-             mm::wait(smem_addr(taken + buf), buffer.flip ^ 1);
-        umma::fence_after_sync();
-        if (ok && elect_one()) {
+      // no copy may land after the exit: the pair's last products have read every stage
+      ok = mm::wait(smem_addr(done), 0) && ok;
+    } else if (warp <= kAddWarps + 2 && rank == 0) {
+      // ---- products of the pair: a warp for each half of the columns (one warp's waits and
+      // issues took 960 cycles a group, the products take 512)
+      const int h = warp - (kAddWarps + 1);
+      Ring<kStages> ring;
+      Ring<2> buffer;
+      for (long long i = pair; i < tiles && ok; i += pairs) {
+        for (int k = 0; k < p.groups && ok; ++k, ring.next(), buffer.next()) {
+          const int st = ring.at, buf = 2 * h + buffer.at;
           const uint32_t at = smem_addr(sm + st * kStage);
           const uint64_t a = umma::smem_desc_sw128(at, 16, 1024);
-          const uint64_t b = umma::smem_desc_sw128(at + kHalf, 16, 1024);
+          const uint64_t b = umma::smem_desc_sw128(at + kHalf + h * (kHalf / 2), 16, 1024);
+          ok = mm::wait_both(smem_addr(full + st), ring.flip, smem_addr(taken + buf),
+                             buffer.flip ^ 1);
+          umma::fence_after_sync();
+          if (ok && elect_one()) {
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            mm::mma_f8<2>(tmem + buf * kTile, a + 2 * s, b + 2 * s, kInstr, s > 0);
-          commit_pair(smem_addr(empty + st));
-          commit_pair(smem_addr(sums + buf));
+            for (int s = 0; s < 4; ++s)
+              mm::mma_f8<2>(tmem + buf * kHalfN, a + 2 * s, b + 2 * s, kInstr, s > 0);
+            commit_pair(smem_addr(sums + buf));
+            commit_pair(smem_addr(empty + st));
+          }
+          __syncwarp();
         }
-        __syncwarp();
+      }
+      if (elect_one()) commit_pair(smem_addr(done));
+      __syncwarp();
+      ok = mm::wait(smem_addr(done), 0) && ok;
+    } else if (warp == kAddWarps + 3) {
+      // ---- scales of the CTA's 128 rows and of the tile's two halves, spans of 8 groups: 8
+      // lanes take a row's, so that its 32 bytes are one sector
+      Ring<kSpans> ring;
+      for (long long i = pair; i < tiles && ok; i += pairs) {
+        int tm, tn;
+        walk.at(i, &tm, &tn);
+        const int m0 = tm * kTile + 128 * static_cast<int>(rank) + lane / 8;
+        const int n0 = tn * kTile;
+        for (int k = 0; k < p.groups && ok; k += kSpan, ring.next()) {
+          float* to = reinterpret_cast<float*>(sm + kScaleOff + ring.at * kSpanBytes);
+          const int g = k + lane % 8;
+          const bool in = g < p.groups;
+          const float* from = p.a_scale + static_cast<long long>(m0) * p.groups + g;
+          const int n = n0 + lane / 8 * kHalfN;
+          const float b = in && lane < 16 && n < p.n
+                              ? p.b_scale[static_cast<long long>(n / kScaleGroup) * p.groups + g] : 0.f;
+#pragma unroll 1
+          for (int h = 0; h < 32; h += 16) {
+            float v[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              v[r] = in && m0 + 4 * (h + r) < p.m ? from[static_cast<long long>(4 * (h + r)) * p.groups]
+                                                  : 0.f;
+            if (h == 0) ok = mm::wait(smem_addr(used + ring.at), ring.flip ^ 1);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) to[lane % 8 * kPitch + lane / 8 + 4 * (h + r)] = v[r];
+          }
+          if (lane < 16) to[kSpan * kPitch + lane] = b;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(scaled + ring.at));
+        }
       }
     }
-    if (elect_one()) commit_pair(smem_addr(done));
-    __syncwarp();
-    ok = mm::wait(smem_addr(done), 0) && ok;
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
-    // ---- scale and add: row 32 (warp % 4) + lane, columns 128 (warp / 4) .. + 127
-    const int quarter = warp & 3, half = warp >> 2;
-    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
-    float* mine = reinterpret_cast<float*>(sm + kWarpOff + warp * kWarpBytes);
-    const uint32_t free_bar[2] = {mm::at_rank(smem_addr(taken), 0),
-                                  mm::at_rank(smem_addr(taken + 1), 0)};
+    // ---- scale and add: row 32 (warp % 4) + lane, kCols columns from kCols (warp / 4) on
+    const int quarter = warp & 3, first = warp / 4 * kCols, half = first / kHalfN;
+    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kTile +
+                        first % kHalfN;
+    uint4* piece = reinterpret_cast<uint4*>(sm + kWarpOff + warp * kWarpBytes);
+    const uint32_t free_bar = mm::at_rank(smem_addr(taken + 2 * half), 0);
     Ring<2> buffer;
+    Ring<kSpans> spans;
     for (long long i = pair; i < tiles; i += pairs) {
+      uint64_t acc[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
+      for (int k0 = 0; k0 < p.groups; k0 += kSpan, spans.next()) {
+        const float* sa = reinterpret_cast<const float*>(sm + kScaleOff + spans.at * kSpanBytes) +
+                          32 * quarter + lane;
+        const float* sb = sa - 32 * quarter - lane + kSpan * kPitch + kSpan * half;
+        if (ok) ok = mm::wait(smem_addr(scaled + spans.at), spans.flip);
+        const int span = min(kSpan, p.groups - k0);
+#pragma unroll 1
+        for (int k = 0; k < span; ++k, buffer.next()) {
+          const int buf = buffer.at;
+          const float s = __fmul_rn(sa[k * kPitch], sb[k]);
+          const uint64_t s2 = f2pack(s, s);
+          if (ok) ok = mm::wait(smem_addr(sums + 2 * half + buf), buffer.flip);
+          umma::fence_after_sync();
+          // 16 columns are on their way while 16 are added
+          float t[2][16];
+          umma::ld16(at + buf * kHalfN, t[0]);
+#pragma unroll
+          for (int j = 0; j < kCols / 16; ++j) {
+            umma::wait_ld();
+            if (j < kCols / 16 - 1) {
+              umma::ld16(at + buf * kHalfN + 16 * (j + 1), t[(j + 1) & 1]);
+            } else {
+              umma::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) arrive_remote(free_bar + 8 * buf);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              add_scaled(acc[8 * j + c], t[j & 1][2 * c], t[j & 1][2 * c + 1], s2);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(used + spans.at));
+      }
       int tm, tn;
       walk.at(i, &tm, &tn);
       const int m0 = tm * kTile + 128 * static_cast<int>(rank) + 32 * quarter;
-      const int n0 = tn * kTile + 128 * half;
-      const bool live = n0 < p.n;
-      const float* sb = p.b_scale + static_cast<long long>(live ? n0 / kScaleGroup : 0) * p.groups;
-      uint64_t acc[64];
-#pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0;
-      for (int k = 0; k < p.groups; ++k, buffer.next()) {
-        if (k % kSpan == 0) {
-          // sa sb of the warp's 32 rows and the next 32 groups: fetched with a lane per
-          // group, read with a lane per row; (row, group) at 32 row + (group ^ row)
-          const int g = k + lane;
-          const float b = g < p.groups ? sb[g] : 0.f;
-          __syncwarp();
-#pragma unroll 8
-          for (int r = 0; r < 32; ++r) {
-            const float a = m0 + r < p.m && g < p.groups
-                                ? p.a_scale[static_cast<long long>(m0 + r) * p.groups + g] : 0.f;
-            mine[32 * r + (lane ^ r)] = __fmul_rn(a, b);
-          }
-          __syncwarp();
-        }
-        const int buf = buffer.at;
-        const float s = mine[32 * lane + ((k % kSpan) ^ lane)];
-        const uint64_t s2 = f2pack(s, s);
-        if (ok) ok = mm::wait(smem_addr(sums + buf), buffer.flip);
-        umma::fence_after_sync();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float t[32];
-          umma::ld32(at + buf * kTile + 32 * j, t);
-          umma::wait_ld();
-          if (j == 3) {
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) arrive_remote(free_bar[buf]);
-          }
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            add_scaled(acc[16 * j + c], t[2 * c], t[2 * c + 1], s2);
-        }
-      }
-      // ---- the warp's 32 rows, 128 bytes at a time through its shared memory
+      const int n0 = tn * kTile + first;
+      // ---- the warp's 32 rows, 32 bytes at a time through its shared memory
       __syncwarp();
       constexpr int kElem = kOut == KVP_F32 ? 4 : 2;
-      constexpr int kCols = 128 / kElem;           // columns of a piece
+      constexpr int kPiece = 32 / kElem;           // columns of a piece
       const bool wide = p.out_stride * kElem % 16 == 0 &&
                         (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
-      uint4* piece = reinterpret_cast<uint4*>(mine);
       // unrolled: acc is indexed by constants
 #pragma unroll
-      for (int c0 = 0; c0 < 128; c0 += kCols) {
+      for (int c0 = 0; c0 < kCols; c0 += kPiece) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {              // 16 bytes of this lane's row
+        for (int q = 0; q < 2; ++q) {              // 16 bytes of this lane's row
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -271,31 +324,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) w[e] = 0;
           }
-          piece[8 * lane + (q ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+          piece[2 * lane + (q ^ (lane >> 2 & 1))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
         const int n = n0 + c0;
-        if (wide && n + kCols <= p.n) {
+        if (wide && n + kPiece <= p.n) {
 #pragma unroll
-          for (int r = 0; r < 32; r += 4) {
-            const int row = r + lane / 8, q = lane & 7;
-            const uint4 v = piece[8 * row + (q ^ (row & 7))];
+          for (int r = 0; r < 32; r += 16) {
+            const int row = r + lane / 2, q = lane & 1;
+            const uint4 v = piece[2 * row + (q ^ (row >> 2 & 1))];
             if (m0 + row < p.m)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
                                         ((m0 + row) * p.out_stride + n) * kElem + 16 * q) = v;
           }
-        } else {
+        } else if (lane < kPiece && n + lane < p.n) {
+          const int q = lane * kElem / 16;
           for (int r = 0; r < 32 && m0 + r < p.m; ++r) {
-            for (int c = lane; c < kCols && n + c < p.n; c += 32) {
-              const int q = c * kElem / 16;
-              const void* from = reinterpret_cast<const uint8_t*>(piece) +
-                                 16 * (8 * r + (q ^ (r & 7))) + c * kElem % 16;
-              const long long to = (m0 + r) * p.out_stride + n + c;
-              if constexpr (kOut == KVP_F32)
-                static_cast<float*>(p.out)[to] = *static_cast<const float*>(from);
-              else
-                static_cast<uint16_t*>(p.out)[to] = *static_cast<const uint16_t*>(from);
-            }
+            const void* from = reinterpret_cast<const uint8_t*>(piece) +
+                               16 * (2 * r + (q ^ (r >> 2 & 1))) + lane * kElem % 16;
+            const long long to = (m0 + r) * p.out_stride + n + lane;
+            if constexpr (kOut == KVP_F32)
+              static_cast<float*>(p.out)[to] = *static_cast<const float*>(from);
+            else
+              static_cast<uint16_t*>(p.out)[to] = *static_cast<const uint16_t*>(from);
           }
         }
         __syncwarp();

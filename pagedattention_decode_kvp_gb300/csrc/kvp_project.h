@@ -49,12 +49,14 @@ struct MatmulPlan {
   int tokens;                 // rows of a per tile (256: pairs of CTAs)
   int splits;                 // CTAs that share a tile's K
   int box() const { return tokens < 128 ? tokens : 128; }   // rows of a per copy
+  int box_b() const { return tokens == 256 ? 64 : 128; }    // rows of b
 };
 MatmulPlan matmul_plan(int m, int n, int groups);
 
 cudaError_t launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_quantise_fp8(const QuantiseParams& p, bool bf16, cudaStream_t s);
-// ta, tb: K-major maps of a and b with boxes of 128 bytes x plan.box() (a) and 128 (b) rows.
+// ta, tb: K-major maps of a and b with boxes of 128 bytes x plan.box() (a) and plan.box_b()
+// (b) rows.
 cudaError_t launch_matmul_fp8(const MatmulParams& p, const MatmulPlan& plan, const CUtensorMap& ta,
                               const CUtensorMap& tb, cudaStream_t s);
 cudaError_t launch_matmul_fp8_pair(const MatmulParams& p, const CUtensorMap& ta,
