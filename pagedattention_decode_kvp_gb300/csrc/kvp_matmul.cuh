@@ -54,6 +54,20 @@ __device__ __forceinline__ bool wait_both(uint32_t bar, uint32_t parity, uint32_
   return wait(bar, parity) && wait(bar2, parity2);
 }
 
+// A ring's place and how often it has wrapped (mod 2): what is waited for is the phase
+// `flip` of a full place, and `flip ^ 1` of a free one (a new barrier's passes).
+template <int kPlaces>
+struct Ring {
+  int at = 0;
+  uint32_t flip = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kPlaces) {
+      at = 0;
+      flip ^= 1;
+    }
+  }
+};
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -75,10 +89,31 @@ __device__ __forceinline__ uint32_t load_remote(uint32_t there) {
   return v;
 }
 
+__device__ __forceinline__ float4 load_remote4(uint32_t there) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(there)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void store_out(const MatmulParams& p, long long at, float v) {
   if (p.out_type == KVP_F32) static_cast<float*>(p.out)[at] = v;
   else if (p.out_type == KVP_BF16) static_cast<uint16_t*>(p.out)[at] = dev::from_float<true>(v);
   else static_cast<uint16_t*>(p.out)[at] = dev::from_float<false>(v);
+}
+
+// Four neighbouring results of a row that starts on 4 elements.
+__device__ __forceinline__ void store_out4(const MatmulParams& p, long long at, float4 v) {
+  if (p.out_type == KVP_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+  } else {
+    const bool bf = p.out_type == KVP_BF16;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+        make_uint2(bf ? dev::pack2<true>(v.x, v.y) : dev::pack2<false>(v.x, v.y),
+                   bf ? dev::pack2<true>(v.z, v.w) : dev::pack2<false>(v.z, v.w));
+  }
 }
 
 }  // namespace mm

@@ -6,12 +6,15 @@
 // scales differ from group to group, so every group's sum is read into registers and
 // added there in float32: acc = fma(t, sa sb, acc).
 //
-// The weight's 128 rows are the M side of the instruction (a TMEM lane and a thread
-// each), kTokens rows of A its N side.  Warps: four that scale and add, one that
-// fetches tiles of 128 bytes of K by TMA, one that issues the products; two TMEM
-// buffers, so that a group is scaled while the next is multiplied.  Where few tiles
+// Here for few rows of A: the weight's 128 rows are the M side of the instruction (a
+// TMEM lane and a thread each), kTokens rows of A its N side.  Bound by the weight's
+// bytes, which a ring of TMA copies keeps on the way.  Warps: four that scale and add,
+// one each that fetches tiles, issues products and stages scales.  The products of kBatch
+// groups are handed over at a time, in one of two TMEM buffers: a hand-over takes about
+// 1000 cycles (two barriers, the read), more than the bytes of a group.  Where few tiles
 // meet many SMs, the CTAs of a cluster share a tile's K and add their sums through
-// distributed shared memory, in the order of their ranks.
+// distributed shared memory, in the order of their ranks.  (kvp_matmul_fp8_pair.cu: many
+// rows.)
 #include "kvp_matmul.cuh"
 
 namespace kvp {
@@ -20,40 +23,50 @@ namespace {
 
 constexpr int kRowsB = 128;                  // weight rows of a tile
 constexpr uint32_t kTileB = kRowsB * 128;    // bytes of a stage's weight tile
-constexpr int kThreads = 192;
-constexpr int kAddWarps = 4;
-constexpr int kScaleSpan = 32;               // groups whose scales are staged at a time
+constexpr int kMaxSplits = 8;                // CTAs of a portable cluster
+constexpr int kSpan = 16;                    // groups whose scales are staged at a time
+constexpr int kSpans = 2;
 
 template <int kTokens>
 struct Shape {
+  static constexpr int kCols = kTokens < 32 ? kTokens : 32;   // tokens of an adding thread
+  static constexpr int kAddWarps = 4 * kTokens / kCols;
+  static constexpr int kThreads = (kAddWarps + 3) * 32;
   static constexpr uint32_t kTileA = kTokens * 128;
   static constexpr uint32_t kStage = kTileB + kTileA;
-  // two CTAs per SM up to 64 tokens; at 128 the sums take the registers of one
+  // two CTAs per SM up to 64 tokens
   static constexpr int kCtas = kTokens <= 64 ? 2 : 1;
   static constexpr int kStages = kTokens <= 64 ? 98304 / kStage : 6;
+  static constexpr int kBatch = kTokens == 16 ? 8 : kTokens == 32 ? 4 : 2;
+  static constexpr int kPitch = kTokens + 4;  // floats from one group's scales to the next's
   static constexpr uint32_t kScaleOff = kStages * kStage;
-  static constexpr uint32_t kBarOff = kScaleOff + kTokens * kScaleSpan * 4;
-  static constexpr uint32_t kSmem = 1024 + kBarOff + (2 * kStages + 5) * 8 + 16;
-  static constexpr uint32_t kTmem = 2 * kTokens < 32 ? 32 : 2 * kTokens;
+  static constexpr uint32_t kBarOff = kScaleOff + kSpans * kSpan * kPitch * 4;
+  static constexpr uint32_t kSmem = 1024 + kBarOff + (2 * kStages + 5 + 2 * kSpans) * 8 + 16;
+  static constexpr uint32_t kTmem = 2 * kBatch * kTokens;
+  static_assert(kSmem * kCtas <= (kCtas == 2 ? 226 : 227) * 1024, "shared memory of an SM");
+  static_assert(kTmem * kCtas <= 512 && kSpan % kBatch == 0, "TMEM, spans of whole batches");
   static_assert(kStages * kStage >= kTokens * kRowsB * 4, "the sums are exchanged in the ring");
 };
 
 // grid.x = (token tile, weight tile, rank of the cluster), the last running fastest.
 template <int kTokens>
-__global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
+__global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCtas)
     matmul_fp8_kernel(const MatmulParams p, int splits, const __grid_constant__ CUtensorMap ta,
                       const __grid_constant__ CUtensorMap tb) {
   using namespace dev;
   using S = Shape<kTokens>;
+  constexpr int kAddWarps = S::kAddWarps;
   constexpr uint32_t kInstr = umma::instr_desc_f16(kRowsB, kTokens, false, false, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
-  float* scales = reinterpret_cast<float*>(sm + S::kScaleOff);   // [kScaleSpan][kTokens]
+  float* scales = reinterpret_cast<float*>(sm + S::kScaleOff);   // [kSpans][kSpan][kPitch]
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kBarOff);
   uint64_t* empty = full + S::kStages;
-  uint64_t* sums = empty + S::kStages;     // [2] a TMEM buffer holds a group's sums
+  uint64_t* sums = empty + S::kStages;     // [2] a TMEM buffer holds a batch's sums
   uint64_t* taken = sums + 2;              // [2] they are in registers
-  uint64_t* done = taken + 2;              // every product of the CTA complete
+  uint64_t* scaled = taken + 2;            // [kSpans] scales are there
+  uint64_t* used = scaled + kSpans;        // [kSpans] they have been read
+  uint64_t* done = used + kSpans;          // every product of the CTA complete
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ int failed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -74,11 +87,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
       mbar_init(smem_addr(sums + i), 1);
       mbar_init(smem_addr(taken + i), kAddWarps);
     }
+    for (int i = 0; i < kSpans; ++i) {
+      mbar_init(smem_addr(scaled + i), 1);
+      mbar_init(smem_addr(used + i), kAddWarps);
+    }
     mbar_init(smem_addr(done), 1);
     prefetch_tensormap(&ta);
     prefetch_tensormap(&tb);
     fence_barrier_init();
   }
+  // (as many columns as all resident CTAs together find: no CTA waits for another's)
   if (warp == kAddWarps + 1) umma::alloc(smem_addr(tslot), S::kTmem);
   umma::fence_before_sync();
   __syncthreads();
@@ -89,12 +107,12 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
   bool ok = true;
   if (warp == kAddWarps) {
     // ---- fetch: a stage is free again once its products are complete
+    mm::Ring<S::kStages> ring;
     int fetched = 0;
-    for (int k = 0; k < count && ok; ++k) {
-      const int st = k % S::kStages;
-      if (k >= S::kStages) ok = mbar_wait_bounded(smem_addr(empty + st), (k / S::kStages - 1) & 1);
+    for (int k = 0; k < count && ok; ++k, ring.next()) {
+      ok = mm::wait(smem_addr(empty + ring.at), ring.flip ^ 1);
       if (ok && elect_one()) {
-        const uint32_t bar = smem_addr(full + st), at = smem_addr(sm + st * S::kStage);
+        const uint32_t bar = smem_addr(full + ring.at), at = smem_addr(sm + ring.at * S::kStage);
         mbar_arrive_expect_tx(bar, S::kStage);
         tma_load_2d(at, &tb, (first + k) * 128, n0, bar);
         tma_load_2d(at + kTileB, &ta, (first + k) * 128, m0, bar);
@@ -104,68 +122,106 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
     }
     // no copy may land after the exit
     for (int k = max(0, fetched - S::kStages); k < fetched; ++k)
-      ok = mbar_wait_bounded(smem_addr(full + k % S::kStages), (k / S::kStages) & 1) && ok;
+      ok = mm::wait(smem_addr(full + k % S::kStages), (k / S::kStages) & 1) && ok;
   } else if (warp == kAddWarps + 1) {
-    // ---- products: 4 x K = 32 of a stage into TMEM buffer k % 2
-    for (int k = 0; k < count && ok; ++k) {
-      const int st = k % S::kStages, buf = k & 1;
-      ok = mbar_wait_bounded(smem_addr(full + st), (k / S::kStages) & 1);
-      if (ok && k >= 2) ok = mbar_wait_bounded(smem_addr(taken + buf), (k / 2 - 1) & 1);
+    // ---- products: 4 x K = 32 of a stage for a group, kBatch groups to a TMEM buffer
+    mm::Ring<S::kStages> ring;
+    mm::Ring<2> buffer;
+    for (int k = 0; k < count && ok; ++k, ring.next()) {
+      const int in = k % S::kBatch;
+      const bool last = in == S::kBatch - 1 || k == count - 1;
+      if (in == 0)
+        ok = mm::wait_both(smem_addr(full + ring.at), ring.flip, smem_addr(taken + buffer.at),
+                           buffer.flip ^ 1);
+      else
+        ok = mm::wait(smem_addr(full + ring.at), ring.flip);
       umma::fence_after_sync();
       if (ok && elect_one()) {
-        const uint32_t at = smem_addr(sm + st * S::kStage);
+        const uint32_t at = smem_addr(sm + ring.at * S::kStage);
         const uint64_t b = umma::smem_desc_sw128(at, 16, 1024);
         const uint64_t a = umma::smem_desc_sw128(at + kTileB, 16, 1024);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          mm::mma_f8<1>(tmem + buf * kTokens, b + 2 * s, a + 2 * s, kInstr, s > 0);
-        umma::commit(smem_addr(empty + st));
-        umma::commit(smem_addr(sums + buf));
+          mm::mma_f8<1>(tmem + (buffer.at * S::kBatch + in) * kTokens, b + 2 * s, a + 2 * s, kInstr,
+                        s > 0);
+        umma::commit(smem_addr(empty + ring.at));
+        if (last) umma::commit(smem_addr(sums + buffer.at));
       }
       __syncwarp();
+      if (last) buffer.next();
     }
     if (elect_one()) umma::commit(smem_addr(done));
     __syncwarp();
-    ok = mbar_wait_bounded(smem_addr(done), 0) && ok;
+    ok = mm::wait(smem_addr(done), 0) && ok;
+  } else if (warp == kAddWarps + 2) {
+    // ---- scales sa sb of the tile, spans of 16 groups, 16 lanes to a token
+    mm::Ring<kSpans> ring;
+    const float* sb = p.b_scale + static_cast<long long>(n0 / kScaleGroup) * p.groups + first;
+    for (int k = 0; k < count && ok; k += kSpan, ring.next()) {
+      float* to = scales + (ring.at * kSpan + lane % kSpan) * S::kPitch + lane / kSpan;
+      const int g = k + lane % kSpan;
+      const float b = g < count ? sb[g] : 0.f;
+      const float* sa = p.a_scale + first + g;
+      constexpr int kLoads = kTokens / 2 < 16 ? kTokens / 2 : 16;   // on the way at a time
+#pragma unroll 1
+      for (int t = 0; t < kTokens; t += 2 * kLoads) {
+        float v[kLoads];
+#pragma unroll
+        for (int r = 0; r < kLoads; ++r) {
+          const long long m = m0 + t + 2 * r + lane / kSpan;
+          v[r] = g < count && m < p.m ? sa[m * p.groups] : 0.f;
+        }
+        if (t == 0) ok = mm::wait(smem_addr(used + ring.at), ring.flip ^ 1);
+#pragma unroll
+        for (int r = 0; r < kLoads; ++r) to[t + 2 * r] = __fmul_rn(v[r], b);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(scaled + ring.at));
+    }
   }
 
-  uint64_t acc[kTokens / 2];   // token pairs of this thread's weight row
+  // ---- scale and add: weight row `row` and tokens col .. col + kCols - 1
+  constexpr int kCols = S::kCols;
+  const int row = tid % kRowsB, col = warp / 4 * kCols;
+  uint64_t acc[kCols / 2];
   if (warp < kAddWarps) {
 #pragma unroll
-    for (int j = 0; j < kTokens / 2; ++j) acc[j] = 0;
-    const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    for (int k = 0; k < count; ++k) {
-      if (k % kScaleSpan == 0) {
-        // sa sb of the next groups, [group][token]; a thread takes one token's groups
-        constexpr int kPer = kAddWarps * 32 / kTokens;
-        if (k > 0) named_bar_sync(1, kAddWarps * 32);
-        const int m = m0 + tid % kTokens;
-        const int span = min(kScaleSpan, count - k);
-        const float* sb = p.b_scale + static_cast<long long>(n0 / kScaleGroup) * p.groups + first + k;
-        const float* sa = p.a_scale + static_cast<long long>(m) * p.groups + first + k;
-        for (int g = tid / kTokens; g < span; g += kPer)
-          scales[g * kTokens + tid % kTokens] = m < p.m ? __fmul_rn(sa[g], sb[g]) : 0.f;
-        named_bar_sync(1, kAddWarps * 32);
-      }
-      const int buf = k & 1;
-      if (ok) ok = mbar_wait_bounded(smem_addr(sums + buf), (k >> 1) & 1);
+    for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
+    const uint32_t at = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + col;
+    mm::Ring<2> buffer;
+    mm::Ring<kSpans> spans;
+    for (int k0 = 0; k0 < count; k0 += S::kBatch, buffer.next()) {
+      if (k0 % kSpan == 0 && ok) ok = mm::wait(smem_addr(scaled + spans.at), spans.flip);
+      const float* sc = scales + (spans.at * kSpan + k0 % kSpan) * S::kPitch + col;
+      if (ok) ok = mm::wait(smem_addr(sums + buffer.at), buffer.flip);
       umma::fence_after_sync();
-      const float* sc = scales + (k % kScaleSpan) * kTokens;
+      const int batch = min(S::kBatch, count - k0);
+#pragma unroll 1
+      for (int g = 0; g < batch; ++g) {
 #pragma unroll
-      for (int j = 0; j < kTokens; j += 16) {
-        float t[16];
-        umma::ld16(at + buf * kTokens + j, t);
-        umma::wait_ld();
+        for (int j = 0; j < kCols; j += 16) {
+          float t[16];
+          umma::ld16(at + (buffer.at * S::kBatch + g) * kTokens + j, t);
+          ulonglong2 s2[4];
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const ulonglong2 s2 = *reinterpret_cast<const ulonglong2*>(sc + j + i);
-          acc[(j + i) / 2] = ffma2(f2pack(t[i], t[i + 1]), s2.x, acc[(j + i) / 2]);
-          acc[(j + i) / 2 + 1] = ffma2(f2pack(t[i + 2], t[i + 3]), s2.y, acc[(j + i) / 2 + 1]);
+          for (int i = 0; i < 4; ++i)
+            s2[i] = *reinterpret_cast<const ulonglong2*>(sc + g * S::kPitch + j + 4 * i);
+          umma::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = j / 2 + 2 * i;
+            acc[c] = ffma2(f2pack(t[4 * i], t[4 * i + 1]), s2[i].x, acc[c]);
+            acc[c + 1] = ffma2(f2pack(t[4 * i + 2], t[4 * i + 3]), s2[i].y, acc[c + 1]);
+          }
         }
       }
       umma::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(taken + buf));
+      if (lane == 0) mbar_arrive(smem_addr(taken + buffer.at));
+      if ((k0 + S::kBatch) % kSpan == 0) {
+        if (lane == 0) mbar_arrive(smem_addr(used + spans.at));
+        spans.next();
+      }
     }
   }
   if (!ok) atomicExch(&failed, 1);
@@ -176,14 +232,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
   bool bad = failed != 0;
   if (bad && tid == 0) set_status(p.status, kErrTimeout);
 
-  const int n = n0 + tid;
+  const int n = n0 + row;
   if (splits == 1) {
     if (warp >= kAddWarps || n >= p.n) return;
 #pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
+    for (int j = 0; j < kCols; ++j) {
       const float2 v = f2unpack(acc[j / 2]);
-      if (m0 + j < p.m)
-        mm::store_out(p, static_cast<long long>(m0 + j) * p.out_stride + n, bad ? 0.f : j & 1 ? v.y : v.x);
+      const int m = m0 + col + j;
+      if (m < p.m)
+        mm::store_out(p, static_cast<long long>(m) * p.out_stride + n, bad ? 0.f : j & 1 ? v.y : v.x);
     }
     return;
   }
@@ -191,20 +248,55 @@ __global__ void __launch_bounds__(kThreads, Shape<kTokens>::kCtas)
   float* mine = reinterpret_cast<float*>(sm);   // [kTokens][128]
   if (warp < kAddWarps) {
 #pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
+    for (int j = 0; j < kCols; ++j) {
       const float2 v = f2unpack(acc[j / 2]);
-      mine[j * kRowsB + tid] = j & 1 ? v.y : v.x;
+      mine[(col + j) * kRowsB + row] = j & 1 ? v.y : v.x;
     }
   }
   mm::cluster_sync();
-  for (int r = 0; r < splits; ++r) bad = mm::load_remote(mm::at_rank(smem_addr(&failed), r)) != 0 || bad;
-  if (warp < kAddWarps && n < p.n) {
+  for (int r = 0; r < splits; ++r)
+    bad = mm::load_remote(mm::at_rank(smem_addr(&failed), r)) != 0 || bad;
+  if (warp < kAddWarps) {
+    // a warp takes a token, a lane four weight rows
+    constexpr int kAtOnce = 2;
     const int end = min(static_cast<int>(kTokens * (rank + 1) / splits), p.m - m0);
-    for (int j = kTokens * rank / splits; j < end; ++j) {
-      float v = 0.f;
-      for (int r = 0; r < splits; ++r)
-        v += __uint_as_float(mm::load_remote(mm::at_rank(smem_addr(mine + j * kRowsB + tid), r)));
-      mm::store_out(p, static_cast<long long>(m0 + j) * p.out_stride + n, bad ? 0.f : v);
+    const int n4 = n0 + 4 * lane;
+    const bool whole = n4 + 4 <= p.n && p.out_stride % 4 == 0 &&
+                       reinterpret_cast<uintptr_t>(p.out) % (p.out_type == KVP_F32 ? 16 : 8) == 0;
+    for (int j0 = kTokens * rank / splits + warp; j0 < end; j0 += kAddWarps * kAtOnce) {
+      float4 v[kAtOnce][kMaxSplits];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          if (r < splits && j0 + u * kAddWarps < end)
+            v[u][r] = mm::load_remote4(
+                mm::at_rank(smem_addr(mine + (j0 + u * kAddWarps) * kRowsB + 4 * lane), r));
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int j = j0 + u * kAddWarps;
+        if (j >= end) continue;
+        float4 x = v[u][0];
+#pragma unroll
+        for (int r = 1; r < kMaxSplits; ++r) {
+          if (r < splits) {
+            x.x += v[u][r].x;
+            x.y += v[u][r].y;
+            x.z += v[u][r].z;
+            x.w += v[u][r].w;
+          }
+        }
+        if (bad) x = make_float4(0.f, 0.f, 0.f, 0.f);
+        const long long at = static_cast<long long>(m0 + j) * p.out_stride + n4;
+        if (whole) {
+          mm::store_out4(p, at, x);
+        } else {
+          const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n4 + i < p.n) mm::store_out(p, at + i, y[i]);
+        }
+      }
     }
   }
   mm::cluster_sync();
@@ -221,7 +313,7 @@ cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, con
                           ((p.m + kTokens - 1) / kTokens);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -240,17 +332,18 @@ cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, con
 
 MatmulPlan matmul_plan(int m, int n, int groups) {
   MatmulPlan plan;
-  plan.tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  const long long tiles = static_cast<long long>((n + kRowsB - 1) / kRowsB) *
-                          ((m + plan.tokens - 1) / plan.tokens);
   plan.splits = 1;
   // pairs where their tiles are enough for the SMs
   if (m > 128 && static_cast<long long>((m + 255) / 256) * ((n + 255) / 256) >= kNumSms / 2) {
     plan.tokens = 256;
     return plan;
   }
-  while (plan.splits < 8 && tiles * plan.splits * 2 <= 304 && plan.splits * 4 <= groups)
-    plan.splits *= 2;
+  plan.tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  const long long tiles = static_cast<long long>((n + kRowsB - 1) / kRowsB) *
+                          ((m + plan.tokens - 1) / plan.tokens);
+  const int slots = kNumSms * (plan.tokens <= 64 ? 2 : 1);
+  while (plan.splits < kMaxSplits && tiles * (plan.splits + 1) <= slots && (plan.splits + 1) * 2 <= groups)
+    ++plan.splits;
   return plan;
 }
 

@@ -98,20 +98,6 @@ struct Walk {
   }
 };
 
-// A ring's place and how often it has wrapped (mod 2): what is waited for is the phase
-// `flip` of a full place, and `flip ^ 1` of a free one (a new barrier's passes).
-template <int kPlaces>
-struct Ring {
-  int at = 0;
-  uint32_t flip = 0;
-  __device__ __forceinline__ void next() {
-    if (++at == kPlaces) {
-      at = 0;
-      flip ^= 1;
-    }
-  }
-};
-
 template <int kOut>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_fp8_pair_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap ta,
@@ -166,7 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kAddWarps) {
       // ---- fetch this CTA's halves; the first CTA expects the bytes of both
-      Ring<kStages> ring;
+      mm::Ring<kStages> ring;
       for (long long i = pair; i < tiles && ok; i += pairs) {
         int tm, tn;
         walk.at(i, &tm, &tn);
@@ -191,8 +177,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- products of the pair: a warp for each half of the columns (one warp's waits and
       // issues took 960 cycles a group, the products take 512)
       const int h = warp - (kAddWarps + 1);
-      Ring<kStages> ring;
-      Ring<2> buffer;
+      mm::Ring<kStages> ring;
+      mm::Ring<2> buffer;
       for (long long i = pair; i < tiles && ok; i += pairs) {
         for (int k = 0; k < p.groups && ok; ++k, ring.next(), buffer.next()) {
           const int st = ring.at, buf = 2 * h + buffer.at;
@@ -218,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == kAddWarps + 3) {
       // ---- scales of the CTA's 128 rows and of the tile's two halves, spans of 8 groups: 8
       // lanes take a row's, so that its 32 bytes are one sector
-      Ring<kSpans> ring;
+      mm::Ring<kSpans> ring;
       for (long long i = pair; i < tiles && ok; i += pairs) {
         int tm, tn;
         walk.at(i, &tm, &tn);
@@ -257,8 +243,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         first % kHalfN;
     uint4* piece = reinterpret_cast<uint4*>(sm + kWarpOff + warp * kWarpBytes);
     const uint32_t free_bar = mm::at_rank(smem_addr(taken + 2 * half), 0);
-    Ring<2> buffer;
-    Ring<kSpans> spans;
+    mm::Ring<2> buffer;
+    mm::Ring<kSpans> spans;
     for (long long i = pair; i < tiles; i += pairs) {
       uint64_t acc[kCols / 2];
 #pragma unroll
