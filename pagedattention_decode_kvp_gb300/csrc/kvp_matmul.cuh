@@ -83,10 +83,8 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
   return there;
 }
-__device__ __forceinline__ uint32_t load_remote(uint32_t there) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
-  return v;
+__device__ __forceinline__ void store_remote(uint32_t there, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ float4 load_remote4(uint32_t there) {

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
   uint64_t* used = scaled + kSpans;        // [kSpans] they have been read
   uint64_t* done = used + kSpans;          // every product of the CTA complete
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
-  __shared__ int failed;
+  __shared__ volatile int failed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = splits > 1 ? mm::cluster_rank() : 0;
   const long long tile = blockIdx.x / splits;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
       }
     }
   }
-  if (!ok) atomicExch(&failed, 1);
+  if (!ok) failed = 1;
   umma::fence_before_sync();
   __syncthreads();
   launch_dependents();
@@ -253,12 +253,12 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
       mine[(col + j) * kRowsB + row] = j & 1 ? v.y : v.x;
     }
   }
+  if (bad && tid < splits) mm::store_remote(mm::at_rank(smem_addr(const_cast<int*>(&failed)), tid), 1);
   mm::cluster_sync();
-  for (int r = 0; r < splits; ++r)
-    bad = mm::load_remote(mm::at_rank(smem_addr(&failed), r)) != 0 || bad;
+  bad = failed != 0;
   if (warp < kAddWarps) {
     // a warp takes a token, a lane four weight rows
-    constexpr int kAtOnce = 2;
+    constexpr int kAtOnce = kTokens == 64 ? 1 : 2;   // (registers)
     const int end = min(static_cast<int>(kTokens * (rank + 1) / splits), p.m - m0);
     const int n4 = n0 + 4 * lane;
     const bool whole = n4 + 4 <= p.n && p.out_stride % 4 == 0 &&
@@ -330,20 +330,39 @@ cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, con
 
 }  // namespace
 
+// The plan with the least time by a model of what was measured, in us: 2.6 for the start of a
+// wave of CTAs (pairs: 3.5 once), a group of a CTA by its tokens and by whether its SM holds another CTA, the
+// exchange of a cluster's sums, and the bytes of a and b at the rate of HBM.  Measured and
+// modelled (tokens x splits): 1 x 4096 x 4096 16x1 11.1 and 11.2, 16x4 6.9 and 6.8; 64 x 4096
+// x 4096 32x4 8.4 and 8.5, 64x4 9.4 and 9.2, 64x1 16.8 and 16.4; 64 x 10240 x 8192 64x3 21.9
+// and 23.4, 64x1 29.9 and 30.1; 256 x 4096 x 4096 128x2 14.7 and 13.8, pairs 20.8 and 20.5;
+// 517 x 4096 x 4096 128x1 34.4 and 36.5, pairs 21.0 and 20.5.
 MatmulPlan matmul_plan(int m, int n, int groups) {
-  MatmulPlan plan;
-  plan.splits = 1;
-  // pairs where their tiles are enough for the SMs
-  if (m > 128 && static_cast<long long>((m + 255) / 256) * ((n + 255) / 256) >= kNumSms / 2) {
-    plan.tokens = 256;
-    return plan;
+  struct Kind {
+    int tokens, resident;      // rows of a per tile, CTAs of an SM
+    double alone, shared;      // us a group
+  };
+  constexpr Kind kKinds[] = {{16, 2, 0.27, 0.33}, {32, 2, 0.30, 0.44}, {64, 2, 0.43, 0.83},
+                             {128, 1, 0.53, 0.53}};
+  const auto tiles = [](long long x, int per) { return (x + per - 1) / per; };
+  MatmulPlan plan{256, 1};
+  double best = 3.5 + 0.53 * groups * tiles(tiles(m, 256) * tiles(n, 256), kNumSms / 2);
+  const double bytes = 2.6 + (static_cast<double>(m) + n) * groups * 128 / 6.5e6;
+  for (const Kind& k : kKinds) {
+    if (k.tokens >= 2 * m && k.tokens > 16) break;   // (a smaller one holds all rows)
+    for (int splits = 1; splits <= kMaxSplits && (splits == 1 || 2 * splits <= groups); ++splits) {
+      const long long ctas = tiles(m, k.tokens) * tiles(n, kRowsB) * splits;
+      const double waves = static_cast<double>(tiles(ctas, kNumSms * k.resident));
+      if (splits > 1 && waves > 1) break;
+      double t = waves * (2.6 + tiles(groups, splits) * (ctas > kNumSms ? k.shared : k.alone));
+      if (splits > 1) t += 0.8 + 0.2 * splits + 0.006 * k.tokens * splits;
+      if (t < bytes) t = bytes + (splits > 1 ? 0.1 * splits : 0.0);
+      if (t < best) {
+        best = t;
+        plan = MatmulPlan{k.tokens, splits};
+      }
+    }
   }
-  plan.tokens = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  const long long tiles = static_cast<long long>((n + kRowsB - 1) / kRowsB) *
-                          ((m + plan.tokens - 1) / plan.tokens);
-  const int slots = kNumSms * (plan.tokens <= 64 ? 2 : 1);
-  while (plan.splits < kMaxSplits && tiles * (plan.splits + 1) <= slots && (plan.splits + 1) * 2 <= groups)
-    ++plan.splits;
   return plan;
 }
 
