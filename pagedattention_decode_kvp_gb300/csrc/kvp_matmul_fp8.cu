@@ -342,6 +342,10 @@ MatmulPlan matmul_plan(int m, int n, int groups) {
     int tokens, resident;      // rows of a per tile, CTAs of an SM
     double alone, shared;      // us a group
   };
+  // clusters of 1 .. 8 CTAs that the GPU holds at a time, by the CTAs of an SM (its GPCs
+  // have no multiple of most sizes: 48 clusters of 3, one CTA to an SM, take two waves)
+  constexpr int kFit[2][kMaxSplits] = {{152, 76, 46, 36, 28, 23, 15, 15},
+                                       {304, 152, 97, 74, 58, 46, 38, 36}};
   constexpr Kind kKinds[] = {{16, 2, 0.27, 0.33}, {32, 2, 0.30, 0.44}, {64, 2, 0.43, 0.83},
                              {128, 1, 0.53, 0.53}};
   const auto tiles = [](long long x, int per) { return (x + per - 1) / per; };
@@ -351,8 +355,8 @@ MatmulPlan matmul_plan(int m, int n, int groups) {
   for (const Kind& k : kKinds) {
     if (k.tokens >= 2 * m && k.tokens > 16) break;   // (a smaller one holds all rows)
     for (int splits = 1; splits <= kMaxSplits && (splits == 1 || 2 * splits <= groups); ++splits) {
-      const long long ctas = tiles(m, k.tokens) * tiles(n, kRowsB) * splits;
-      const double waves = static_cast<double>(tiles(ctas, kNumSms * k.resident));
+      const long long clusters = tiles(m, k.tokens) * tiles(n, kRowsB), ctas = clusters * splits;
+      const double waves = static_cast<double>(tiles(clusters, kFit[k.resident - 1][splits - 1]));
       if (splits > 1 && waves > 1) break;
       double t = waves * (2.6 + tiles(groups, splits) * (ctas > kNumSms ? k.shared : k.alone));
       if (splits > 1) t += 0.8 + 0.2 * splits + 0.006 * k.tokens * splits;

@@ -73,116 +73,146 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// kThreads threads hold a row, kChunks chunks each; up to 32 of them: several rows to a
-// CTA of 128 threads; more: a CTA to a row.
-template <bool kBf16, bool kFp8, int kThreads, int kChunks>
+// kThreads threads hold a row, kChunks chunks each; up to 32 of them: 128 / kThreads slots
+// to a CTA, kRows rows a slot, fetched together; more: a CTA to a row.
+template <bool kBf16, bool kFp8, int kThreads, int kChunks, int kRows>
 __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kernel(NormParams p) {
-  constexpr int kRows = kThreads < 128 ? 128 / kThreads : 1;   // of a CTA
+  constexpr int kSlots = kThreads < 128 ? 128 / kThreads : 1;
   constexpr int kGroupLanes = kThreads < 16 ? kThreads : 16;
   dev::grid_dependency_wait();
   dev::launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kThreads;
-  const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kThreads;
-  const long long rows = static_cast<long long>(p.num_tokens) * p.num_heads;
-  const bool in = row < rows;
-  const long long t = p.num_heads == 1 ? row : row / p.num_heads;
-  const int head = p.num_heads == 1 ? 0 : static_cast<int>(row - t * p.num_heads);
-  const long long col = static_cast<long long>(head) * p.dim;   // of the row within its token
-  uint4 raw[kChunks], other[kChunks];
+  const uint32_t rows = static_cast<uint32_t>(p.num_tokens) * static_cast<uint32_t>(p.num_heads);
+  uint4 raw[kRows][kChunks], other[kRows][kChunks];
+  bool in[kRows];
+  uint32_t t[kRows], col[kRows];   // token, and where the row lies within it
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int at = 8 * (lane + c * kThreads);
-    raw[c] = other[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && at < p.dim) {
-      raw[c] = load16(p.x + t * p.x_stride + col + at);
-      if (p.residual != nullptr) other[c] = load16(p.residual + t * p.residual_stride + at);
-    }
-  }
-  float sum = 0.f;
+  for (int j = 0; j < kRows; ++j) {
+    const uint32_t row = (blockIdx.x * kRows + j) * kSlots + threadIdx.x / kThreads;
+    in[j] = row < rows;
+    t[j] = p.num_heads == 1 ? row : row / static_cast<uint32_t>(p.num_heads);
+    col[j] = (row - t[j] * static_cast<uint32_t>(p.num_heads)) * static_cast<uint32_t>(p.dim);
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    float x[8];
-    widen<kBf16>(raw[c], x);
-    if (p.residual != nullptr) {
-      float r[8];
-      widen<kBf16>(other[c], r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] += r[i];
-      raw[c] = narrow<kBf16>(x);
-      widen<kBf16>(raw[c], x);
+    for (int c = 0; c < kChunks; ++c) {
       const int at = 8 * (lane + c * kThreads);
-      if (in && at < p.dim)
-        *reinterpret_cast<uint4*>(p.residual_out + t * p.residual_out_stride + at) = raw[c];
+      raw[j][c] = other[j][c] = make_uint4(0u, 0u, 0u, 0u);
+      if (in[j] && at < p.dim) {
+        raw[j][c] = load16(p.x + t[j] * p.x_stride + col[j] + at);
+        if (p.residual != nullptr)
+          other[j][c] = load16(p.residual + t[j] * p.residual_stride + at);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float x[8];
+      widen<kBf16>(raw[j][c], x);
+      if (p.residual != nullptr) {
+        float r[8];
+        widen<kBf16>(other[j][c], r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] += r[i];
+        raw[j][c] = narrow<kBf16>(x);
+        widen<kBf16>(raw[j][c], x);
+        const int at = 8 * (lane + c * kThreads);
+        if (in[j] && at < p.dim)
+          *reinterpret_cast<uint4*>(p.residual_out + t[j] * p.residual_out_stride + at) = raw[j][c];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-  }
+    for (int o = (kThreads < 32 ? kThreads : 32) / 2; o > 0; o >>= 1)
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (kThreads > 32) {
+      __shared__ float part[kThreads / 32];
+      if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+      __syncthreads();
+      sum = 0.f;
 #pragma unroll
-  for (int o = (kThreads < 32 ? kThreads : 32) / 2; o > 0; o >>= 1)
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if constexpr (kThreads > 32) {
-    __shared__ float part[kThreads / 32];
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
-    __syncthreads();
-    sum = 0.f;
+      for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
+    }
+    const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(p.dim)), p.eps));
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
-  }
-  const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(p.dim)), p.eps));
+    for (int c = 0; c < kChunks; ++c) {
+      const int at = 8 * (lane + c * kThreads);
+      const bool mine = in[j] && at < p.dim;
+      float x[8], w[8];
+      widen<kBf16>(raw[j][c], x);
+      widen<kBf16>(at < p.dim ? load16(p.weight + at) : make_uint4(0u, 0u, 0u, 0u), w);
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int at = 8 * (lane + c * kThreads);
-    const bool mine = in && at < p.dim;
-    float x[8], w[8];
-    widen<kBf16>(raw[c], x);
-    widen<kBf16>(mine ? load16(p.weight + at) : make_uint4(0u, 0u, 0u, 0u), w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-    if constexpr (kFp8) {
-      const float most = lanes_max<kGroupLanes>(mine ? absmax8(x) : 0.f);
-      float up;
-      const float scale = group_scale(most, &up);
-      if (mine) {
-        *reinterpret_cast<uint2*>(p.codes + t * p.codes_stride + at) = codes8(x, up);
-        if (at % kScaleGroup == 0)
-          p.scales[t * ((p.dim + kScaleGroup - 1) / kScaleGroup) + at / kScaleGroup] = scale;
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+      if constexpr (kFp8) {
+        const float most = lanes_max<kGroupLanes>(mine ? absmax8(x) : 0.f);
+        float up;
+        const float scale = group_scale(most, &up);
+        if (mine) {
+          *reinterpret_cast<uint2*>(p.codes + t[j] * p.codes_stride + at) = codes8(x, up);
+          if (at % kScaleGroup == 0)
+            p.scales[static_cast<size_t>(t[j]) * ((p.dim + kScaleGroup - 1) / kScaleGroup) +
+                     at / kScaleGroup] = scale;
+        }
+      } else if (mine) {
+        *reinterpret_cast<uint4*>(p.out + t[j] * p.out_stride + col[j] + at) = narrow<kBf16>(x);
       }
-    } else if (mine) {
-      *reinterpret_cast<uint4*>(p.out + t * p.out_stride + col + at) = narrow<kBf16>(x);
     }
   }
 }
 
-// Rows by themselves: 16 lanes take a group, kUnits groups one after the other.
-constexpr int kQuantUnits = 4;
-constexpr int kQuantSlots = 16;   // groups that a CTA of 256 threads works on at a time
+// Largest magnitude of two 16-byte chunks, by pairs of 16-bit values (exact).
 template <bool kBf16>
-__global__ void __launch_bounds__(256) quantise_rows_kernel(QuantiseParams p, int groups) {
+__device__ __forceinline__ uint32_t absmax_pair(const uint4& a, const uint4& b) {
+  using dev::absmax2;
+  return absmax2<kBf16>(absmax2<kBf16>(absmax2<kBf16>(a.x, a.y), absmax2<kBf16>(a.z, a.w)),
+                        absmax2<kBf16>(absmax2<kBf16>(b.x, b.y), absmax2<kBf16>(b.z, b.w)));
+}
+
+// Rows by themselves: 8 lanes take a group, 16 elements each, kUnits groups fetched
+// together.
+constexpr int kQuantUnits = 4;
+constexpr int kQuantSlots = 32;   // groups that a CTA of 256 threads works on at a time
+template <bool kBf16>
+__global__ void __launch_bounds__(256) quantise_rows_kernel(QuantiseParams p, uint32_t groups) {
   dev::grid_dependency_wait();
   dev::launch_dependents();
-  const int sub = threadIdx.x % 16;
-  const long long units = static_cast<long long>(p.rows) * groups;
-  const long long first =
-      static_cast<long long>(blockIdx.x) * (kQuantSlots * kQuantUnits) + threadIdx.x / 16;
-  uint4 raw[kQuantUnits];
-  long long row[kQuantUnits];
+  const int sub = threadIdx.x % 8;
+  const uint32_t units = static_cast<uint32_t>(p.rows) * groups;
+  const uint32_t first = blockIdx.x * (kQuantSlots * kQuantUnits) + threadIdx.x / 8;
+  uint4 raw[kQuantUnits][2];
+  uint32_t row[kQuantUnits];
   int at[kQuantUnits];
 #pragma unroll
   for (int j = 0; j < kQuantUnits; ++j) {
-    const long long u = first + j * kQuantSlots;
+    const uint32_t u = first + j * kQuantSlots;
     row[j] = u / groups;
-    at[j] = static_cast<int>(u - row[j] * groups) * kScaleGroup + 8 * sub;
+    at[j] = static_cast<int>(u - row[j] * groups) * kScaleGroup + 16 * sub;
     if (u >= units || at[j] >= p.cols) at[j] = -1;
-    raw[j] = at[j] >= 0 ? load16(p.x + row[j] * p.x_stride + at[j]) : make_uint4(0u, 0u, 0u, 0u);
+    raw[j][0] = raw[j][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (at[j] >= 0) {
+      const uint16_t* x = p.x + row[j] * p.x_stride + at[j];
+      raw[j][0] = load16(x);
+      raw[j][1] = load16(x + 8);
+    }
   }
 #pragma unroll
   for (int j = 0; j < kQuantUnits; ++j) {
-    float x[8], up;
-    widen<kBf16>(raw[j], x);
-    const float scale = group_scale(lanes_max<16>(absmax8(x)), &up);
+    uint32_t m = absmax_pair<kBf16>(raw[j][0], raw[j][1]);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+      m = dev::absmax2<kBf16>(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float2 two = dev::unpack2<kBf16>(m);
+    float x[8], y[8], up;
+    const float scale = group_scale(fmaxf(two.x, two.y), &up);
     if (at[j] < 0) continue;
-    *reinterpret_cast<uint2*>(p.codes + row[j] * p.codes_stride + at[j]) = codes8(x, up);
-    if (sub == 0) p.scales[row[j] * groups + at[j] / kScaleGroup] = scale;
+    widen<kBf16>(raw[j][0], x);
+    widen<kBf16>(raw[j][1], y);
+    const uint2 a = codes8(x, up), b = codes8(y, up);
+    *reinterpret_cast<uint4*>(p.codes + row[j] * p.codes_stride + at[j]) =
+        make_uint4(a.x, a.y, b.x, b.y);
+    if (sub == 0) p.scales[static_cast<size_t>(row[j]) * groups + at[j] / kScaleGroup] = scale;
   }
 }
 
@@ -195,19 +225,18 @@ __global__ void __launch_bounds__(256) quantise_blocks_kernel(QuantiseParams p, 
   const int group = blockIdx.x % groups;
   const int at = group * kScaleGroup + 8 * (threadIdx.x % 16);
   uint4 raw[8];
-  float most = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const long long row = block * kScaleGroup + threadIdx.x / 16 + 16 * j;
     raw[j] = row < p.rows && at < p.cols ? load16(p.x + row * p.x_stride + at)
                                          : make_uint4(0u, 0u, 0u, 0u);
   }
+  uint32_t m = 0u;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float x[8];
-    widen<kBf16>(raw[j], x);
-    most = fmaxf(most, absmax8(x));
-  }
+  for (int j = 0; j < 8; j += 2)
+    m = dev::absmax2<kBf16>(m, absmax_pair<kBf16>(raw[j], raw[j + 1]));
+  const float2 two = dev::unpack2<kBf16>(m);
+  float most = fmaxf(two.x, two.y);
   most = dev::warp_max(most);
   __shared__ float part[8];
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = most;
@@ -231,23 +260,23 @@ template <bool kBf16, bool kFp8>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   const long long rows = static_cast<long long>(p.num_tokens) * p.num_heads;
   const int chunks = p.dim / 8;
-#define KVP_NORM(T, C)                                                                  \
+#define KVP_NORM(T, C, R)                                                               \
   {                                                                                     \
-    constexpr int kRows = T < 128 ? 128 / T : 1;                                        \
-    return launch_pdl(rms_norm_kernel<kBf16, kFp8, T, C>,                               \
-                      dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)),          \
+    constexpr int kPer = R * (T < 128 ? 128 / T : 1);                                   \
+    return launch_pdl(rms_norm_kernel<kBf16, kFp8, T, C, R>,                            \
+                      dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),            \
                       dim3(T < 128 ? 128 : T), 0, s, p);                                \
   }
-  if (chunks <= 8) KVP_NORM(8, 1)
-  if (chunks <= 16) KVP_NORM(16, 1)
-  if (chunks <= 32) KVP_NORM(32, 1)
-  if (chunks <= 64) KVP_NORM(32, 2)
-  if (chunks <= 128) KVP_NORM(128, 1)
-  if (chunks <= 256) KVP_NORM(128, 2)
-  if (chunks <= 512) KVP_NORM(256, 2)
-  if (chunks <= 1024) KVP_NORM(512, 2)
-  if (chunks <= 2048) KVP_NORM(1024, 2)
-  if (chunks <= 4096) KVP_NORM(1024, 4)
+  if (chunks <= 8) KVP_NORM(8, 1, 4)
+  if (chunks <= 16) KVP_NORM(16, 1, 4)
+  if (chunks <= 32) KVP_NORM(32, 1, 4)
+  if (chunks <= 64) KVP_NORM(32, 2, 2)
+  if (chunks <= 128) KVP_NORM(128, 1, 1)
+  if (chunks <= 256) KVP_NORM(128, 2, 1)
+  if (chunks <= 512) KVP_NORM(256, 2, 1)
+  if (chunks <= 1024) KVP_NORM(512, 2, 1)
+  if (chunks <= 2048) KVP_NORM(1024, 2, 1)
+  if (chunks <= 4096) KVP_NORM(1024, 4, 1)
 #undef KVP_NORM
   return cudaErrorInvalidValue;
 }
@@ -266,7 +295,7 @@ cudaError_t launch_quantise_fp8(const QuantiseParams& p, bool bf16, cudaStream_t
     constexpr int kPer = kQuantSlots * kQuantUnits;
     const dim3 grid(static_cast<unsigned>((units + kPer - 1) / kPer));
     return launch_pdl(bf16 ? quantise_rows_kernel<true> : quantise_rows_kernel<false>, grid,
-                      dim3(256), 0, s, p, groups);
+                      dim3(256), 0, s, p, static_cast<uint32_t>(groups));
   }
   const long long blocks = (static_cast<long long>(p.rows) + kScaleGroup - 1) / kScaleGroup;
   const dim3 grid(static_cast<unsigned>(blocks * groups));
