@@ -4,7 +4,7 @@ Thin marshalling over the C ABI in ``include/kvp.h``: every function here has
 the C entry point's name, turns torch tensors into pointers and sizes, passes
 torch's current CUDA stream, and raises :class:`KvpError` on a non-OK status.
 All computation happens in the library's CUDA kernels; there is no fallback.
-The short entry points (4-bit cache, rotary append, tables) are called through
+The short entry points (4-bit cache, rotary append, tables, projections) are called through
 ``_lib/_kvp_calls.so``, which looks at the tensors in C++.
 If the libraries have not been built, the first call raises
 ``RuntimeError`` (build them with ``__graft_entry__.build()`` or
@@ -919,6 +919,9 @@ def kvp_rms_norm(out, x, weight, eps, *, residual=None, residual_out=None, strea
     slice of one projection's output).  h is x, or with residual [T, D] x + residual,
     rounded to the dtype and written to residual_out.  out may be x, residual_out may
     be residual."""
+    if stream is None and _made(_calls().rms_norm(out, x, weight, eps, residual, residual_out),
+                                "kvp_rms_norm"):
+        return
     lib = load_library()
     s = _on_one_device(stream, x, out, weight, residual, residual_out)
     dtype = x.dtype
@@ -938,6 +941,9 @@ def kvp_rms_norm_fp8(codes, scales, x, weight, eps, *, residual=None, residual_o
                      stream=None) -> None:
     """As kvp_rms_norm of x [T, D], the results held as E4M3 codes [T, D] (uint8 or
     float8_e4m3fn) with float32 scales [T, ceil(D / 128)]: a of kvp_matmul_fp8."""
+    if stream is None and _made(_calls().rms_norm_fp8(codes, scales, x, weight, eps, residual,
+                                                      residual_out), "kvp_rms_norm_fp8"):
+        return
     lib = load_library()
     s = _on_one_device(stream, x, codes, scales, weight, residual, residual_out)
     dtype = x.dtype
@@ -954,6 +960,9 @@ def kvp_quantise_fp8(codes, scales, x, *, block_rows=1, stream=None) -> None:
     """x [R, D] (fp16/bf16) as E4M3 codes [R, D] (uint8 or float8_e4m3fn) with float32
     scales [ceil(R / block_rows), ceil(D / 128)]: block_rows = 1 for activations, 128 for
     weights, one scale per 128 x 128 elements."""
+    if stream is None and _made(_calls().quantise_fp8(codes, scales, x, block_rows),
+                                "kvp_quantise_fp8"):
+        return
     lib = load_library()
     s = _on_one_device(stream, x, codes, scales)
     code = _dtype_code(x)
@@ -971,6 +980,9 @@ def kvp_matmul_fp8(out, a, a_scale, b, b_scale, *, status=None, stream=None) -> 
     (uint8 or float8_e4m3fn) with float32 scales a_scale [M, ceil(K / 128)] and b_scale
     [ceil(N / 128), ceil(K / 128)], as kvp_rms_norm_fp8 and kvp_quantise_fp8 write them.
     Rows may be strided (codes by multiples of 16)."""
+    if stream is None and _made(_calls().matmul_fp8(out, a, a_scale, b, b_scale, status),
+                                "kvp_matmul_fp8"):
+        return
     lib = load_library()
     s = _on_one_device(stream, out, a, a_scale, b, b_scale, status)
     torch = _torch()

@@ -358,6 +358,152 @@ PyObject* release_tables(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// t [rows, n] of `type` with contiguous rows: their stride in elements.
+bool matrix(const Tensor* t, ScalarType type, int64_t rows, int64_t n, int64_t* stride) {
+  if (t->scalar_type() != type || !shape(t, {rows, n}) || (n > 1 && t->stride(1) != 1)) return false;
+  *stride = rows > 1 ? t->stride(0) : n;
+  return true;
+}
+
+// Codes [rows, n], held as uint8 or float8_e4m3fn.
+bool codes(const Tensor* t, int64_t rows, int64_t n, int64_t* stride) {
+  return matrix(t, t->scalar_type() == ScalarType::Byte ? ScalarType::Byte : ScalarType::Float8_e4m3fn,
+                rows, n, stride);
+}
+
+int64_t groups(int64_t n) { return (n + 127) / 128; }
+
+// What both norms take behind their outputs: x, weight, eps, residual, residual_out.
+struct Norm {
+  const Tensor *x, *w, *r = nullptr, *ro = nullptr;
+  kvp_dtype dt;
+  float eps;
+  int64_t T, H = 1, D, xs, rs = 0, ros = 0;
+
+  bool take(Args& a, bool heads) {
+    if (!(x = a.any()) || !dtype_code(x, &dt) || !(w = a.whole(x->scalar_type())) || !a.real(&eps))
+      return false;
+    const ScalarType type = x->scalar_type();
+    if (heads && x->dim() == 3) {
+      T = x->size(0), H = x->size(1), D = x->size(2);
+      if (!row_stride(x, type, T, H, D, &xs)) return false;
+    } else {
+      if (x->dim() != 2) return false;
+      T = x->size(0), D = x->size(1);
+      if (!matrix(x, type, T, D, &xs)) return false;
+    }
+    if (!small(T) || !small(H) || !small(D) || !shape(w, {D})) return false;
+    const bool none = a.none();
+    if (!none && !(r = a.any())) return false;
+    if (none) return a.none();
+    return x->dim() == 2 && (ro = a.any()) && matrix(r, type, T, D, &rs) &&
+           matrix(ro, type, T, D, &ros);
+  }
+};
+
+template <class T>
+T* ptr_or_null(const Tensor* t) {
+  return t != nullptr ? ptr<T>(t) : nullptr;
+}
+
+// out, x, weight, eps, residual, residual_out
+PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&](kvp_status* s) {
+    Args a(args, n);
+    const Tensor* out = a.any();
+    Norm v;
+    int64_t os;
+    if (out == nullptr || !v.take(a, true)) return false;
+    const ScalarType type = v.x->scalar_type();
+    if (v.x->dim() == 3 ? !row_stride(out, type, v.T, v.H, v.D, &os)
+                        : !matrix(out, type, v.T, v.D, &os))
+      return false;
+    const kvp_stream_t st = a.stream();
+    const WithoutGil guard;
+    *s = kvp_rms_norm(ptr<void>(out), os, ptr<void>(v.x), v.xs, ptr_or_null<void>(v.r), v.rs,
+                      ptr_or_null<void>(v.ro), v.ros, ptr<void>(v.w), v.eps,
+                      static_cast<int32_t>(v.T), static_cast<int32_t>(v.H),
+                      static_cast<int32_t>(v.D), v.dt, st);
+    return true;
+  });
+}
+
+// codes, scales, x, weight, eps, residual, residual_out
+PyObject* rms_norm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&](kvp_status* s) {
+    Args a(args, n);
+    const Tensor* c = a.any();
+    const Tensor* sc = a.whole(ScalarType::Float);
+    Norm v;
+    int64_t cs;
+    if (c == nullptr || sc == nullptr || !v.take(a, false) || !codes(c, v.T, v.D, &cs) ||
+        !shape(sc, {v.T, groups(v.D)}))
+      return false;
+    const kvp_stream_t st = a.stream();
+    const WithoutGil guard;
+    *s = kvp_rms_norm_fp8(ptr<uint8_t>(c), cs, ptr<float>(sc), ptr<void>(v.x), v.xs,
+                          ptr_or_null<void>(v.r), v.rs, ptr_or_null<void>(v.ro), v.ros,
+                          ptr<void>(v.w), v.eps, static_cast<int32_t>(v.T),
+                          static_cast<int32_t>(v.D), v.dt, st);
+    return true;
+  });
+}
+
+// codes, scales, x, block_rows
+PyObject* quantise_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&](kvp_status* s) {
+    Args a(args, n);
+    const Tensor* c = a.any();
+    const Tensor* sc = a.whole(ScalarType::Float);
+    const Tensor* x = a.any();
+    kvp_dtype dt;
+    int32_t block;
+    int64_t xs, cs;
+    if (c == nullptr || sc == nullptr || x == nullptr || !dtype_code(x, &dt) || x->dim() != 2 ||
+        !a.number(&block) || (block != 1 && block != 128))
+      return false;
+    const int64_t R = x->size(0), D = x->size(1);
+    if (!small(R) || !small(D) || !matrix(x, x->scalar_type(), R, D, &xs) || !codes(c, R, D, &cs) ||
+        !shape(sc, {(R + block - 1) / block, groups(D)}))
+      return false;
+    const kvp_stream_t st = a.stream();
+    const WithoutGil guard;
+    *s = kvp_quantise_fp8(ptr<uint8_t>(c), cs, ptr<float>(sc), ptr<void>(x), xs,
+                          static_cast<int32_t>(R), static_cast<int32_t>(D), block, dt, st);
+    return true;
+  });
+}
+
+// out, a, a_scale, b, b_scale, status
+PyObject* matmul_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&](kvp_status* s) {
+    Args v(args, n);
+    const Tensor* out = v.any();
+    const Tensor* a = v.any();
+    const Tensor* sa = v.whole(ScalarType::Float);
+    const Tensor* b = v.any();
+    const Tensor* sb = v.whole(ScalarType::Float);
+    kvp_dtype dt = KVP_F32;
+    int32_t* status;
+    int64_t os, as, bs;
+    if (out == nullptr || a == nullptr || sa == nullptr || b == nullptr || sb == nullptr ||
+        !v.status(&status) || a->dim() != 2 || b->dim() != 2 ||
+        (out->scalar_type() != ScalarType::Float && !dtype_code(out, &dt)))
+      return false;
+    const int64_t M = a->size(0), K = a->size(1), N = b->size(0), G = groups(K);
+    if (!small(M) || !small(K) || !small(N) || !codes(a, M, K, &as) || !codes(b, N, K, &bs) ||
+        !matrix(out, out->scalar_type(), M, N, &os) || !shape(sa, {M, G}) ||
+        !shape(sb, {groups(N), G}))
+      return false;
+    const kvp_stream_t st = v.stream();
+    const WithoutGil guard;
+    *s = kvp_matmul_fp8(ptr<void>(out), os, dt, ptr<uint8_t>(a), as, ptr<float>(sa),
+                        ptr<uint8_t>(b), bs, ptr<float>(sb), static_cast<int32_t>(M),
+                        static_cast<int32_t>(N), static_cast<int32_t>(K), status, st);
+    return true;
+  });
+}
+
 #define KVP_METHOD(name, f) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {KVP_METHOD("append_int4", (&rows_int4<false>)),
@@ -367,6 +513,10 @@ PyMethodDef kMethods[] = {KVP_METHOD("append_int4", (&rows_int4<false>)),
                           KVP_METHOD("rope_append_int4", (&rope_append<true>)),
                           KVP_METHOD("extend_tables", &extend_tables),
                           KVP_METHOD("release_tables", &release_tables),
+                          KVP_METHOD("rms_norm", &rms_norm),
+                          KVP_METHOD("rms_norm_fp8", &rms_norm_fp8),
+                          KVP_METHOD("quantise_fp8", &quantise_fp8),
+                          KVP_METHOD("matmul_fp8", &matmul_fp8),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_kvp_calls", nullptr, -1, kMethods,
                        nullptr,               nullptr,      nullptr, nullptr};

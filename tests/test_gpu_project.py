@@ -446,3 +446,94 @@ def test_tensors_of_another_place_are_refused():
         kvp.kvp_rms_norm(x, x, x[0].cpu(), 1e-5)
     with pytest.raises(ValueError):
         kvp.kvp_quantise_fp8(gpu(2, 128, dtype=U8), torch.zeros(2, 1), x)
+
+
+# ------------------------------------------------------------------ the compiled way
+def arguments(dtype):
+    """Arguments of every entry point, in the order of the compiled functions."""
+    T, D, N = 5, 272, 130
+    x, r = randn((T, D), dtype, 1).cuda(), randn((T, D), dtype, 2).cuda()
+    out, total, w = gpu(T, D, dtype=dtype), gpu(T, D, dtype=dtype), weight(D, dtype, 3).cuda()
+    codes, scales = gpu(T, D, dtype=U8), gpu(T, 3, dtype=F32)
+    a, sa, b, sb = (t.cuda() for t in operands(T, N, D, 4))
+    status = gpu(1, dtype=torch.int32)
+    return {"rms_norm": [out, x, w, 1e-5, r, total],
+            "rms_norm_fp8": [codes, scales, x, w, 1e-5, r, total],
+            "quantise_fp8": [codes, scales, x, 1],
+            "matmul_fp8": [gpu(T, N, dtype=dtype), a, sa, b, sb, status]}
+
+
+def by_python(name, args):
+    """The same call by the public function on an explicit stream, which takes the way
+    through Python."""
+    kw = dict(stream=torch.cuda.current_stream())
+    if name.startswith("rms"):
+        kw.update(residual=args[-2], residual_out=args[-1])
+        args = args[:-2]
+    elif name == "quantise_fp8":
+        kw.update(block_rows=args[-1])
+        args = args[:-1]
+    else:
+        kw.update(status=args[-1])
+        args = args[:-1]
+    getattr(kvp, "kvp_" + name)(*args, **kw)
+
+
+NAMES = ["rms_norm", "rms_norm_fp8", "quantise_fp8", "matmul_fp8"]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", NAMES)
+def test_both_ways_give_the_same(name, dtype):
+    a, b = arguments(dtype)[name], arguments(dtype)[name]
+    assert getattr(kvp._calls(), name)(*a) == kvp.KVP_OK
+    by_python(name, b)
+    torch.cuda.synchronize()
+    for x, y in zip(a, b):
+        if isinstance(x, torch.Tensor):
+            assert torch.equal(bits(x), bits(y))
+    # without what may be left out, and of other types
+    if name.startswith("rms"):
+        assert getattr(kvp._calls(), name)(*a[:-2], None, None) == kvp.KVP_OK
+    if name == "rms_norm":
+        heads = gpu(3, 7, 64, dtype=dtype)[:, 2:5]
+        assert kvp._calls().rms_norm(heads, heads, gpu(64, dtype=dtype), 0.5, None,
+                                     None) == kvp.KVP_OK
+    if name == "matmul_fp8":
+        for out in (a[0], gpu(5, 130, dtype=F32), gpu(5, 140, dtype=dtype)[:, 3:133]):
+            assert kvp._calls().matmul_fp8(out, a[1].view(F8), a[2], a[3].view(F8), a[4],
+                                           None) == kvp.KVP_OK
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_what_is_not_in_order_is_left_alone(name):
+    """Every tensor in turn of another type, on the CPU, one row short, with strided rows
+    or something else altogether: not called, and nothing written."""
+    call = getattr(kvp._calls(), name)
+    good = arguments(torch.float16)[name]
+    before = [x.clone() if isinstance(x, torch.Tensor) else x for x in good]
+    for i, x in enumerate(good):
+        if not isinstance(x, torch.Tensor):
+            continue
+        wide = torch.zeros((*x.shape[:-1], 2 * x.shape[-1]), dtype=x.dtype, device="cuda")
+        bad = [x.double(), x.cpu(), "x", 3, wide[..., ::2], x[None]]
+        if not (name == "matmul_fp8" and i == 5):
+            bad += [x[:-1], None]
+        if x.dim() > 1:
+            bad.append(x.t().contiguous().t())
+        for y in bad:
+            if isinstance(y, torch.Tensor) and y.is_cuda and y.shape == x.shape and \
+                    y.dtype == x.dtype and y.is_contiguous():
+                continue
+            if name == "matmul_fp8" and i == 5 and getattr(y, "dtype", None) == x.dtype and y.is_cuda:
+                continue                     # (a status word of any shape)
+            assert call(*good[:i], y, *good[i + 1:]) is None, (i, getattr(y, "shape", y))
+    for i, x in enumerate(good):
+        if isinstance(x, (int, float)):
+            for y in ("1", None, 2.5 if isinstance(x, int) else 1, 2 ** 40, 64):
+                assert call(*good[:i], y, *good[i + 1:]) is None
+    torch.cuda.synchronize()
+    for x, y in zip(good, before):
+        if isinstance(x, torch.Tensor):
+            assert torch.equal(bits(x), bits(y))
