@@ -124,31 +124,44 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
     for (int k = max(0, fetched - S::kStages); k < fetched; ++k)
       ok = mm::wait(smem_addr(full + k % S::kStages), (k / S::kStages) & 1) && ok;
   } else if (warp == kAddWarps + 1) {
-    // ---- products: 4 x K = 32 of a stage for a group, kBatch groups to a TMEM buffer
+    // ---- products: 4 x K = 32 of a stage for a group, kBatch groups to a TMEM buffer; two
+    // stages are waited for at a time
     mm::Ring<S::kStages> ring;
     mm::Ring<2> buffer;
-    for (int k = 0; k < count && ok; ++k, ring.next()) {
+    for (int k = 0; k < count && ok; k += 2) {
       const int in = k % S::kBatch;
-      const bool last = in == S::kBatch - 1 || k == count - 1;
-      if (in == 0)
-        ok = mm::wait_both(smem_addr(full + ring.at), ring.flip, smem_addr(taken + buffer.at),
-                           buffer.flip ^ 1);
-      else
-        ok = mm::wait(smem_addr(full + ring.at), ring.flip);
+      const bool two = k + 1 < count;
+      const bool last = in == S::kBatch - 2 || k + 2 >= count;
+      mm::Ring<S::kStages> second = ring;
+      second.next();
+      bool ready = mbar_try_wait(smem_addr(full + ring.at), ring.flip);
+      if (two) ready &= mbar_try_wait(smem_addr(full + second.at), second.flip);
+      if (in == 0) ready &= mbar_try_wait(smem_addr(taken + buffer.at), buffer.flip ^ 1);
+      if (!ready)
+        ok = mm::wait(smem_addr(full + ring.at), ring.flip) &&
+             (!two || mm::wait(smem_addr(full + second.at), second.flip)) &&
+             (in != 0 || mm::wait(smem_addr(taken + buffer.at), buffer.flip ^ 1));
       umma::fence_after_sync();
       if (ok && elect_one()) {
-        const uint32_t at = smem_addr(sm + ring.at * S::kStage);
-        const uint64_t b = umma::smem_desc_sw128(at, 16, 1024);
-        const uint64_t a = umma::smem_desc_sw128(at + kTileB, 16, 1024);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          mm::mma_f8<1>(tmem + (buffer.at * S::kBatch + in) * kTokens, b + 2 * s, a + 2 * s, kInstr,
-                        s > 0);
-        umma::commit(smem_addr(empty + ring.at));
+        for (int q = 0; q < 2; ++q) {
+          if (q == 1 && !two) break;
+          const int st = q == 0 ? ring.at : second.at;
+          const uint32_t at = smem_addr(sm + st * S::kStage);
+          const uint64_t b = umma::smem_desc_sw128(at, 16, 1024);
+          const uint64_t a = umma::smem_desc_sw128(at + kTileB, 16, 1024);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            mm::mma_f8<1>(tmem + (buffer.at * S::kBatch + in + q) * kTokens, b + 2 * s, a + 2 * s,
+                          kInstr, s > 0);
+          umma::commit(smem_addr(empty + st));
+        }
         if (last) umma::commit(smem_addr(sums + buffer.at));
       }
       __syncwarp();
       if (last) buffer.next();
+      ring = second;
+      ring.next();
     }
     if (elect_one()) umma::commit(smem_addr(done));
     __syncwarp();
