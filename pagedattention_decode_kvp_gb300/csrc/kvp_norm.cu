@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kern
       }
     }
   }
+  float sums[kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     float sum = 0.f;
@@ -135,7 +136,17 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kern
 #pragma unroll
       for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
     }
-    const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(p.dim)), p.eps));
+    sums[j] = sum;
+  }
+  // lane j % kRows of a row's lanes works out row j's factor for all of them
+  float mine_r = sums[0];
+#pragma unroll
+  for (int j = 1; j < kRows; ++j) mine_r = lane % kRows == j ? sums[j] : mine_r;
+  mine_r = __frsqrt_rn(__fadd_rn(__fdiv_rn(mine_r, static_cast<float>(p.dim)), p.eps));
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    float r = mine_r;
+    if constexpr (kRows > 1) r = __shfl_sync(0xffffffffu, mine_r, j, kThreads < 32 ? kThreads : 32);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int at = 8 * (lane + c * kThreads);
