@@ -45,8 +45,30 @@ struct Shape {
   static constexpr uint32_t kTmem = 2 * kBatch * kTokens;
   static_assert(kSmem * kCtas <= (kCtas == 2 ? 226 : 227) * 1024, "shared memory of an SM");
   static_assert(kTmem * kCtas <= 512 && kSpan % kBatch == 0, "TMEM, spans of whole batches");
-  static_assert(kStages * kStage >= kTokens * kRowsB * 4, "the sums are exchanged in the ring");
+  static_assert(kStages * kStage >= kTokens * (kRowsB + 4) * 4, "the sums are exchanged in the ring");
 };
+
+// 16 rows x 8 kReps columns of TMEM: lane l holds columns 8 j + 2 (l % 4) and the next of rows
+// l / 4 (registers 4 j, 4 j + 1) and l / 4 + 8 (4 j + 2, 4 j + 3).
+template <int kReps>
+__device__ __forceinline__ void load_16(uint32_t taddr, uint32_t (&r)[4 * kReps]) {
+  static_assert(kReps == 2 || kReps == 4, "repetitions");
+  if constexpr (kReps == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr));
+  }
+}
 
 // grid.x = (token tile, weight tile, rank of the cluster), the last running fastest.
 template <int kTokens>
@@ -193,40 +215,44 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
     }
   }
 
-  // ---- scale and add: weight row `row` and tokens col .. col + kCols - 1
+  // ---- scale and add: weight rows 32 (warp % 4) + lane / 4 + 8 i (i < 4), tokens
+  // col + 8 j + 2 (lane % 4) and the next: so a lane needs a quarter of the scales only
   constexpr int kCols = S::kCols;
-  const int row = tid % kRowsB, col = warp / 4 * kCols;
-  uint64_t acc[kCols / 2];
+  constexpr int kReps = kCols / 8;
+  const int col = warp / 4 * kCols;
+  uint64_t acc[4][kReps];
   if (warp < kAddWarps) {
 #pragma unroll
-    for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < kReps; ++j) acc[i][j] = 0;
     const uint32_t at = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + col;
     mm::Ring<2> buffer;
     mm::Ring<kSpans> spans;
     for (int k0 = 0; k0 < count; k0 += S::kBatch, buffer.next()) {
       if (k0 % kSpan == 0 && ok) ok = mm::wait(smem_addr(scaled + spans.at), spans.flip);
-      const float* sc = scales + (spans.at * kSpan + k0 % kSpan) * S::kPitch + col;
+      const float* sc = scales + (spans.at * kSpan + k0 % kSpan) * S::kPitch + col + 2 * (lane % 4);
       if (ok) ok = mm::wait(smem_addr(sums + buffer.at), buffer.flip);
       umma::fence_after_sync();
       const int batch = min(S::kBatch, count - k0);
 #pragma unroll 1
       for (int g = 0; g < batch; ++g) {
+        uint32_t t[2][4 * kReps];
+        const uint32_t from = at + (buffer.at * S::kBatch + g) * kTokens;
+        load_16<kReps>(from, t[0]);
+        load_16<kReps>(from + (16u << 16), t[1]);
+        uint64_t s2[kReps];
 #pragma unroll
-        for (int j = 0; j < kCols; j += 16) {
-          float t[16];
-          umma::ld16(at + (buffer.at * S::kBatch + g) * kTokens + j, t);
-          ulonglong2 s2[4];
+        for (int j = 0; j < kReps; ++j)
+          s2[j] = *reinterpret_cast<const uint64_t*>(sc + g * S::kPitch + 8 * j);
+        umma::wait_ld();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s2[i] = *reinterpret_cast<const ulonglong2*>(sc + g * S::kPitch + j + 4 * i);
-          umma::wait_ld();
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = j / 2 + 2 * i;
-            acc[c] = ffma2(f2pack(t[4 * i], t[4 * i + 1]), s2[i].x, acc[c]);
-            acc[c + 1] = ffma2(f2pack(t[4 * i + 2], t[4 * i + 3]), s2[i].y, acc[c + 1]);
+          for (int j = 0; j < kReps; ++j) {
+            const uint32_t* v = t[i / 2] + 4 * j + 2 * (i % 2);
+            acc[i][j] = ffma2(f2pack(__uint_as_float(v[0]), __uint_as_float(v[1])), s2[j], acc[i][j]);
           }
-        }
       }
       umma::fence_before_sync();
       __syncwarp();
@@ -245,30 +271,29 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
   bool bad = failed != 0;
   if (bad && tid == 0) set_status(p.status, kErrTimeout);
 
-  const int n = n0 + row;
-  if (splits == 1) {
-    if (warp >= kAddWarps || n >= p.n) return;
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const float2 v = f2unpack(acc[j / 2]);
-      const int m = m0 + col + j;
-      if (m < p.m)
-        mm::store_out(p, static_cast<long long>(m) * p.out_stride + n, bad ? 0.f : j & 1 ? v.y : v.x);
-    }
-    return;
-  }
-  // ---- the cluster's sums: every CTA adds and writes its share of the tokens
-  float* mine = reinterpret_cast<float*>(sm);   // [kTokens][128]
+  // ---- the sums go through shared memory, a cluster's to all of its CTAs: each adds and
+  // writes its share of the tokens
+  constexpr int kSumPitch = kRowsB + 4;
+  float* mine = reinterpret_cast<float*>(sm);   // [kTokens][kSumPitch]
   if (warp < kAddWarps) {
+    float* to = mine + (col + 2 * (lane % 4)) * kSumPitch + warp % 4 * 32 + lane / 4;
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const float2 v = f2unpack(acc[j / 2]);
-      mine[(col + j) * kRowsB + row] = j & 1 ? v.y : v.x;
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < kReps; ++j) {
+        const float2 v = f2unpack(acc[i][j]);
+        to[8 * j * kSumPitch + 8 * i] = v.x;
+        to[(8 * j + 1) * kSumPitch + 8 * i] = v.y;
+      }
   }
-  if (bad && tid < splits) mm::store_remote(mm::at_rank(smem_addr(const_cast<int*>(&failed)), tid), 1);
-  mm::cluster_sync();
-  bad = failed != 0;
+  if (splits > 1) {
+    if (bad && tid < splits)
+      mm::store_remote(mm::at_rank(smem_addr(const_cast<int*>(&failed)), tid), 1);
+    mm::cluster_sync();
+    bad = failed != 0;
+  } else {
+    __syncthreads();
+  }
   if (warp < kAddWarps) {
     // a warp takes a token, a lane four weight rows
     constexpr int kAtOnce = kTokens == 64 ? 1 : 2;   // (registers)
@@ -284,7 +309,7 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
         for (int r = 0; r < kMaxSplits; ++r)
           if (r < splits && j0 + u * kAddWarps < end)
             v[u][r] = mm::load_remote4(
-                mm::at_rank(smem_addr(mine + (j0 + u * kAddWarps) * kRowsB + 4 * lane), r));
+                mm::at_rank(smem_addr(mine + (j0 + u * kAddWarps) * kSumPitch + 4 * lane), r));
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
         const int j = j0 + u * kAddWarps;
@@ -312,7 +337,7 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
       }
     }
   }
-  mm::cluster_sync();
+  if (splits > 1) mm::cluster_sync();
 }
 
 template <int kTokens>
