@@ -369,12 +369,12 @@ cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, con
 }  // namespace
 
 // The plan with the least time by a model of what was measured, in us: 2.6 for the start of a
-// wave of CTAs (pairs: 3.5 once), a group of a CTA by its tokens and by whether its SM holds another CTA, the
-// exchange of a cluster's sums, and the bytes of a and b at the rate of HBM.  Measured and
-// modelled (tokens x splits): 1 x 4096 x 4096 16x1 11.1 and 11.2, 16x4 6.9 and 6.8; 64 x 4096
-// x 4096 32x4 8.4 and 8.5, 64x4 9.4 and 9.2, 64x1 16.8 and 16.4; 64 x 10240 x 8192 64x3 21.9
-// and 23.4, 64x1 29.9 and 30.1; 256 x 4096 x 4096 128x2 14.7 and 13.8, pairs 20.8 and 20.5;
-// 517 x 4096 x 4096 128x1 34.4 and 36.5, pairs 21.0 and 20.5.
+// wave of CTAs (pairs: 3.5 once), a group of a CTA by its tokens and by whether its SM holds
+// another CTA, the exchange of a cluster's sums, and the bytes of a and b at the rate of HBM.
+// Measured and modelled (tokens x splits): 16 x 10240 x 8192 16x1 18.6 and 18.0, 16x3 16.9 and
+// 15.8; 64 x 4096 x 4096 32x4 8.2 and 7.7, 64x4 8.7 and 8.5, 64x1 14.0 and 13.8; 64 x 10240 x
+// 8192 64x3 19.1 and 17.9, 64x1 24.3 and 25.0; 256 x 4096 x 4096 128x2 12.9 and 12.5, pairs 20.7
+// and 20.5; 517 x 4096 x 4096 128x1 27.3 and 34.0, pairs 21.0 and 20.5.
 MatmulPlan matmul_plan(int m, int n, int groups) {
   struct Kind {
     int tokens, resident;      // rows of a per tile, CTAs of an SM
@@ -384,8 +384,8 @@ MatmulPlan matmul_plan(int m, int n, int groups) {
   // have no multiple of most sizes: 48 clusters of 3, one CTA to an SM, take two waves)
   constexpr int kFit[2][kMaxSplits] = {{152, 76, 46, 36, 28, 23, 15, 15},
                                        {304, 152, 97, 74, 58, 46, 38, 36}};
-  constexpr Kind kKinds[] = {{16, 2, 0.27, 0.33}, {32, 2, 0.30, 0.44}, {64, 2, 0.43, 0.83},
-                             {128, 1, 0.53, 0.53}};
+  constexpr Kind kKinds[] = {{16, 2, 0.24, 0.28}, {32, 2, 0.30, 0.34}, {64, 2, 0.35, 0.58},
+                             {128, 1, 0.45, 0.45}};
   const auto tiles = [](long long x, int per) { return (x + per - 1) / per; };
   MatmulPlan plan{256, 1};
   double best = 3.5 + 0.53 * groups * tiles(tiles(m, 256) * tiles(n, 256), kNumSms / 2);
