@@ -360,15 +360,16 @@ PyObject* release_tables(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // t [rows, n] of `type` with contiguous rows: their stride in elements.
 bool matrix(const Tensor* t, ScalarType type, int64_t rows, int64_t n, int64_t* stride) {
-  if (t->scalar_type() != type || !shape(t, {rows, n}) || (n > 1 && t->stride(1) != 1)) return false;
+  if (t->scalar_type() != type || !shape(t, {rows, n}) || (n > 1 && t->stride(1) != 1))
+    return false;
   *stride = rows > 1 ? t->stride(0) : n;
   return true;
 }
 
 // Codes [rows, n], held as uint8 or float8_e4m3fn.
 bool codes(const Tensor* t, int64_t rows, int64_t n, int64_t* stride) {
-  return matrix(t, t->scalar_type() == ScalarType::Byte ? ScalarType::Byte : ScalarType::Float8_e4m3fn,
-                rows, n, stride);
+  const bool bytes = t->scalar_type() == ScalarType::Byte;
+  return matrix(t, bytes ? ScalarType::Byte : ScalarType::Float8_e4m3fn, rows, n, stride);
 }
 
 int64_t groups(int64_t n) { return (n + 127) / 128; }

@@ -44,16 +44,6 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// Both barriers: one trip to shared memory where both are done (a trip takes about 130
-// cycles).
-__device__ __forceinline__ bool wait_both(uint32_t bar, uint32_t parity, uint32_t bar2,
-                                          uint32_t parity2) {
-  const bool one = dev::mbar_try_wait(bar, parity);
-  const bool two = dev::mbar_try_wait(bar2, parity2);
-  if (one && two) return true;
-  return wait(bar, parity) && wait(bar2, parity2);
-}
-
 // A ring's place and how often it has wrapped (mod 2): what is waited for is the phase
 // `flip` of a full place, and `flip ^ 1` of a free one (a new barrier's passes).
 template <int kPlaces>

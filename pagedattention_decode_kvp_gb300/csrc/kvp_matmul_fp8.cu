@@ -45,7 +45,7 @@ struct Shape {
   static constexpr uint32_t kTmem = 2 * kBatch * kTokens;
   static_assert(kSmem * kCtas <= (kCtas == 2 ? 226 : 227) * 1024, "shared memory of an SM");
   static_assert(kTmem * kCtas <= 512 && kSpan % kBatch == 0, "TMEM, spans of whole batches");
-  static_assert(kStages * kStage >= kTokens * (kRowsB + 4) * 4, "the sums are exchanged in the ring");
+  static_assert(kStages * kStage >= kTokens * (kRowsB + 4) * 4, "the sums lie in the ring");
 };
 
 // 16 rows x 8 kReps columns of TMEM: lane l holds columns 8 j + 2 (l % 4) and the next of rows
@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
   const int n0 = static_cast<int>(tile % tiles_n) * kRowsB;
   const int m0 = static_cast<int>(tile / tiles_n) * kTokens;
   const int first = static_cast<int>(static_cast<long long>(p.groups) * rank / splits);
-  const int count = static_cast<int>(static_cast<long long>(p.groups) * (rank + 1) / splits) - first;
+  const int end_group = static_cast<int>(static_cast<long long>(p.groups) * (rank + 1) / splits);
+  const int count = end_group - first;
   if (tid == 0) {
     failed = 0;
     for (int i = 0; i < S::kStages; ++i) {
@@ -251,7 +252,8 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
 #pragma unroll
           for (int j = 0; j < kReps; ++j) {
             const uint32_t* v = t[i / 2] + 4 * j + 2 * (i % 2);
-            acc[i][j] = ffma2(f2pack(__uint_as_float(v[0]), __uint_as_float(v[1])), s2[j], acc[i][j]);
+            acc[i][j] =
+                ffma2(f2pack(__uint_as_float(v[0]), __uint_as_float(v[1])), s2[j], acc[i][j]);
           }
       }
       umma::fence_before_sync();

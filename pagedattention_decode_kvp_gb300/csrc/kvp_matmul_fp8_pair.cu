@@ -1,17 +1,23 @@
 // kvp_matmul_fp8_pair.cu -- the block-scaled product of kvp_matmul_fp8 for many rows:
 // pairs of CTAs on tiles of 256 x 256.
 //
-// A pair's tcgen05.mma (cta_group::2, M = 256, N = 128) takes half of A's rows and half
-// of B's from each CTA's shared memory, so that a byte fetched serves 256 rows; each CTA
-// holds the sums of 128 rows in its TMEM.  Eight warps read a group's sums, a thread 128
-// columns of one row, and add them, scaled, to float32 sums in registers (whose columns
-// share one scale of B, and whose row one of A) while the tensor cores form the next
-// group's.  Persistent: a pair walks the tiles, and the fetching warps run on into the
-// next one.
+// A pair's tcgen05.mma (cta_group::2, M = N = 256) takes half of A's rows and half of B's
+// from each CTA's shared memory, so that a byte fetched serves 256 rows; each CTA holds the
+// sums of 128 rows in its TMEM: two buffers of 256 columns, all of it.  Eight warps read a
+// group's sums, a thread 128 columns of one row, and add them, scaled, to float32 sums in
+// registers (whose columns share one scale of B, and whose row one of A) while the tensor
+// cores form the next group's.  Persistent: a pair walks the tiles; the warps that fetch
+// tiles and scales run on into the next one.
 //
-// What bounds it is the way round of a TMEM buffer: product, commit, read, arrival from
-// both CTAs, next product.  A tile's two column halves therefore go round by themselves,
-// each with two buffers of 128 columns and four adding warps per CTA.
+// Measured: 8192 x 8192 x 8192 445 us, 2470 TFLOP/s; 33098 x 12288 x 4096 1440 us, 2310;
+// 8191 x 10240 x 8192 548 us, 2500.  The products alone take 240 us of the first (4600
+// TFLOP/s), with the fetches 283; the rest is the way round of a TMEM buffer (product,
+// commit, read, arrivals from both CTAs) and the 2 x 64 two-lane multiply-adds a thread
+// and group; run for seconds it is held by the board's power (1370 W, SM clock 1970 MHz,
+// 2220 TFLOP/s).  Tried: 16 adding warps of 64 columns (their 104 registers cost moves and
+// spills: 502 us), 16 columns a read (449), halves of 128 columns with a warp and buffers
+// each (equal, and A read twice from shared memory), the next group's first read ahead of
+// this one's last sums (501).
 #include "kvp_matmul.cuh"
 
 namespace kvp {
@@ -19,16 +25,15 @@ namespace kvp {
 namespace {
 
 constexpr int kTile = 256;                    // rows and columns of a pair's tile
-constexpr int kHalfN = 128;                   // columns of a half: one instruction's
 constexpr uint32_t kHalf = 128 * 128;         // bytes of a CTA's half of A or B per stage
 constexpr uint32_t kStage = 2 * kHalf;
 constexpr int kStages = 6;
 constexpr int kAddWarps = 8;
 constexpr int kCols = 128;                    // a thread's, of one row
 constexpr int kThreads = (kAddWarps + 4) * 32;   // three warpgroups
-// Registers: the launch's 168 a thread are split anew, 256 * 216 + 128 * 72 = 384 * 168.
-constexpr int kAddRegs = 216;
-constexpr int kOtherRegs = 72;
+// Registers: the launch's 168 a thread are split anew, 256 * 224 + 128 * 56 = 384 * 168.
+constexpr int kAddRegs = 224;
+constexpr int kOtherRegs = 56;
 static_assert(kAddWarps * 32 * kAddRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
 constexpr uint32_t kWarpBytes = 1024;         // each adding warp's, for its results
 constexpr int kSpan = 8;                      // groups whose scales are staged at a time
@@ -38,15 +43,15 @@ constexpr uint32_t kSpanBytes = (kSpan * kPitch + 2 * kSpan) * 4;   // rows', th
 constexpr uint32_t kScaleOff = kStages * kStage;
 constexpr uint32_t kWarpOff = kScaleOff + kSpans * kSpanBytes;
 constexpr uint32_t kBarOff = kWarpOff + kAddWarps * kWarpBytes;
-constexpr int kNumBars = 2 * kStages + 9 + 2 * kSpans;
+constexpr int kNumBars = 2 * kStages + 5 + 2 * kSpans;
 constexpr uint32_t kSmem = 1024 + kBarOff + kNumBars * 8 + 16;
 constexpr uint32_t kTmem = 512;
 constexpr int kBand = 8;                      // row tiles that are walked together
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // A tile of codes, at this CTA's `dst`; completes on the pair's first CTA's `bar`.
-__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                          uint32_t bar) {
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                          int32_t y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
       ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -88,13 +93,12 @@ __device__ __forceinline__ void add_scaled(uint64_t& acc, float t0, float t1, ui
 // column, so that the pairs at work at one time share rows of A and of B in L2.
 struct Walk {
   int tiles_m, tiles_n;
-  __device__ __forceinline__ void at(long long i, int* m, int* n) const {
-    const long long per = static_cast<long long>(kBand) * tiles_n;
-    const int band = static_cast<int>(i / per);
-    const int in = static_cast<int>(i - band * per);
-    const int height = min(kBand, tiles_m - band * kBand);
-    *n = in / height;
-    *m = band * kBand + in % height;
+  __device__ __forceinline__ void at(uint32_t i, int* m, int* n) const {
+    const uint32_t per = static_cast<uint32_t>(kBand) * tiles_n;
+    const uint32_t band = i / per, in = i - band * per;
+    const uint32_t height = min(kBand, tiles_m - static_cast<int>(band) * kBand);
+    *n = static_cast<int>(in / height);
+    *m = static_cast<int>(band * kBand + in % height);
   }
 };
 
@@ -103,38 +107,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_fp8_pair_kernel(const MatmulParams p, const __grid_constant__ CUtensorMap ta,
                            const __grid_constant__ CUtensorMap tb) {
   using namespace dev;
-  constexpr uint32_t kInstr = umma::instr_desc_f16(kTile, kHalfN, false, false, false);
+  constexpr uint32_t kInstr = umma::instr_desc_f16(kTile, kTile, false, false, false);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBarOff);   // (of the first CTA)
-  uint64_t* empty = full + kStages;
-  uint64_t* sums = empty + kStages;   // [half][2] a TMEM buffer holds a group's sums
-  uint64_t* taken = sums + 4;         // [half][2] both CTAs have read them (first CTA's)
-  uint64_t* scaled = taken + 4;       // [kSpans] scales are there
-  uint64_t* used = scaled + kSpans;   // [kSpans] they have been read
-  uint64_t* done = used + kSpans;     // every product of the pair complete
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  // barriers, by their shared addresses
+  const uint32_t base = smem_addr(sm);
+  const uint32_t full = base + kBarOff;                // [kStages] (the first CTA's)
+  const uint32_t empty = full + 8 * kStages;           // [kStages]
+  const uint32_t sums = empty + 8 * kStages;           // [2] a TMEM buffer holds a group's sums
+  const uint32_t taken = sums + 16;                    // [2] both CTAs have read them (first's)
+  const uint32_t scaled = taken + 16;                  // [kSpans] scales are there
+  const uint32_t used = scaled + 8 * kSpans;           // [kSpans] they have been read
+  const uint32_t done = used + 8 * kSpans;             // every product of the pair complete
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + kBarOff + (kNumBars - 1) * 8 + 8);
   __shared__ int failed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = mm::cluster_rank();
   const Walk walk{(p.m + kTile - 1) / kTile, (p.n + kTile - 1) / kTile};
-  const long long tiles = static_cast<long long>(walk.tiles_m) * walk.tiles_n;
-  const long long pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const uint32_t tiles = static_cast<uint32_t>(walk.tiles_m) * walk.tiles_n;   // (below 2^31)
+  const uint32_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   if (tid == 0) {
     failed = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(full + i), 1);
-      mbar_init(smem_addr(empty + i), 2);
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_addr(sums + i), 1);
-      mbar_init(smem_addr(taken + i), kAddWarps);   // half of each CTA's
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sums + 8 * i, 1);
+      mbar_init(taken + 8 * i, 2 * kAddWarps);
     }
     for (int i = 0; i < kSpans; ++i) {
-      mbar_init(smem_addr(scaled + i), 1);
-      mbar_init(smem_addr(used + i), kAddWarps);
+      mbar_init(scaled + 8 * i, 1);
+      mbar_init(used + 8 * i, kAddWarps);
     }
-    mbar_init(smem_addr(done), 2);
+    mbar_init(done, 1);
     prefetch_tensormap(&ta);
     prefetch_tensormap(&tb);
     fence_barrier_init();
@@ -153,59 +159,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kAddWarps) {
       // ---- fetch this CTA's halves; the first CTA expects the bytes of both
       mm::Ring<kStages> ring;
-      for (long long i = pair; i < tiles && ok; i += pairs) {
+      for (uint32_t i = pair; i < tiles && ok; i += pairs) {
         int tm, tn;
         walk.at(i, &tm, &tn);
-        const int m0 = tm * kTile + 128 * rank, n0 = tn * kTile + 64 * rank;
+        const int m0 = tm * kTile + 128 * rank, n0 = tn * kTile + 128 * rank;
         for (int k = 0; k < p.groups && ok; ++k, ring.next()) {
           const int st = ring.at;
-          ok = mm::wait(smem_addr(empty + st), ring.flip ^ 1);
+          ok = mm::wait(empty + 8 * st, ring.flip ^ 1);
           if (ok && elect_one()) {
-            const uint32_t bar = mm::at_rank(smem_addr(full + st), 0);
-            const uint32_t at = smem_addr(sm + st * kStage);
-            if (rank == 0) mbar_arrive_expect_tx(smem_addr(full + st), 2 * kStage);
+            const uint32_t bar = mm::at_rank(full + 8 * st, 0);
+            const uint32_t at = base + st * kStage;
+            if (rank == 0) mbar_arrive_expect_tx(full + 8 * st, 2 * kStage);
             load_pair(at, &ta, k * 128, m0, bar);
             load_pair(at + kHalf, &tb, k * 128, n0, bar);
-            load_pair(at + kHalf + kHalf / 2, &tb, k * 128, n0 + kHalfN, bar);
+            load_pair(at + kHalf + kHalf / 2, &tb, k * 128, n0 + 64, bar);
           }
           __syncwarp();
         }
       }
       // no copy may land after the exit: the pair's last products have read every stage
-      ok = mm::wait(smem_addr(done), 0) && ok;
-    } else if (warp <= kAddWarps + 2 && rank == 0) {
-      // ---- products of the pair: a warp for each half of the columns (one warp's waits and
-      // issues took 960 cycles a group, the products take 512)
-      const int h = warp - (kAddWarps + 1);
+      ok = mm::wait(done, 0) && ok;
+    } else if (warp == kAddWarps + 1 && rank == 0) {
+      // ---- products of the pair
       mm::Ring<kStages> ring;
       mm::Ring<2> buffer;
-      for (long long i = pair; i < tiles && ok; i += pairs) {
+      for (uint32_t i = pair; i < tiles && ok; i += pairs) {
         for (int k = 0; k < p.groups && ok; ++k, ring.next(), buffer.next()) {
-          const int st = ring.at, buf = 2 * h + buffer.at;
-          const uint32_t at = smem_addr(sm + st * kStage);
+          const int st = ring.at, buf = buffer.at;
+          const uint32_t at = base + st * kStage;
           const uint64_t a = umma::smem_desc_sw128(at, 16, 1024);
-          const uint64_t b = umma::smem_desc_sw128(at + kHalf + h * (kHalf / 2), 16, 1024);
-          ok = mm::wait_both(smem_addr(full + st), ring.flip, smem_addr(taken + buf),
-                             buffer.flip ^ 1);
+          const uint64_t b = umma::smem_desc_sw128(at + kHalf, 16, 1024);
+          // (two trips to shared memory at a time)
+          const bool ready = mbar_try_wait(full + 8 * st, ring.flip) &
+                             mbar_try_wait(taken + 8 * buf, buffer.flip ^ 1);
+          if (!ready)
+            ok = mm::wait(full + 8 * st, ring.flip) && mm::wait(taken + 8 * buf, buffer.flip ^ 1);
           umma::fence_after_sync();
           if (ok && elect_one()) {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              mm::mma_f8<2>(tmem + buf * kHalfN, a + 2 * s, b + 2 * s, kInstr, s > 0);
-            commit_pair(smem_addr(sums + buf));
-            commit_pair(smem_addr(empty + st));
+              mm::mma_f8<2>(tmem + buf * kTile, a + 2 * s, b + 2 * s, kInstr, s > 0);
+            commit_pair(sums + 8 * buf);
+            commit_pair(empty + 8 * st);
           }
           __syncwarp();
         }
       }
-      if (elect_one()) commit_pair(smem_addr(done));
+      if (elect_one()) commit_pair(done);
       __syncwarp();
-      ok = mm::wait(smem_addr(done), 0) && ok;
+      ok = mm::wait(done, 0) && ok;
     } else if (warp == kAddWarps + 3) {
       // ---- scales of the CTA's 128 rows and of the tile's two halves, spans of 8 groups: 8
       // lanes take a row's, so that its 32 bytes are one sector
       mm::Ring<kSpans> ring;
-      for (long long i = pair; i < tiles && ok; i += pairs) {
+      for (uint32_t i = pair; i < tiles && ok; i += pairs) {
         int tm, tn;
         walk.at(i, &tm, &tn);
         const int m0 = tm * kTile + 128 * static_cast<int>(rank) + lane / 8;
@@ -215,37 +222,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int g = k + lane % 8;
           const bool in = g < p.groups;
           const float* from = p.a_scale + static_cast<long long>(m0) * p.groups + g;
-          const int n = n0 + lane / 8 * kHalfN;
-          const float b = in && lane < 16 && n < p.n
-                              ? p.b_scale[static_cast<long long>(n / kScaleGroup) * p.groups + g] : 0.f;
+          const int n = n0 + lane / 8 * kScaleGroup;
+          const long long block = n / kScaleGroup;
+          const float b = in && lane < 16 && n < p.n ? p.b_scale[block * p.groups + g] : 0.f;
 #pragma unroll 1
-          for (int h = 0; h < 32; h += 16) {
-            float v[16];
+          for (int h = 0; h < 32; h += 8) {
+            float v[8];
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              v[r] = in && m0 + 4 * (h + r) < p.m ? from[static_cast<long long>(4 * (h + r)) * p.groups]
-                                                  : 0.f;
-            if (h == 0) ok = mm::wait(smem_addr(used + ring.at), ring.flip ^ 1);
+            for (int r = 0; r < 8; ++r)
+              v[r] = in && m0 + 4 * (h + r) < p.m
+                         ? from[static_cast<long long>(4 * (h + r)) * p.groups] : 0.f;
+            if (h == 0) ok = mm::wait(used + 8 * ring.at, ring.flip ^ 1);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) to[lane % 8 * kPitch + lane / 8 + 4 * (h + r)] = v[r];
+            for (int r = 0; r < 8; ++r) to[lane % 8 * kPitch + lane / 8 + 4 * (h + r)] = v[r];
           }
           if (lane < 16) to[kSpan * kPitch + lane] = b;
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(scaled + ring.at));
+          if (lane == 0) mbar_arrive(scaled + 8 * ring.at);
         }
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAddRegs));
     // ---- scale and add: row 32 (warp % 4) + lane, kCols columns from kCols (warp / 4) on
-    const int quarter = warp & 3, first = warp / 4 * kCols, half = first / kHalfN;
-    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kTile +
-                        first % kHalfN;
+    const int quarter = warp & 3, first = warp / 4 * kCols, half = first / kScaleGroup;
+    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + first;
     uint4* piece = reinterpret_cast<uint4*>(sm + kWarpOff + warp * kWarpBytes);
-    const uint32_t free_bar = mm::at_rank(smem_addr(taken + 2 * half), 0);
+    const uint32_t free_bar = mm::at_rank(taken, 0);
     mm::Ring<2> buffer;
     mm::Ring<kSpans> spans;
-    for (long long i = pair; i < tiles; i += pairs) {
+    for (uint32_t i = pair; i < tiles; i += pairs) {
       uint64_t acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
@@ -253,35 +259,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float* sa = reinterpret_cast<const float*>(sm + kScaleOff + spans.at * kSpanBytes) +
                           32 * quarter + lane;
         const float* sb = sa - 32 * quarter - lane + kSpan * kPitch + kSpan * half;
-        if (ok) ok = mm::wait(smem_addr(scaled + spans.at), spans.flip);
+        if (ok) ok = mm::wait(scaled + 8 * spans.at, spans.flip);
         const int span = min(kSpan, p.groups - k0);
 #pragma unroll 1
         for (int k = 0; k < span; ++k, buffer.next()) {
           const int buf = buffer.at;
           const float s = __fmul_rn(sa[k * kPitch], sb[k]);
           const uint64_t s2 = f2pack(s, s);
-          if (ok) ok = mm::wait(smem_addr(sums + 2 * half + buf), buffer.flip);
+          if (ok) ok = mm::wait(sums + 8 * buf, buffer.flip);
           umma::fence_after_sync();
-          // 16 columns are on their way while 16 are added
-          float t[2][16];
-          umma::ld16(at + buf * kHalfN, t[0]);
+          // 32 columns are on their way while 32 are added
+          float t[2][32];
+          umma::ld32(at + buf * kTile, t[0]);
 #pragma unroll
-          for (int j = 0; j < kCols / 16; ++j) {
+          for (int j = 0; j < kCols / 32; ++j) {
             umma::wait_ld();
-            if (j < kCols / 16 - 1) {
-              umma::ld16(at + buf * kHalfN + 16 * (j + 1), t[(j + 1) & 1]);
+            if (j < kCols / 32 - 1) {
+              umma::ld32(at + buf * kTile + 32 * (j + 1), t[(j + 1) & 1]);
             } else {
               umma::fence_before_sync();
               __syncwarp();
               if (lane == 0) arrive_remote(free_bar + 8 * buf);
             }
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              add_scaled(acc[8 * j + c], t[j & 1][2 * c], t[j & 1][2 * c + 1], s2);
+            for (int c = 0; c < 16; ++c)
+              add_scaled(acc[16 * j + c], t[j & 1][2 * c], t[j & 1][2 * c + 1], s2);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(used + spans.at));
+        if (lane == 0) mbar_arrive(used + 8 * spans.at);
       }
       int tm, tn;
       walk.at(i, &tm, &tn);

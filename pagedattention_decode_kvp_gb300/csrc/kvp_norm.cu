@@ -295,7 +295,8 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s) {
-  if (p.out == nullptr) return bf16 ? launch_norm<true, true>(p, s) : launch_norm<false, true>(p, s);
+  if (p.out == nullptr)
+    return bf16 ? launch_norm<true, true>(p, s) : launch_norm<false, true>(p, s);
   return bf16 ? launch_norm<true, false>(p, s) : launch_norm<false, false>(p, s);
 }
 
