@@ -9,8 +9,8 @@
 // cores form the next group's.  Persistent: a pair walks the tiles; the warps that fetch
 // tiles and scales run on into the next one.
 //
-// Measured: 8192 x 8192 x 8192 445 us, 2470 TFLOP/s; 33098 x 12288 x 4096 1440 us, 2310;
-// 8191 x 10240 x 8192 548 us, 2500.  The products alone take 240 us of the first (4600
+// Measured: 8192 x 8192 x 8192 402 us, 2735 TFLOP/s; 33098 x 12288 x 4096 1312 us, 2540;
+// 8191 x 10240 x 8192 496 us, 2770.  The products alone take 240 us of the first (4600
 // TFLOP/s), with the fetches 283; the rest is the way round of a TMEM buffer (product,
 // commit, read, arrivals from both CTAs) and the 2 x 64 two-lane multiply-adds a thread
 // and group; run for seconds it is held by the board's power (1370 W, SM clock 1970 MHz,
@@ -27,7 +27,7 @@ namespace {
 constexpr int kTile = 256;                    // rows and columns of a pair's tile
 constexpr uint32_t kHalf = 128 * 128;         // bytes of a CTA's half of A or B per stage
 constexpr uint32_t kStage = 2 * kHalf;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kAddWarps = 8;
 constexpr int kCols = 128;                    // a thread's, of one row
 constexpr int kThreads = (kAddWarps + 4) * 32;   // three warpgroups
@@ -35,7 +35,7 @@ constexpr int kThreads = (kAddWarps + 4) * 32;   // three warpgroups
 constexpr int kAddRegs = 224;
 constexpr int kOtherRegs = 56;
 static_assert(kAddWarps * 32 * kAddRegs + 128 * kOtherRegs <= kThreads * 168, "registers");
-constexpr uint32_t kWarpBytes = 1024;         // each adding warp's, for its results
+constexpr uint32_t kWarpBytes = 4096;         // each adding warp's, for its results
 constexpr int kSpan = 8;                      // groups whose scales are staged at a time
 constexpr int kSpans = 4;                     // spans that are there
 constexpr int kPitch = 132;                   // floats from one group's row scales to the next's
@@ -293,17 +293,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       walk.at(i, &tm, &tn);
       const int m0 = tm * kTile + 128 * static_cast<int>(rank) + 32 * quarter;
       const int n0 = tn * kTile + first;
-      // ---- the warp's 32 rows, 32 bytes at a time through its shared memory
+      // ---- the warp's 32 rows, 128 bytes at a time through its shared memory
       __syncwarp();
       constexpr int kElem = kOut == KVP_F32 ? 4 : 2;
-      constexpr int kPiece = 32 / kElem;           // columns of a piece
+      constexpr int kPiece = 128 / kElem;          // columns of a piece
       const bool wide = p.out_stride * kElem % 16 == 0 &&
                         (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
       // unrolled: acc is indexed by constants
 #pragma unroll
       for (int c0 = 0; c0 < kCols; c0 += kPiece) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {              // 16 bytes of this lane's row
+        for (int q = 0; q < 8; ++q) {              // 16 bytes of this lane's row
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -316,25 +316,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok) w[e] = 0;
           }
-          piece[2 * lane + (q ^ (lane >> 2 & 1))] = make_uint4(w[0], w[1], w[2], w[3]);
+          piece[8 * lane + (q ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
         const int n = n0 + c0;
         if (wide && n + kPiece <= p.n) {
 #pragma unroll
-          for (int r = 0; r < 32; r += 16) {
-            const int row = r + lane / 2, q = lane & 1;
-            const uint4 v = piece[2 * row + (q ^ (row >> 2 & 1))];
+          for (int r = 0; r < 32; r += 4) {
+            const int row = r + lane / 8, q = lane & 7;
+            const uint4 v = piece[8 * row + (q ^ (row & 7))];
             if (m0 + row < p.m)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
                                         ((m0 + row) * p.out_stride + n) * kElem + 16 * q) = v;
           }
-        } else if (lane < kPiece && n + lane < p.n) {
-          const int q = lane * kElem / 16;
-          for (int r = 0; r < 32 && m0 + r < p.m; ++r) {
+        } else {
+#pragma unroll 4
+          for (int e = lane; e < 32 * kPiece; e += 32) {
+            const int r = e / kPiece, c = e % kPiece;
+            if (m0 + r >= p.m || n + c >= p.n) continue;
             const void* from = reinterpret_cast<const uint8_t*>(piece) +
-                               16 * (2 * r + (q ^ (r >> 2 & 1))) + lane * kElem % 16;
-            const long long to = (m0 + r) * p.out_stride + n + lane;
+                               16 * (8 * r + (c * kElem / 16 ^ (r & 7))) + c * kElem % 16;
+            const long long to = (m0 + r) * p.out_stride + n + c;
             if constexpr (kOut == KVP_F32)
               static_cast<float*>(p.out)[to] = *static_cast<const float*>(from);
             else
