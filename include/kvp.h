@@ -505,7 +505,8 @@ kvp_status kvp_release_tables(const int32_t* block_tables, int32_t max_blocks_pe
  * elements per token (1 head: the whole token; several: e.g. q's or key's heads in
  * front of kvp_rope_append), the heads of a token one behind the other, the token
  * strides in elements -- so x may be a slice of one projection's output.  weight:
- * [dim] of `dtype`.  dim: a multiple of 8, at most 32768; fewer than 2^31 rows.
+ * [dim] of `dtype`.  dim: a multiple of 8, at most 32768; fewer than 2^31 rows, and
+ * elements of a token.  eps: finite, not negative (with 0, a row of zeros gives NaN).
  * residual and residual_out: both or neither (NULL), with one head only.  out may be
  * x (same stride); residual_out may be residual or x (same stride); otherwise outputs
  * must not overlap an input or each other.  All rows 16-byte aligned, strides

@@ -504,10 +504,11 @@ kvp_status check_norm(const NormParams& p, kvp_dtype dtype) {
     return KVP_ERR_INVALID_ARG;
   if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return KVP_ERR_INVALID_ARG;
   if (p.dim % 8 != 0 || p.dim > kMaxNormDim) return KVP_ERR_UNSUPPORTED;
-  // CTAs of at least one row each
-  if (static_cast<long long>(p.num_tokens) * p.num_heads >= (1ll << 31)) return KVP_ERR_UNSUPPORTED;
-  if (p.num_tokens == 0) return KVP_OK;
+  // rows, and places within a token, are counted in 32 bits
   const int64_t n = static_cast<int64_t>(p.num_heads) * p.dim;
+  if (static_cast<int64_t>(p.num_tokens) * p.num_heads >= (1ll << 31) || n >= (1ll << 31))
+    return KVP_ERR_UNSUPPORTED;
+  if (p.num_tokens == 0) return KVP_OK;
   if (!rows16_ok(p.x, p.x_stride, n) || p.weight == nullptr || !aligned(p.weight, 16))
     return KVP_ERR_INVALID_ARG;
   if ((p.residual == nullptr) != (p.residual_out == nullptr)) return KVP_ERR_INVALID_ARG;
@@ -1173,8 +1174,8 @@ kvp_status kvp_quantise_fp8(uint8_t* codes, int64_t codes_stride, float* scales,
   KVP_NVTX_RANGE("kvp_quantise_fp8");
   if (rows < 0 || cols <= 0 || (dtype != KVP_F16 && dtype != KVP_BF16)) return KVP_ERR_INVALID_ARG;
   if (cols % 16 != 0 || (block_rows != 1 && block_rows != kScaleGroup)) return KVP_ERR_UNSUPPORTED;
-  if (static_cast<long long>(rows) * ((cols + kScaleGroup - 1) / kScaleGroup) >= (1ll << 31))
-    return KVP_ERR_UNSUPPORTED;
+  const int64_t groups = (static_cast<int64_t>(cols) + kScaleGroup - 1) / kScaleGroup;
+  if (cols > INT32_MAX - 127 || rows * groups >= (1ll << 31)) return KVP_ERR_UNSUPPORTED;
   if (rows == 0) return KVP_OK;
   if (!rows16_ok(x, x_stride, cols) || !codes_ok(codes, codes_stride, cols) || scales == nullptr ||
       !aligned(scales, 4))

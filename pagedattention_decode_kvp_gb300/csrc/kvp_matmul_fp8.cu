@@ -6,15 +6,22 @@
 // scales differ from group to group, so every group's sum is read into registers and
 // added there in float32: acc = fma(t, sa sb, acc).
 //
-// Here for few rows of A: the weight's 128 rows are the M side of the instruction (a
-// TMEM lane and a thread each), kTokens rows of A its N side.  Bound by the weight's
-// bytes, which a ring of TMA copies keeps on the way.  Warps: four that scale and add,
-// one each that fetches tiles, issues products and stages scales.  The products of kBatch
-// groups are handed over at a time, in one of two TMEM buffers: a hand-over takes about
-// 1000 cycles (two barriers, the read), more than the bytes of a group.  Where few tiles
-// meet many SMs, the CTAs of a cluster share a tile's K and add their sums through
+// Here for few rows of A: the weight's 128 rows are the M side of the instruction (a TMEM
+// lane each), kTokens rows of A its N side.  Bound by the weight's bytes, which a ring of
+// TMA copies keeps on the way, and by the start and end of a CTA (2.6 us).  Warps: those
+// that scale and add, one each that fetches tiles, issues products and stages scales.  The
+// products of kBatch groups are handed over at a time, in one of two TMEM buffers: a
+// hand-over takes about 1000 cycles (two barriers, the read), more than the bytes of a
+// group.  TMEM is read in pieces of 16 rows, whose lanes hold two columns in eight: with a
+// row to a lane every lane needs every token's scale, and those broadcasts took as many
+// cycles of shared memory as the operands (64 x 10240 x 8192 21.0 us, now 18.9).  Where few
+// tiles meet many SMs, the CTAs of a cluster share a tile's K and add their sums through
 // distributed shared memory, in the order of their ranks.  (kvp_matmul_fp8_pair.cu: many
 // rows.)
+//
+// Measured (us; at HBM's measured rate the bytes alone take): 1 x 768 x 512 2.9 (0.1), 1 x
+// 10240 x 8192 16.3 (12.6), 64 x 10240 x 8192 18.9 (12.8), 64 x 4096 x 4096 8.0 (2.6), 33 x
+// 32000 x 4096 with 32-bit results 25.7 (20.3), 128 x 10240 x 8192 27.4 (13.1).
 #include "kvp_matmul.cuh"
 
 namespace kvp {

@@ -296,6 +296,39 @@ def test_empty_calls():
     torch.cuda.synchronize()
 
 
+def test_offsets_past_32_bits():
+    """Rows more than 2^31 elements, and bytes, apart."""
+    T, D, N, step = 3, 256, 136, 2 ** 31 + 64
+    a, sa, b, sb = operands(T, N, D, 5)
+    want = gpu(T, N, dtype=torch.bfloat16)
+    kvp.kvp_matmul_fp8(want, a.cuda(), sa.cuda(), b.cuda(), sb.cuda())
+    far = torch.empty(2 * step + D, dtype=torch.bfloat16, device="cuda")
+    wide = far.as_strided((T, D), (step, 1))
+    bytes_ = far.view(U8).as_strided((T, D), (step, 1))
+    bytes_.copy_(a.cuda())
+    out = gpu(T, N, dtype=torch.bfloat16)
+    kvp.kvp_matmul_fp8(out, bytes_, sa.cuda(), b.cuda(), sb.cuda())
+    assert torch.equal(bits(out), bits(want))
+    kvp.kvp_matmul_fp8(wide[:, :N], a.cuda(), sa.cuda(), b.cuda(), sb.cuda())
+    assert torch.equal(bits(wide[:, :N]), bits(want))
+    x, w = randn((T, D), torch.bfloat16, 6).cuda(), weight(D, torch.bfloat16, 7).cuda()
+    y = torch.empty_like(x)
+    kvp.kvp_rms_norm(y, x, w, 1e-5)
+    wide.copy_(x)
+    kvp.kvp_rms_norm(wide, wide, w, 1e-5)
+    assert torch.equal(bits(wide), bits(y))
+    codes, scales = gpu(T, D, dtype=U8), gpu(T, 2, dtype=F32)
+    kvp.kvp_quantise_fp8(codes, scales, y)
+    kvp.kvp_quantise_fp8(bytes_, scales, y)
+    assert torch.equal(bytes_.cpu(), codes.cpu())
+    many = 2 ** 24 + 3                                  # rows x scales past 2^31 bytes
+    x = torch.zeros((many, 128), dtype=torch.float16, device="cuda")
+    x[-1, 5] = 7
+    out = torch.empty_like(x)
+    kvp.kvp_rms_norm(out, x, gpu(128, dtype=torch.float16, fill=1), 1e-6)
+    assert out[-1, 5] > 11 and not out[:-1].any()
+
+
 # ------------------------------------------------------------------ together
 def layer(T, hidden, Hq, Hkv, D, dtype, seed):
     """What a layer's attention keeps: norms, quantised weights, pools."""
@@ -446,6 +479,35 @@ def test_tensors_of_another_place_are_refused():
         kvp.kvp_rms_norm(x, x, x[0].cpu(), 1e-5)
     with pytest.raises(ValueError):
         kvp.kvp_quantise_fp8(gpu(2, 128, dtype=U8), torch.zeros(2, 1), x)
+
+
+def test_the_readmes_projections():
+    """The README's lines, as they stand there."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md"), encoding="utf-8") as f:
+        lines, = (b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "matmul_fp8" in b)
+    T, hidden, Hq, Hkv, D, dt = 5, 512, 4, 2, 64, torch.bfloat16
+    L = layer(T, hidden, Hq, Hkv, D, dt, 60)
+    x, r = randn((T, hidden), dt, 1).cuda(), randn((T, hidden), dt, 2).cuda()
+    out = randn((T, Hq, D), dt, 3).cuda()
+    v = dict(kvp=kvp, T=T, Hq=Hq, Hkv=Hkv, x=x.clone(), residual=r.clone(), norm_weight=L["w1"],
+             codes=gpu(T, hidden, dtype=U8), scales=gpu(T, 4, dtype=F32), qkv_codes=L["qkv"],
+             qkv_scales=L["qkv_s"], qkv=gpu(T, Hq + 2 * Hkv, D, dtype=dt), q_weight=L["wq"],
+             k_weight=L["wk"], out=out, out_codes=gpu(T, Hq * D, dtype=U8),
+             out_scales=gpu(T, 2, dtype=F32), o_codes=L["o"], o_scales=L["o_s"])
+    exec(lines, v)
+    assert torch.equal(bits(v["residual"]), bits(ref.total(x.cpu(), r.cpu())))
+    codes, scales = ref.quantise(out.cpu().view(T, -1))
+    assert torch.equal(v["out_codes"].cpu(), codes) and torch.equal(v["out_scales"].cpu(), scales)
+    want, size = ref.matmul(codes, scales, L["o"].cpu(), L["o_s"].cpu())
+    assert ((v["x"].cpu().double() - want).abs()
+            <= ref.matmul_bound(size, Hq * D, want, dt)).all()
+    want, size = ref.matmul(v["codes"].cpu(), v["scales"].cpu(), L["qkv"].cpu(), L["qkv_s"].cpu())
+    got = v["qkv"].cpu().view(T, -1).double()[:, (Hq + Hkv) * D:]
+    assert ((got - want[:, -got.shape[1]:]).abs()
+            <= ref.matmul_bound(size, hidden, want, dt)[:, -got.shape[1]:]).all()
 
 
 # ------------------------------------------------------------------ the compiled way

@@ -43,6 +43,7 @@ def test_norm(lib, fp8):
         assert call(H=0) == INVALID and call(H=2) == INVALID       # strides of one head
         assert call(H=2, D=512, r=A, rs=1024, ro=A, ros=1024) == UNSUPPORTED
         assert call(T=1 << 20, H=1 << 11, D=8, xs=1 << 14, os=1 << 14) == UNSUPPORTED
+        assert call(T=1, H=1 << 16, D=32768, xs=1 << 31, os=1 << 31) == UNSUPPORTED
 
 
 def test_quantise(lib):
@@ -58,6 +59,7 @@ def test_quantise(lib):
     assert call(s=None) == INVALID and call(s=A + 2) == INVALID
     assert call(cs=1000) == INVALID and call(cs=1032) == INVALID and call(xs=1020) == INVALID
     assert call(R=1 << 30, D=256, cs=256, xs=256) == UNSUPPORTED
+    assert call(R=1, D=2 ** 31 - 16, cs=2 ** 31, xs=2 ** 31) == UNSUPPORTED
 
 
 def test_matmul(lib):
