@@ -466,6 +466,57 @@ def test_the_same_call_gives_the_same_bits(M, N, K):
         assert torch.equal(bits(o), bits(outs[0]))
 
 
+def test_captured_products_beside_other_work():
+    """Products cut over clusters, by pairs and in one piece, captured into two graphs that
+    share their inputs, replayed on two streams beside an FP8 decode and a norm: the same
+    bits as alone."""
+    shapes = [(64, 2048, 4096), (1, 512, 2048), (128, 4096, 1024), (2600, 2048, 1024), (33, 8200, 256)]
+    calls = [[t.cuda() for t in operands(*s, seed=s[0])] for s in shapes]
+    want = [gpu(M, N, dtype=torch.bfloat16) for M, N, _ in shapes]
+    for o, c in zip(want, calls):
+        kvp.kvp_matmul_fp8(o, *c)
+    B, Hkv, D, MB = 16, 2, 128, 64
+    codes = torch.randint(0, 120, (2, B * MB, Hkv, 16, D), dtype=U8).cuda()
+    pool_scales = torch.rand((2, B * MB, Hkv, 16)).cuda()
+    tables = torch.arange(B * MB, dtype=torch.int32, device="cuda").view(B, MB)
+    lens = torch.full((B,), 16 * MB, dtype=torch.int32, device="cuda")
+    q = randn((B, 8, D), torch.bfloat16, 1).cuda()
+    x, w = randn((500, 1024), torch.bfloat16, 2).cuda(), weight(1024, torch.bfloat16, 3).cuda()
+
+    def decode(out, ws):
+        kvp.kvp_attention_decode_fp8(out, q, *codes, *pool_scales, tables, lens, 0.05, workspace=ws,
+                                     partition_blocks=16)
+
+    nbytes = kvp.kvp_decode_workspace_bytes(B, 8, kvp.cache_desc(codes[0]), MB, 16, kv_fp8=True)
+    ws = [gpu(nbytes, dtype=U8) for _ in range(2)]
+    att, norm = torch.empty_like(q), torch.empty_like(x)
+    decode(att, ws[0])
+    kvp.kvp_rms_norm(norm, x, w, 1e-5)
+    torch.cuda.synchronize()
+    sides = []
+    for side in range(2):
+        outs = [gpu(M, N, dtype=torch.bfloat16) for M, N, _ in shapes]
+        rest = torch.empty_like(q), torch.empty_like(x)
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            for i in range(10):
+                j = (i * (side + 1) + side) % len(shapes)
+                kvp.kvp_matmul_fp8(outs[j], *calls[j])
+                decode(rest[0], ws[side])
+                kvp.kvp_rms_norm(rest[1], x, w, 1e-5)
+        sides.append((stream, graph, outs, rest))
+    for _ in range(5):
+        for stream, graph, *_ in sides:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, outs, rest in sides:
+        for o, v in zip(outs, want):
+            assert torch.equal(bits(o), bits(v))
+        assert torch.equal(bits(rest[0]), bits(att)) and torch.equal(bits(rest[1]), bits(norm))
+
+
 def test_tensors_of_another_place_are_refused():
     a, sa, b, sb = operands(2, 128, 128, 1)
     out = gpu(2, 128, dtype=F32)
