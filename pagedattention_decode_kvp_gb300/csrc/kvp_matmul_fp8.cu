@@ -382,8 +382,8 @@ cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, con
 // another CTA, the exchange of a cluster's sums, and the bytes of a and b at the rate of HBM.
 // Measured and modelled (tokens x splits): 16 x 10240 x 8192 16x1 18.6 and 18.0, 16x3 16.9 and
 // 15.8; 64 x 4096 x 4096 32x4 8.2 and 7.7, 64x4 8.7 and 8.5, 64x1 14.0 and 13.8; 64 x 10240 x
-// 8192 64x3 19.1 and 17.9, 64x1 24.3 and 25.0; 256 x 4096 x 4096 128x2 12.9 and 12.5, pairs 20.7
-// and 20.5; 517 x 4096 x 4096 128x1 27.3 and 34.0, pairs 21.0 and 20.5.
+// 8192 64x3 19.1 and 17.9, 64x1 24.3 and 25.0; 256 x 4096 x 4096 128x2 12.9 and 12.5, pairs 17.4
+// and 18.2; 517 x 4096 x 4096 128x1 27.3 and 34.0, pairs 18.6 and 18.2.
 MatmulPlan matmul_plan(int m, int n, int groups) {
   struct Kind {
     int tokens, resident;      // rows of a per tile, CTAs of an SM
@@ -397,7 +397,7 @@ MatmulPlan matmul_plan(int m, int n, int groups) {
                              {128, 1, 0.45, 0.45}};
   const auto tiles = [](long long x, int per) { return (x + per - 1) / per; };
   MatmulPlan plan{256, 1};
-  double best = 3.5 + 0.53 * groups * tiles(tiles(m, 256) * tiles(n, 256), kNumSms / 2);
+  double best = 3.5 + 0.46 * groups * tiles(tiles(m, 256) * tiles(n, 256), kNumSms / 2);
   const double bytes = 2.6 + (static_cast<double>(m) + n) * groups * 128 / 6.5e6;
   for (const Kind& k : kKinds) {
     if (k.tokens >= 2 * m && k.tokens > 16) break;   // (a smaller one holds all rows)
