@@ -1202,7 +1202,7 @@ kvp_status kvp_matmul_fp8(void* out, int64_t out_stride, kvp_dtype out_dtype, co
       (out_dtype != KVP_F16 && out_dtype != KVP_BF16 && out_dtype != KVP_F32))
     return KVP_ERR_INVALID_ARG;
   if (k % 16 != 0 || k > INT32_MAX - 127) return KVP_ERR_UNSUPPORTED;
-  if (n > INT32_MAX - 127 || m > INT32_MAX - 255) return KVP_ERR_UNSUPPORTED;
+  if (n > INT32_MAX - 255 || m > INT32_MAX - 255) return KVP_ERR_UNSUPPORTED;
   if (m == 0) return KVP_OK;
   if (!codes_ok(a, a_stride, k) || !codes_ok(b, b_stride, k) || a_scale == nullptr ||
       b_scale == nullptr || !aligned(a_scale, 4) || !aligned(b_scale, 4))

@@ -9,15 +9,16 @@
 // cores form the next group's.  Persistent: a pair walks the tiles; the warps that fetch
 // tiles and scales run on into the next one.
 //
-// Measured: 8192 x 8192 x 8192 402 us, 2735 TFLOP/s; 33098 x 12288 x 4096 1312 us, 2540;
-// 8191 x 10240 x 8192 496 us, 2770.  The products alone take 240 us of the first (4600
+// Measured: 8192 x 8192 x 8192 395 us, 2780 TFLOP/s; 33098 x 12288 x 4096 1310 us, 2540;
+// 8191 x 10240 x 8192 500 us, 2750.  The products alone take 240 us of the first (4600
 // TFLOP/s), with the fetches 283; the rest is the way round of a TMEM buffer (product,
-// commit, read, arrivals from both CTAs) and the 2 x 64 two-lane multiply-adds a thread
-// and group; run for seconds it is held by the board's power (1370 W, SM clock 1970 MHz,
-// 2220 TFLOP/s).  Tried: 16 adding warps of 64 columns (their 104 registers cost moves and
-// spills: 502 us), 16 columns a read (449), halves of 128 columns with a warp and buffers
-// each (equal, and A read twice from shared memory), the next group's first read ahead of
-// this one's last sums (501).
+// commit, read, arrivals from both CTAs: 900 cycles a group where the product takes 512).
+// Run for seconds it is held by the board's power (1350 W, SM clock 1640 MHz, 2300
+// TFLOP/s).  Tried, on the first shape: 16 adding warps of 64 columns (their 104 registers
+// cost moves and spills: 502 us), 16 columns a read (449), the next group's first read
+// ahead of this one's last sums (501), halves of 128 columns with a warp, barriers and
+// buffers each (430), tiles of 192 columns (506: a group takes as long), the issuing warp's
+// loop by one lane (411), a look at the next buffer before the last sums (407).
 #include "kvp_matmul.cuh"
 
 namespace kvp {
