@@ -19,9 +19,9 @@
 // distributed shared memory, in the order of their ranks.  (kvp_matmul_fp8_pair.cu: many
 // rows.)
 //
-// Measured (us; at HBM's measured rate the bytes alone take): 1 x 768 x 512 2.9 (0.1), 1 x
-// 10240 x 8192 16.3 (12.6), 64 x 10240 x 8192 18.9 (12.8), 64 x 4096 x 4096 8.0 (2.6), 33 x
-// 32000 x 4096 with 32-bit results 25.7 (20.3), 128 x 10240 x 8192 27.4 (13.1).
+// Measured (us; at HBM's measured rate the bytes alone take): 1 x 768 x 512 2.8 (0.1), 1 x
+// 10240 x 8192 16.0 (12.6), 64 x 10240 x 8192 18.8 (12.8), 64 x 4096 x 4096 8.0 (2.6), 33 x
+// 32000 x 4096 with 32-bit results 24.4 (20.3), 128 x 10240 x 8192 26.7 (13.1).
 #include "kvp_matmul.cuh"
 
 namespace kvp {
@@ -33,6 +33,7 @@ constexpr uint32_t kTileB = kRowsB * 128;    // bytes of a stage's weight tile
 constexpr int kMaxSplits = 8;                // CTAs of a portable cluster
 constexpr int kSpan = 16;                    // groups whose scales are staged at a time
 constexpr int kSpans = 2;
+constexpr int kSumPitch = kRowsB + 4;        // floats from one token's sums to the next's
 
 template <int kTokens>
 struct Shape {
@@ -52,7 +53,7 @@ struct Shape {
   static constexpr uint32_t kTmem = 2 * kBatch * kTokens;
   static_assert(kSmem * kCtas <= (kCtas == 2 ? 226 : 227) * 1024, "shared memory of an SM");
   static_assert(kTmem * kCtas <= 512 && kSpan % kBatch == 0, "TMEM, spans of whole batches");
-  static_assert(kStages * kStage >= kTokens * (kRowsB + 4) * 4, "the sums lie in the ring");
+  static_assert(kStages * kStage >= kTokens * kSumPitch * 4, "the sums lie in the ring");
 };
 
 // 16 rows x 8 kReps columns of TMEM: lane l holds columns 8 j + 2 (l % 4) and the next of rows
@@ -77,12 +78,65 @@ __device__ __forceinline__ void load_16(uint32_t taddr, uint32_t (&r)[4 * kReps]
   }
 }
 
-// grid.x = (token tile, weight tile, rank of the cluster), the last running fastest.
-template <int kTokens>
+// Results of tokens begin, begin + kWarps, ... < end of the tile: a warp takes a token, a lane
+// four weight rows; the sums of the CTAs of the cluster (at most kSplits) are added in the
+// order of their ranks, kAtOnce tokens at a time.
+template <int kAtOnce, int kSplits, int kWarps>
+__device__ __forceinline__ void write_sums(const MatmulParams& p, const float* mine, int splits,
+                                           int begin, int end, int m0, int n0, bool bad) {
+  const int n4 = n0 + 4 * static_cast<int>(threadIdx.x % 32);
+  const uint32_t from = dev::smem_addr(mine + 4 * (threadIdx.x % 32));
+  const bool whole = n4 + 4 <= p.n && p.out_stride % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(p.out) % (p.out_type == KVP_F32 ? 16 : 8) == 0;
+  for (int j0 = begin; j0 < end; j0 += kWarps * kAtOnce) {
+    float4 v[kAtOnce][kSplits];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int r = 0; r < kSplits; ++r)
+        if (r < splits && j0 + u * kWarps < end) {
+          const int at = (j0 + u * kWarps) * kSumPitch;
+          if constexpr (kSplits == 1)
+            v[u][r] = *reinterpret_cast<const float4*>(mine + at + 4 * (threadIdx.x % 32));
+          else
+            v[u][r] = mm::load_remote4(mm::at_rank(from + 4 * at, r));
+        }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int j = j0 + u * kWarps;
+      if (j >= end) continue;
+      float4 x = v[u][0];
+#pragma unroll
+      for (int r = 1; r < kSplits; ++r) {
+        if (r < splits) {
+          x.x += v[u][r].x;
+          x.y += v[u][r].y;
+          x.z += v[u][r].z;
+          x.w += v[u][r].w;
+        }
+      }
+      if (bad) x = make_float4(0.f, 0.f, 0.f, 0.f);
+      const long long at = static_cast<long long>(m0 + j) * p.out_stride + n4;
+      if (whole) {
+        mm::store_out4(p, at, x);
+      } else {
+        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n4 + i < p.n) mm::store_out(p, at + i, y[i]);
+      }
+    }
+  }
+}
+
+// grid.x = (token tile, weight tile, rank of the cluster), the last running fastest.  Tiles
+// of one CTA (not kCluster) have a kernel of their own: less code to fetch.
+template <int kTokens, bool kCluster>
 __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCtas)
-    matmul_fp8_kernel(const MatmulParams p, int splits, const __grid_constant__ CUtensorMap ta,
+    matmul_fp8_kernel(const MatmulParams p, int ctas, const __grid_constant__ CUtensorMap ta,
                       const __grid_constant__ CUtensorMap tb) {
   using namespace dev;
+  const int splits = kCluster ? ctas : 1;
   using S = Shape<kTokens>;
   constexpr int kAddWarps = S::kAddWarps;
   constexpr uint32_t kInstr = umma::instr_desc_f16(kRowsB, kTokens, false, false, false);
@@ -99,7 +153,7 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
   uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ volatile int failed;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = splits > 1 ? mm::cluster_rank() : 0;
+  const uint32_t rank = kCluster ? mm::cluster_rank() : 0;
   const long long tile = blockIdx.x / splits;
   const int tiles_n = (p.n + kRowsB - 1) / kRowsB;
   const int n0 = static_cast<int>(tile % tiles_n) * kRowsB;
@@ -282,7 +336,6 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
 
   // ---- the sums go through shared memory, a cluster's to all of its CTAs: each adds and
   // writes its share of the tokens
-  constexpr int kSumPitch = kRowsB + 4;
   float* mine = reinterpret_cast<float*>(sm);   // [kTokens][kSumPitch]
   if (warp < kAddWarps) {
     float* to = mine + (col + 2 * (lane % 4)) * kSumPitch + warp % 4 * 32 + lane / 4;
@@ -295,7 +348,7 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
         to[(8 * j + 1) * kSumPitch + 8 * i] = v.y;
       }
   }
-  if (splits > 1) {
+  if constexpr (kCluster) {
     if (bad && tid < splits)
       mm::store_remote(mm::at_rank(smem_addr(const_cast<int*>(&failed)), tid), 1);
     mm::cluster_sync();
@@ -304,56 +357,20 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
     __syncthreads();
   }
   if (warp < kAddWarps) {
-    // a warp takes a token, a lane four weight rows
-    constexpr int kAtOnce = kTokens == 64 ? 1 : 2;   // (registers)
+    const int begin = static_cast<int>(kTokens * rank / splits) + warp;
     const int end = min(static_cast<int>(kTokens * (rank + 1) / splits), p.m - m0);
-    const int n4 = n0 + 4 * lane;
-    const bool whole = n4 + 4 <= p.n && p.out_stride % 4 == 0 &&
-                       reinterpret_cast<uintptr_t>(p.out) % (p.out_type == KVP_F32 ? 16 : 8) == 0;
-    for (int j0 = kTokens * rank / splits + warp; j0 < end; j0 += kAddWarps * kAtOnce) {
-      float4 v[kAtOnce][kMaxSplits];
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-          if (r < splits && j0 + u * kAddWarps < end)
-            v[u][r] = mm::load_remote4(
-                mm::at_rank(smem_addr(mine + (j0 + u * kAddWarps) * kSumPitch + 4 * lane), r));
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int j = j0 + u * kAddWarps;
-        if (j >= end) continue;
-        float4 x = v[u][0];
-#pragma unroll
-        for (int r = 1; r < kMaxSplits; ++r) {
-          if (r < splits) {
-            x.x += v[u][r].x;
-            x.y += v[u][r].y;
-            x.z += v[u][r].z;
-            x.w += v[u][r].w;
-          }
-        }
-        if (bad) x = make_float4(0.f, 0.f, 0.f, 0.f);
-        const long long at = static_cast<long long>(m0 + j) * p.out_stride + n4;
-        if (whole) {
-          mm::store_out4(p, at, x);
-        } else {
-          const float y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n4 + i < p.n) mm::store_out(p, at + i, y[i]);
-        }
-      }
-    }
+    constexpr int kAtOnce = kCluster ? (kTokens == 64 ? 1 : 2) : 4;
+    write_sums<kAtOnce, kCluster ? kMaxSplits : 1, kAddWarps>(p, mine, splits, begin, end, m0, n0,
+                                                              bad);
   }
-  if (splits > 1) mm::cluster_sync();
+  if constexpr (kCluster) mm::cluster_sync();
 }
 
-template <int kTokens>
-cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, const CUtensorMap& tb,
-                   cudaStream_t s) {
+template <int kTokens, bool kCluster>
+cudaError_t launch_kernel(const MatmulParams& p, int splits, const CUtensorMap& ta,
+                          const CUtensorMap& tb, cudaStream_t s) {
   using S = Shape<kTokens>;
-  auto kernel = matmul_fp8_kernel<kTokens>;
+  auto kernel = matmul_fp8_kernel<kTokens, kCluster>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), S::kSmem);
   if (e != cudaSuccess) return e;
   const long long tiles = static_cast<long long>((p.n + kRowsB - 1) / kRowsB) *
@@ -371,8 +388,15 @@ cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, con
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
+  cfg.numAttrs = kCluster ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, splits, ta, tb);
+}
+
+template <int kTokens>
+cudaError_t launch(const MatmulParams& p, int splits, const CUtensorMap& ta, const CUtensorMap& tb,
+                   cudaStream_t s) {
+  return splits > 1 ? launch_kernel<kTokens, true>(p, splits, ta, tb, s)
+                    : launch_kernel<kTokens, false>(p, splits, ta, tb, s);
 }
 
 }  // namespace
