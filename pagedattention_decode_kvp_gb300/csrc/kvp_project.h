@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kvp_internal.h"
+#include "kvp_matmul_plan.h"
 
 namespace kvp {
 
@@ -41,17 +42,6 @@ struct MatmulParams {
   int32_t m, n, groups;       // groups = ceil(K / 128)
   int32_t out_type;           // a kvp_dtype
 };
-
-constexpr int kNumSms = 152;
-
-// How a matrix product is cut (matmul_plan).
-struct MatmulPlan {
-  int tokens;                 // rows of a per tile (256: pairs of CTAs)
-  int splits;                 // CTAs that share a tile's K
-  int box() const { return tokens < 128 ? tokens : 128; }   // rows of a per copy
-  int box_b() const { return tokens == 256 ? 64 : 128; }    // rows of b
-};
-MatmulPlan matmul_plan(int m, int n, int groups);
 
 cudaError_t launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_quantise_fp8(const QuantiseParams& p, bool bf16, cudaStream_t s);
