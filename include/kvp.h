@@ -510,8 +510,9 @@ kvp_status kvp_release_tables(const int32_t* block_tables, int32_t max_blocks_pe
  * residual and residual_out: both or neither (NULL), with one head only.  out may be
  * x (same stride); residual_out may be residual or x (same stride); otherwise outputs
  * must not overlap an input or each other.  All rows 16-byte aligned, strides
- * multiples of 8.  Squares are summed in float32: elements of 2^63 and more (bf16)
- * give a row of zeros.
+ * multiples of 8.  Squares are summed in float32, of rows for which that is too small a
+ * range (bf16 elements from some 2^56 on, or below 2^-40 with an eps below 2^-100) scaled by
+ * a power of two: any finite row has its norm.
  */
 kvp_status kvp_rms_norm(void* out, int64_t out_stride, const void* x, int64_t x_stride,
                         const void* residual, int64_t residual_stride, void* residual_out,

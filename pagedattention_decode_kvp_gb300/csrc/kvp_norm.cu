@@ -79,12 +79,111 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
+// Sum of the values of a row's `kThreads` neighbouring threads (part: kThreads / 32 floats
+// where they are a CTA).
+template <int kThreads>
+__device__ __forceinline__ float row_sum(float sum, float* part) {
+#pragma unroll
+  for (int o = (kThreads < 32 ? kThreads : 32) / 2; o > 0; o >>= 1)
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if constexpr (kThreads > 32) {
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
+  }
+  return sum;
+}
+
+__device__ __forceinline__ float mean_square(float sum, int dim, float eps) {
+  return __fadd_rn(__fdiv_rn(sum, static_cast<float>(dim)), eps);
+}
+
+__device__ __forceinline__ uint4 load_weight(const NormParams& p, int at) {
+  return at < p.dim ? load16(p.weight + at) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Results of 8 elements x of a row: token t, `at` elements behind the row's start, which is
+// col elements behind the token's; r: the row's factor; weight: that of the elements.  Lanes
+// that hold none (not `mine`) only take part in a group's maximum.
+template <bool kBf16, bool kFp8, int kThreads>
+__device__ __forceinline__ void put_results(const NormParams& p, uint32_t t, uint32_t col, int at,
+                                            bool mine, float (&x)[8], float r,
+                                            const uint4& weight) {
+  float w[8];
+  widen<kBf16>(weight, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+  if constexpr (kFp8) {
+    const float most = lanes_max<(kThreads < 16 ? kThreads : 16)>(mine ? absmax8(x) : 0.f);
+    float up;
+    const float scale = group_scale(most, &up);
+    if (mine) {
+      *reinterpret_cast<uint2*>(p.codes + t * p.codes_stride + at) = codes8(x, up);
+      if (at % kScaleGroup == 0)
+        p.scales[static_cast<size_t>(t) * ((p.dim + kScaleGroup - 1) / kScaleGroup) +
+                 at / kScaleGroup] = scale;
+    }
+  } else if (mine) {
+    *reinterpret_cast<uint4*>(p.out + t * p.out_stride + col + at) = narrow<kBf16>(x);
+  }
+}
+
+// Whether a row's mean square does not give its factor: bf16 elements reach from 2^-133 to
+// 2^128, their squares leave float32 (at 2^-100 those that vanish do not count any more).
+__device__ __forceinline__ bool out_of_range(float mean) {
+  constexpr uint32_t kLow = 27u << 23;   // 2^-100
+  return __float_as_uint(mean) - kLow >= (255u << 23) - kLow;
+}
+
+// A row of bf16 beside, or itself, one that is out of range: read once more (with a
+// residual, the sum that this thread wrote) and scaled by a power of two, a large one, its
+// elements up to 2^128, by 2^-80, a small one, all of it below 2^-40, by 2^100.  Of a large
+// row's factor half of the power stays with the elements, so that neither leaves float32.
+// A row in range gets the bits that it has elsewhere.
+template <bool kFp8, int kThreads, int kChunks>
+__device__ __forceinline__ void put_far_row(const NormParams& p, uint32_t t, uint32_t col, bool in,
+                                            float mean, float* part) {
+  const int lane = static_cast<int>(threadIdx.x) % kThreads;
+  const uint16_t* h = p.residual != nullptr ? p.residual_out + t * p.residual_out_stride
+                                            : p.x + t * p.x_stride + col;
+  float up = 1.f, more = 1.f;
+  if (out_of_range(mean)) up = mean < 1.f ? 0x1p100f : 0x1p-40f;
+  if (up < 1.f) more = up;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < kChunks; ++c) {
+    const int at = 8 * (lane + c * kThreads);
+    float x[8];
+    widen<true>(in && at < p.dim ? load16(h + at) : make_uint4(0u, 0u, 0u, 0u), x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(x[i] * up * more, x[i] * up * more, sum);
+  }
+  if constexpr (kThreads > 32) __syncthreads();   // (part has been read)
+  sum = row_sum<kThreads>(sum, part);
+  const float r =
+      __frsqrt_rn(mean_square(sum, p.dim, p.eps * (up * more) * (up * more))) * more;
+#pragma unroll 1
+  for (int c = 0; c < kChunks; ++c) {
+    const int at = 8 * (lane + c * kThreads);
+    float x[8];
+    widen<true>(in && at < p.dim ? load16(h + at) : make_uint4(0u, 0u, 0u, 0u), x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= up;
+    put_results<true, kFp8, kThreads>(p, t, col, at, in && at < p.dim, x, r,
+                                      load_weight(p, at));
+  }
+}
+
 // kThreads threads hold a row, kChunks chunks each; up to 32 of them: 128 / kThreads slots
-// to a CTA, kRows rows a slot, fetched together; more: a CTA to a row.
-template <bool kBf16, bool kFp8, int kThreads, int kChunks, int kRows>
+// to a CTA, kRows rows a slot, fetched together; more: a CTA to a row.  kAhead: the weight is
+// fetched beside the row.  Its registers cost a prompt's kernels warps (8191 rows of 8192 with
+// a residual 78 us, 85 so), a step's CTAs, one to an SM, nothing (64 such rows 2.5 us, 2.3).
+template <bool kBf16, bool kFp8, int kThreads, int kChunks, int kRows, bool kAhead>
 __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kernel(NormParams p) {
   constexpr int kSlots = kThreads < 128 ? 128 / kThreads : 1;
-  constexpr int kGroupLanes = kThreads < 16 ? kThreads : 16;
+  __shared__ float part[kThreads > 32 ? kThreads / 32 : 1];
   dev::grid_dependency_wait();
   dev::launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kThreads;
@@ -109,6 +208,11 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kern
       }
     }
   }
+  uint4 weight[kAhead ? kChunks : 1];
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) weight[c] = load_weight(p, 8 * (lane + c * kThreads));
+  }
   float sums[kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
@@ -131,24 +235,24 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kern
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
     }
-#pragma unroll
-    for (int o = (kThreads < 32 ? kThreads : 32) / 2; o > 0; o >>= 1)
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if constexpr (kThreads > 32) {
-      __shared__ float part[kThreads / 32];
-      if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
-      __syncthreads();
-      sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) sum += part[i];
-    }
-    sums[j] = sum;
+    sums[j] = row_sum<kThreads>(sum, part);
   }
   // lane j % kRows of a row's lanes works out row j's factor for all of them
   float mine_r = sums[0];
 #pragma unroll
   for (int j = 1; j < kRows; ++j) mine_r = lane % kRows == j ? sums[j] : mine_r;
-  mine_r = __frsqrt_rn(__fadd_rn(__fdiv_rn(mine_r, static_cast<float>(p.dim)), p.eps));
+  mine_r = mean_square(mine_r, p.dim, p.eps);
+  // (a vote of the warp: its rows stay together; of a CTA with one row all threads agree)
+  if constexpr (kBf16) {
+    if (__any_sync(0xffffffffu, out_of_range(mine_r))) {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        put_far_row<kFp8, kThreads, kChunks>(p, t[j], col[j], in[j],
+                                             mean_square(sums[j], p.dim, p.eps), part);
+      return;
+    }
+  }
+  mine_r = __frsqrt_rn(mine_r);
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     float r = mine_r;
@@ -156,25 +260,10 @@ __global__ void __launch_bounds__(kThreads < 128 ? 128 : kThreads) rms_norm_kern
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int at = 8 * (lane + c * kThreads);
-      const bool mine = in[j] && at < p.dim;
-      float x[8], w[8];
+      float x[8];
       widen<kBf16>(raw[j][c], x);
-      widen<kBf16>(at < p.dim ? load16(p.weight + at) : make_uint4(0u, 0u, 0u, 0u), w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-      if constexpr (kFp8) {
-        const float most = lanes_max<kGroupLanes>(mine ? absmax8(x) : 0.f);
-        float up;
-        const float scale = group_scale(most, &up);
-        if (mine) {
-          *reinterpret_cast<uint2*>(p.codes + t[j] * p.codes_stride + at) = codes8(x, up);
-          if (at % kScaleGroup == 0)
-            p.scales[static_cast<size_t>(t[j]) * ((p.dim + kScaleGroup - 1) / kScaleGroup) +
-                     at / kScaleGroup] = scale;
-        }
-      } else if (mine) {
-        *reinterpret_cast<uint4*>(p.out + t[j] * p.out_stride + col[j] + at) = narrow<kBf16>(x);
-      }
+      put_results<kBf16, kFp8, kThreads>(p, t[j], col[j], at, in[j] && at < p.dim, x, r,
+                                         kAhead ? weight[c] : load_weight(p, at));
     }
   }
 }
@@ -280,8 +369,11 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
 #define KVP_NORM(T, C, R)                                                               \
   {                                                                                     \
     constexpr int kPer = R * (T < 128 ? 128 / T : 1);                                   \
-    return launch_pdl(rms_norm_kernel<kBf16, kFp8, T, C, R>,                            \
-                      dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),            \
+    auto kernel = rms_norm_kernel<kBf16, kFp8, T, C, R, false>;                         \
+    if constexpr (T >= 128) {                                                           \
+      if (rows <= kNumSms) kernel = rms_norm_kernel<kBf16, kFp8, T, C, R, true>;        \
+    }                                                                                   \
+    return launch_pdl(kernel, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),    \
                       dim3(T < 128 ? 128 : T), 0, s, p);                                \
   }
   if (chunks <= 8) KVP_NORM(8, 1, 4)
