@@ -550,7 +550,7 @@ kvp_status kvp_quantise_fp8(uint8_t* codes, int64_t codes_stride, float* scales,
  * b_scale: [ceil(n / 128), ceil(k / 128)]; rows of a and b a_stride and b_stride bytes
  * apart.  The sum of a group is formed by the tensor cores, scaled and added to the
  * others in float32, and rounded once to out's type (fp16, bf16 or float32).
- * k: a multiple of 16; m and n: any.  a, b and their strides are multiples of 16
+ * k: a multiple of 16; n: at least 1, m: any.  a, b and their strides are multiples of 16
  * bytes; out: rows of n elements, out_stride >= n elements apart, aligned to its type.
  * A NaN code, or a scale that is no number, gives NaN in the rows (columns) it
  * belongs to.  A product of two scales must lie in float32's normal range.  out must
@@ -562,6 +562,13 @@ kvp_status kvp_matmul_fp8(void* out, int64_t out_stride, kvp_dtype out_dtype, co
                           int64_t a_stride, const float* a_scale, const uint8_t* b,
                           int64_t b_stride, const float* b_scale, int32_t m, int32_t n, int32_t k,
                           int32_t* dev_status, kvp_stream_t stream);
+
+/*
+ * kvp_matmul_fp8_plan -- how kvp_matmul_fp8 cuts a product of these sizes (m > 0), for
+ * profiles and tests; answered on the host.  *tokens: rows of a per tile, 16, 32, 64 or
+ * 128, or 256: tiles of 256 x 256 by pairs of CTAs; *splits: CTAs that share a tile's k.
+ */
+kvp_status kvp_matmul_fp8_plan(int32_t m, int32_t n, int32_t k, int32_t* tokens, int32_t* splits);
 
 /*
  * kvp_attention_prefill -- causal multi-query paged attention over fp16/bf16

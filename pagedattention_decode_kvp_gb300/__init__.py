@@ -118,6 +118,7 @@ SIGNATURES = {
                                 _P]),
     "kvp_quantise_fp8": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _I32, _I32, _P]),
     "kvp_matmul_fp8": (_I32, [_P, _I64, _I32, _P, _I64, _P, _P, _I64, _P, _I32, _I32, _I32, _P, _P]),
+    "kvp_matmul_fp8_plan": (_I32, [_I32, _I32, _I32, _P, _P]),
     "kvp_read_status": (_I32, [_P, _P]),
     "kvp_selftest_wait_timeout": (_I32, [_P, _I64, _P]),
     "kvp_bm_create": (_P, [_I32, _I32, _I64]),
@@ -997,6 +998,17 @@ def kvp_matmul_fp8(out, a, a_scale, b, b_scale, *, status=None, stream=None) -> 
     _check(lib.kvp_matmul_fp8(out.data_ptr(), os_, code, a.data_ptr(), as_, a_scale.data_ptr(),
                               b.data_ptr(), bs, b_scale.data_ptr(), M, N, K, _status_ptr(status), s),
            "kvp_matmul_fp8")
+
+
+def kvp_matmul_fp8_plan(m, n, k) -> tuple:
+    """(tokens, splits) of kvp_matmul_fp8 for these sizes: rows of a per tile (256: pairs
+    of CTAs on 256 x 256) and CTAs that share a tile's k."""
+    tokens, splits = ctypes.c_int32(), ctypes.c_int32()
+    for x, name in ((m, "m"), (n, "n"), (k, "k")):
+        _int32(x, name)
+    _check(load_library().kvp_matmul_fp8_plan(int(m), int(n), int(k), ctypes.byref(tokens),
+                                              ctypes.byref(splits)), "kvp_matmul_fp8_plan")
+    return tokens.value, splits.value
 
 
 def kvp_selftest_wait_timeout(status, limit_ns, stream=None):

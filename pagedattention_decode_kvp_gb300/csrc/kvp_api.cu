@@ -520,6 +520,18 @@ kvp_status check_norm(const NormParams& p, kvp_dtype dtype) {
   return KVP_OK;
 }
 
+// The cut of a product of these sizes, if it can be made (m == 0: nothing to cut).
+kvp_status cut_matmul(int32_t m, int32_t n, int32_t k, MatmulPlan* plan) {
+  if (m < 0 || n <= 0 || k <= 0) return KVP_ERR_INVALID_ARG;
+  if (k % 16 != 0 || k > INT32_MAX - 127) return KVP_ERR_UNSUPPORTED;
+  if (n > INT32_MAX - 255 || m > INT32_MAX - 255) return KVP_ERR_UNSUPPORTED;
+  if (m == 0) return KVP_OK;
+  *plan = matmul_plan(m, n, (k + kScaleGroup - 1) / kScaleGroup);
+  const long long ctas = static_cast<long long>((m + plan->tokens - 1) / plan->tokens) *
+                         ((n + kScaleGroup - 1) / kScaleGroup) * plan->splits;
+  return ctas < (1ll << 31) ? KVP_OK : KVP_ERR_UNSUPPORTED;
+}
+
 // TMA descriptor over codes [rows][k], `stride` bytes from row to row: a box is 128
 // bytes of `box_rows` rows, written with the 128-byte swizzle (K-major operand);
 // what lies past k or rows arrives as zeros.
@@ -1198,12 +1210,11 @@ kvp_status kvp_matmul_fp8(void* out, int64_t out_stride, kvp_dtype out_dtype, co
                           int64_t b_stride, const float* b_scale, int32_t m, int32_t n, int32_t k,
                           int32_t* dev_status, kvp_stream_t stream) {
   KVP_NVTX_RANGE("kvp_matmul_fp8");
-  if (m < 0 || n <= 0 || k <= 0 ||
-      (out_dtype != KVP_F16 && out_dtype != KVP_BF16 && out_dtype != KVP_F32))
+  if (out_dtype != KVP_F16 && out_dtype != KVP_BF16 && out_dtype != KVP_F32)
     return KVP_ERR_INVALID_ARG;
-  if (k % 16 != 0 || k > INT32_MAX - 127) return KVP_ERR_UNSUPPORTED;
-  if (n > INT32_MAX - 255 || m > INT32_MAX - 255) return KVP_ERR_UNSUPPORTED;
-  if (m == 0) return KVP_OK;
+  MatmulPlan plan;
+  kvp_status st = cut_matmul(m, n, k, &plan);
+  if (st != KVP_OK || m == 0) return st;
   if (!codes_ok(a, a_stride, k) || !codes_ok(b, b_stride, k) || a_scale == nullptr ||
       b_scale == nullptr || !aligned(a_scale, 4) || !aligned(b_scale, 4))
     return KVP_ERR_INVALID_ARG;
@@ -1220,15 +1231,21 @@ kvp_status kvp_matmul_fp8(void* out, int64_t out_stride, kvp_dtype out_dtype, co
   p.n = n;
   p.groups = (k + kScaleGroup - 1) / kScaleGroup;
   p.out_type = out_dtype;
-  const MatmulPlan plan = matmul_plan(m, n, p.groups);
-  const long long tiles = static_cast<long long>((m + plan.tokens - 1) / plan.tokens) *
-                          ((n + kScaleGroup - 1) / kScaleGroup) * plan.splits;
-  if (tiles >= (1ll << 31)) return KVP_ERR_UNSUPPORTED;
   CUtensorMap ta, tb;
-  kvp_status st = make_codes_map(&ta, a, a_stride, m, k, plan.box());
+  st = make_codes_map(&ta, a, a_stride, m, k, plan.box());
   if (st == KVP_OK) st = make_codes_map(&tb, b, b_stride, n, k, plan.box_b());
   if (st != KVP_OK) return st;
   return from_cuda(launch_matmul_fp8(p, plan, ta, tb, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvp_status kvp_matmul_fp8_plan(int32_t m, int32_t n, int32_t k, int32_t* tokens, int32_t* splits) {
+  if (m == 0 || tokens == nullptr || splits == nullptr) return KVP_ERR_INVALID_ARG;
+  MatmulPlan plan;
+  const kvp_status st = cut_matmul(m, n, k, &plan);
+  if (st != KVP_OK) return st;
+  *tokens = plan.tokens;
+  *splits = plan.splits;
+  return KVP_OK;
 }
 
 kvp_status kvp_selftest_wait_timeout(int32_t* dev_status, int64_t limit_ns,

@@ -47,3 +47,22 @@ def test_every_size_has_a_plan(plans):
 
 def test_many_rows_go_to_pairs(plans):
     assert all(tokens == 256 for m, n, _, tokens, _ in plans if m >= 33098 and n >= 33098)
+
+
+def test_the_entry_point(plans):
+    import pagedattention_decode_kvp_gb300 as kvp
+    from pagedattention_decode_kvp_gb300 import _build
+    _build.build()
+    for m, n, groups, tokens, splits in plans:
+        if n > 2 ** 31 - 256 or m * n > 2 ** 40:
+            continue                     # (too many tiles are refused below)
+        for k in (128 * groups - 112, 128 * groups):
+            if k <= 2 ** 31 - 128:
+                assert kvp.kvp_matmul_fp8_plan(m, n, k) == (tokens, splits)
+    for bad in ((0, 5, 16), (-1, 5, 16), (5, 0, 16), (5, 5, 0), (5, 5, 24), (2 ** 31 - 1, 5, 16),
+                (5, 2 ** 31 - 1, 16), (5, 5, 2 ** 31 - 16), (2 ** 31 - 300, 2 ** 31 - 300, 16),
+                (2 ** 32 + 5, 5, 16), (5, 2 ** 32 + 5, 16), (5, 5, 2 ** 32 + 16)):
+        with pytest.raises(kvp.KvpError):
+            kvp.kvp_matmul_fp8_plan(*bad)
+    lib = kvp.load_library()
+    assert lib.kvp_matmul_fp8_plan(5, 5, 16, None, None) == kvp.KVP_ERR_INVALID_ARG
