@@ -29,7 +29,8 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
 
 // dev::mbar_wait_bounded without a call: a called function's registers do not go with
 // setmaxnreg.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity,
+                                     uint64_t limit_ns = dev::kWaitTimeoutNs) {
   // (reading the timer takes longer than most waits last)
 #pragma unroll 1
   for (int i = 0; i < 64; ++i) {
@@ -39,7 +40,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
   for (uint32_t i = 0; i < (1u << 26); ++i) {
     if (dev::mbar_try_wait_sleep(bar, parity, dev::kWaitHintNs)) return true;
-    if ((i & 15u) == 15u && dev::global_timer_ns() - t0 > dev::kWaitTimeoutNs) break;
+    if ((i & 15u) == 15u && dev::global_timer_ns() - t0 > limit_ns) break;
   }
   return false;
 }

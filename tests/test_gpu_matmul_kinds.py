@@ -240,3 +240,17 @@ def test_captured_cuts_on_two_streams():
     for _, _, outs in sides:
         for o, v in zip(outs, want):
             assert torch.equal(bits(o), bits(v))
+
+
+def test_a_status_word_keeps_its_first_error():
+    """A product that goes well writes nothing; after a wait that gave up (the products' own is
+    one of the self-test's, all of which have to) the word says so, whatever runs behind it."""
+    clean, timeout = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    kvp.kvp_selftest_wait_timeout(timeout, 5_000_000)
+    for i, s in enumerate(EACH):
+        args = operands(*sizes(s), seed=i)
+        out = torch.empty(s[1:3], dtype=BF16, device="cuda")
+        kvp.kvp_matmul_fp8(out, *args, status=clean)
+        kvp.kvp_matmul_fp8(out, *args, status=timeout)
+    assert kvp.kvp_read_status(clean) == kvp.KVP_OK
+    assert kvp.kvp_read_status(timeout) == kvp.KVP_ERR_TIMEOUT
