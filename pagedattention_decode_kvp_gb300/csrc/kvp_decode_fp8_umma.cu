@@ -107,15 +107,6 @@ __device__ __forceinline__ void st8(uint32_t taddr, const float (&v)[8]) {
       : "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem] over E4M3 codes; issued by one thread.
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                       uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
-
 // log2 on the special-function unit (the lg2.approx PTX instruction).
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
@@ -304,8 +295,8 @@ __global__ void __launch_bounds__(kThreadsU, 2)
         for (int t = 0; t < kTerms; ++t)
 #pragma unroll
           for (int s = 0; s < kD / 32; ++s)
-            mma_f8(tmem + kSCol + sb * kN, kd + ((s * 32) >> 4),
-                   q_desc + ((t * 2048 + s * 32) >> 4), kIdS, (t | s) ? 1u : 0u);
+            umma::mma_f8(tmem + kSCol + sb * kN, kd + ((s * 32) >> 4),
+                         q_desc + ((t * 2048 + s * 32) >> 4), kIdS, (t | s) ? 1u : 0u);
         umma::commit(smem_addr(sfull + sb));
       }
       __syncwarp();
@@ -324,8 +315,8 @@ __global__ void __launch_bounds__(kThreadsU, 2)
         for (int t = 0; t < kTerms; ++t)
 #pragma unroll
           for (int s = 0; s < kChunk / 32; ++s)
-            mma_f8(tmem + kOCol + t * kN, vd + ((s * 32 * 128) >> 4),
-                   pd + ((t * 2048 + s * 32) >> 4), kIdO, (k | s) ? 1u : 0u);
+            umma::mma_f8(tmem + kOCol + t * kN, vd + ((s * 32 * 128) >> 4),
+                         pd + ((t * 2048 + s * 32) >> 4), kIdO, (k | s) ? 1u : 0u);
         umma::commit(smem_addr(pvdone + st));
       }
       __syncwarp();

@@ -1,31 +1,12 @@
-// kvp_matmul.cuh -- what the block-scaled matrix products share: kind::f8f6f4
-// instructions, clusters, and the store of a result.
+// kvp_matmul.cuh -- what the block-scaled matrix products share: waits, rings, clusters,
+// and the store of a result.
 #pragma once
 
 #include "kvp_device.cuh"
 #include "kvp_project.h"
-#include "kvp_umma.cuh"
 
 namespace kvp {
 namespace mm {
-
-// D[tmem] (+)= A[smem] * B[smem] over E4M3 codes; issued by one thread.  kGroup = 2: by
-// the first CTA of a pair, whose halves of A, B and D lie at the same addresses.
-template <int kGroup>
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                       uint32_t idesc, uint32_t accumulate) {
-  if constexpr (kGroup == 1) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-  }
-}
 
 // dev::mbar_wait_bounded without a call: a called function's registers do not go with
 // setmaxnreg.

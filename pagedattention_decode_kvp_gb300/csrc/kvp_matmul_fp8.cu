@@ -23,6 +23,7 @@
 // 10240 x 8192 16.0 (12.6), 64 x 10240 x 8192 18.8 (12.8), 64 x 4096 x 4096 8.0 (2.6), 33 x
 // 32000 x 4096 with 32-bit results 24.4 (20.3), 128 x 10240 x 8192 26.7 (13.1).
 #include "kvp_matmul.cuh"
+#include "kvp_umma.cuh"
 
 namespace kvp {
 
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(Shape<kTokens>::kThreads, Shape<kTokens>::kCta
           const uint64_t a = umma::smem_desc_sw128(at + kTileB, 16, 1024);
 #pragma unroll
           for (int s = 0; s < 4; ++s)
-            mm::mma_f8<1>(tmem + (buffer.at * S::kBatch + in + q) * kTokens, b + 2 * s, a + 2 * s,
-                          kInstr, s > 0);
+            umma::mma_f8(tmem + (buffer.at * S::kBatch + in + q) * kTokens, b + 2 * s, a + 2 * s,
+                         kInstr, s > 0);
           umma::commit(smem_addr(empty + st));
         }
         if (last) umma::commit(smem_addr(sums + buffer.at));

@@ -20,6 +20,7 @@
 // buffers each (430), tiles of 192 columns (506: a group takes as long), the issuing warp's
 // loop by one lane (411), a look at the next buffer before the last sums (407).
 #include "kvp_matmul.cuh"
+#include "kvp_umma.cuh"
 
 namespace kvp {
 
@@ -199,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok && elect_one()) {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              mm::mma_f8<2>(tmem + buf * kTile, a + 2 * s, b + 2 * s, kInstr, s > 0);
+              umma::mma_f8<2>(tmem + buf * kTile, a + 2 * s, b + 2 * s, kInstr, s > 0);
             commit_pair(sums + 8 * buf);
             commit_pair(empty + 8 * st);
           }
