@@ -1233,7 +1233,7 @@ kvp_status kvp_matmul_fp8(void* out, int64_t out_stride, kvp_dtype out_dtype, co
   p.out_type = out_dtype;
   CUtensorMap ta, tb;
   st = make_codes_map(&ta, a, a_stride, m, k, plan.box());
-  if (st == KVP_OK) st = make_codes_map(&tb, b, b_stride, n, k, plan.box_b());
+  if (st == KVP_OK) st = make_codes_map(&tb, b, b_stride, n, k, kScaleGroup);
   if (st != KVP_OK) return st;
   return from_cuda(launch_matmul_fp8(p, plan, ta, tb, reinterpret_cast<cudaStream_t>(stream)));
 }

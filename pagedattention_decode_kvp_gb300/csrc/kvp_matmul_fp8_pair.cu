@@ -174,7 +174,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(full + 8 * st, 2 * kStage);
             load_pair(at, &ta, k * 128, m0, bar);
             load_pair(at + kHalf, &tb, k * 128, n0, bar);
-            load_pair(at + kHalf + kHalf / 2, &tb, k * 128, n0 + 64, bar);
           }
           __syncwarp();
         }

@@ -11,8 +11,7 @@ constexpr int kMaxSplits = 8;     // CTAs of a portable cluster
 struct MatmulPlan {
   int tokens;                     // rows of a per tile (256: pairs of CTAs)
   int splits;                     // CTAs that share a tile's K
-  int box() const { return tokens < 128 ? tokens : 128; }   // rows of a per copy
-  int box_b() const { return tokens == 256 ? 64 : 128; }    // rows of b
+  int box() const { return tokens < 128 ? tokens : 128; }   // rows of a per copy (of b 128)
 };
 
 // The plan with the least time by a model of what was measured, in us: 2.6 for the start of a

@@ -45,8 +45,7 @@ struct MatmulParams {
 
 cudaError_t launch_rms_norm(const NormParams& p, bool bf16, cudaStream_t s);
 cudaError_t launch_quantise_fp8(const QuantiseParams& p, bool bf16, cudaStream_t s);
-// ta, tb: K-major maps of a and b with boxes of 128 bytes x plan.box() (a) and plan.box_b()
-// (b) rows.
+// ta, tb: K-major maps of a and b with boxes of 128 bytes x plan.box() (a) and 128 rows (b).
 cudaError_t launch_matmul_fp8(const MatmulParams& p, const MatmulPlan& plan, const CUtensorMap& ta,
                               const CUtensorMap& tb, cudaStream_t s);
 cudaError_t launch_matmul_fp8_pair(const MatmulParams& p, const CUtensorMap& ta,
