@@ -509,8 +509,8 @@ kvp_status kvp_release_tables(const int32_t* block_tables, int32_t max_blocks_pe
  * elements of a token.  eps: finite, not negative (with 0, a row of zeros gives NaN).
  * residual and residual_out: both or neither (NULL), with one head only.  out may be
  * x (same stride); residual_out may be residual or x (same stride); otherwise outputs
- * must not overlap an input or each other.  All rows 16-byte aligned, strides
- * multiples of 8.  Squares are summed in float32, of rows for which that is too small a
+ * must not overlap an input or each other.  Rows and the weight are 16-byte aligned,
+ * strides multiples of 8.  Squares are summed in float32, of rows for which that is too small a
  * range (bf16 elements from some 2^56 on, or below 2^-40 with an eps below 2^-100) scaled by
  * a power of two: any finite row has its norm.
  */

@@ -14,14 +14,14 @@
 // hand-over takes about 1000 cycles (two barriers, the read), more than the bytes of a
 // group.  TMEM is read in pieces of 16 rows, whose lanes hold two columns in eight: with a
 // row to a lane every lane needs every token's scale, and those broadcasts took as many
-// cycles of shared memory as the operands (64 x 10240 x 8192 21.0 us, now 18.9).  Where few
+// cycles of shared memory as the operands (64 x 10240 x 8192 2.1 us more).  Where few
 // tiles meet many SMs, the CTAs of a cluster share a tile's K and add their sums through
 // distributed shared memory, in the order of their ranks.  (kvp_matmul_fp8_pair.cu: many
 // rows.)
 //
-// Measured (us; at HBM's measured rate the bytes alone take): 1 x 768 x 512 2.8 (0.1), 1 x
-// 10240 x 8192 16.0 (12.6), 64 x 10240 x 8192 18.8 (12.8), 64 x 4096 x 4096 8.0 (2.6), 33 x
-// 32000 x 4096 with 32-bit results 24.4 (20.3), 128 x 10240 x 8192 26.7 (13.1).
+// Measured (us, calls back to back; at HBM's measured rate the bytes alone take): 1 x 768 x
+// 512 2.9 (0.1), 1 x 10240 x 8192 16.7 (12.6), 64 x 10240 x 8192 19.4 (12.9), 64 x 4096 x 4096
+// 7.5 (2.6), 33 x 32000 x 4096 with 32-bit results 24.7 (20.4), 128 x 10240 x 8192 27.7 (13.1).
 #include "kvp_matmul.cuh"
 #include "kvp_umma.cuh"
 

@@ -9,12 +9,15 @@
 // cores form the next group's.  Persistent: a pair walks the tiles; the warps that fetch
 // tiles and scales run on into the next one.
 //
-// Measured: 8192 x 8192 x 8192 395 us, 2780 TFLOP/s; 33098 x 12288 x 4096 1310 us, 2540;
-// 8191 x 10240 x 8192 500 us, 2750.  The products alone take 240 us of the first (4600
+// Measured, calls back to back: 8192 x 8192 x 8192 435 us, 2530 TFLOP/s; 33098 x 12288 x 4096
+// 1350 us, 2470; 8191 x 10240 x 8192 535 us, 2570; few groups a tile, 8191 x 10240 x 512, 74 us
+// (its bytes take 27): a tile's results are written by the warps that add, 4.4 us a tile of
+// which the four groups take 1.8.  These calls are held by the board's power (run for seconds
+// 1350 W, SM clock 1640 MHz, 2300 TFLOP/s); before the clock falls, in a run of a few
+// milliseconds, the first takes 395 to 420 us.  Of 395 the products alone take 240 (4600
 // TFLOP/s), with the fetches 283; the rest is the way round of a TMEM buffer (product,
 // commit, read, arrivals from both CTAs: 900 cycles a group where the product takes 512).
-// Run for seconds it is held by the board's power (1350 W, SM clock 1640 MHz, 2300
-// TFLOP/s).  Tried, on the first shape: 16 adding warps of 64 columns (their 104 registers
+// Two words a thread are spilled (ptxas: 8 bytes).  Tried, on the first shape in such runs: 16 adding warps of 64 columns (their 104 registers
 // cost moves and spills: 502 us), 16 columns a read (449), the next group's first read
 // ahead of this one's last sums (501), halves of 128 columns with a warp, barriers and
 // buffers each (430), tiles of 192 columns (506: a group takes as long), the issuing warp's

@@ -27,7 +27,11 @@ inline MatmulPlan matmul_plan(int m, int n, int groups) {
     double alone, shared;      // us a group
   };
   // clusters of 1 .. 8 CTAs that the GPU holds at a time, by the CTAs of an SM (its GPCs
-  // have no multiple of most sizes: 48 clusters of 3, one CTA to an SM, take two waves)
+  // have no multiple of most sizes: 48 clusters of 3, one CTA to an SM, take two waves).  A
+  // table, so that a product has the same cut, and bits, on every board: four of them had the
+  // first row's numbers, one on which clusters were counted the second's
+  // (cudaOccupancyMaxActiveClusters gives the first row for both).  Where SMs lie otherwise, a
+  // split may take a second wave: slower, not wrong.
   constexpr int kFit[2][kMaxSplits] = {{152, 76, 46, 36, 28, 23, 15, 15},
                                        {304, 152, 97, 74, 58, 46, 38, 36}};
   constexpr Kind kKinds[] = {{16, 2, 0.24, 0.28}, {32, 2, 0.30, 0.34}, {64, 2, 0.35, 0.58},

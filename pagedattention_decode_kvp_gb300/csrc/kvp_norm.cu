@@ -12,12 +12,13 @@
 //
 // A lane holds whole 16-byte chunks of 8 elements, a row's chunks lie on consecutive
 // lanes, so that 16 lanes hold a group.  Bound by HBM for prompts and by one launch for a
-// step.  Measured (shares of the measured copy bandwidth): norm in codes with a residual,
-// 33098 rows of 4096, 138 us (1.03); norm of 8191 x 64 heads of 128, 44 us (0.91, held by
-// its instructions: 80 % of the issue slots; one row a slot 67 us, four 47, a factor
-// worked out once a row 44); 8191 rows of 8192 in codes 31 us (0.97; 8 elements a lane and
-// float maxima 63); a weight of 10240 x 8192 in codes 39 us (0.96; float maxima 48); a step
-// of 64 tokens of 8192 2.6 us, in codes 2.9.
+// step.  Measured (calls back to back; shares of the measured copy bandwidth): norm in codes
+// with a residual, 33098 rows of 4096, 138 us (1.03); norm with a residual, 8191 rows of 8192,
+// 78 us (1.03); norm of 8191 x 64 heads of 128, 45 us (0.90, held by its instructions: 77 % of
+// the issue slots; one row a slot 67 us, four 47, a factor worked out once a row 44, a look
+// whether a row is out of range 0.6 more); 8191 rows of 8192 in codes 31 us (0.97; 8 elements
+// a lane and float maxima 63); a weight of 10240 x 8192 in codes 39 us (0.96; float maxima
+// 48); a step of 64 tokens of 8192 2.5 us, in codes 2.7.
 #include "kvp_device.cuh"
 #include "kvp_project.h"
 
